@@ -13,6 +13,10 @@ Entry points (same names as the C ABI without the ``ets_`` prefix):
   page_table, output, page_size);
 * :func:`topk_ragged` -- packed ragged rows, packed-buffer positions.
 
+The operators around the selection in a sparse decode step (``rope``,
+``cache_write``, ``cache_read``, ``index_scores``, ``attend_selected``,
+``attend_paged``; C ABI in ``include/ets_decode.h``) are bound in ``_decode.py``.
+
 Each output row holds min(k, n) selected entries in unspecified order followed
 by -1 padding.  Scores are ranked by their order-preserving 32-bit key; among
 equal bit patterns the lowest positions win.
@@ -29,7 +33,8 @@ import torch
 __all__ = ["topk_raw", "topk_paged", "topk_ragged", "topk_paged_noalloc", "workspace_size", "row_split", "floor_read",
            "floor_launch", "device_limits", "group_cap", "ticket_cap",
            "new_workspace", "workspace_init", "workspace_error", "workspace_error_async",
-           "library_path", "MAX_K", "NOALLOC_SCRATCH_BYTES", "ERROR_BITS", "EtsError"]
+           "library_path", "MAX_K", "NOALLOC_SCRATCH_BYTES", "ERROR_BITS", "EtsError",
+           "rope", "cache_write", "cache_read", "index_scores", "attend_selected", "attend_paged"]
 
 MAX_K = 2048
 NOALLOC_SCRATCH_BYTES = 4 << 20  # ETS_NOALLOC_SCRATCH_BYTES: topk_paged_noalloc's static scratch
@@ -491,3 +496,6 @@ def floor_launch(B: int, max_row_len: int, device: Optional[torch.device] = None
     with torch.cuda.device(dev):
         st = _load().ets_floor_launch(B, max_row_len, _stream(dev))
     _check(st, "ets_floor_launch")
+
+
+from ._decode import attend_paged, attend_selected, cache_read, cache_write, index_scores, rope  # noqa: E402

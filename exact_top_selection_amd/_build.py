@@ -2,11 +2,14 @@
 from __future__ import annotations
 
 import os
+import shutil
 import subprocess
+import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-SRC = os.path.join(PKG, "csrc", "ets_topk.hip")
+SOURCES = [os.path.join(PKG, "csrc", name) for name in
+           ("ets_topk.hip", "ets_rope_cache.hip", "ets_scores.hip", "ets_attend.hip")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libets_topk.so")
 
@@ -31,15 +34,33 @@ def hipcc() -> str:
 
 
 def build(verbose: bool = False) -> str:
-    """Compile the library (always) and return its path."""
-    tmp = LIB + ".tmp%d" % os.getpid()
-    cmd = [hipcc(), *HIPCC_FLAGS, "-I", INCLUDE, SRC, "-o", tmp]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError("hipcc failed:\n" + res.stdout + res.stderr)
-    os.replace(tmp, LIB)
+    """Compile the library (always, the sources side by side) and return its path."""
+    work = tempfile.mkdtemp(prefix="ets_build_")
+    try:
+        running = []
+        for src in SOURCES:
+            obj = os.path.join(work, os.path.basename(src) + ".o")
+            cmd = [hipcc(), *(f for f in HIPCC_FLAGS if f != "-shared"), "-c", "-I", INCLUDE, src, "-o", obj]
+            if verbose:
+                print(" ".join(cmd), flush=True)
+            log = open(obj + ".log", "w+")
+            running.append((obj, log, subprocess.Popen(cmd, stdout=log, stderr=subprocess.STDOUT)))
+        failed = ""
+        for obj, log, child in running:
+            if child.wait() != 0:
+                log.seek(0)
+                failed += log.read()
+            log.close()
+        if failed:
+            raise RuntimeError("hipcc failed:\n" + failed)
+        tmp = LIB + ".tmp%d" % os.getpid()
+        cmd = [hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", *(obj for obj, _, _ in running), "-o", tmp]
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError("hipcc failed:\n" + res.stdout + res.stderr)
+        os.replace(tmp, LIB)
+    finally:
+        shutil.rmtree(work, ignore_errors=True)
     return LIB
 
 

@@ -1,0 +1,174 @@
+// Device helpers shared by the kernels around the selection: vector types,
+// the 8-bit cache format and cross-lane sums (gfx950, wave64).
+#ifndef ETS_CACHE_FORMAT_H
+#define ETS_CACHE_FORMAT_H
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "ets_decode.h"
+
+namespace ets {
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32v2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32v4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kCacheBlock = 32;    // values that share a scale byte
+constexpr int kScaleBias = 127;    // value = code * 2^(byte - 127)
+constexpr int kScaleLow = -126, kScaleHigh = 119;
+
+// Loads and stores of V at any address (one instruction whatever the alignment).
+template <class V>
+__device__ __forceinline__ V load_any(const void* p) {
+  V v;
+  __builtin_memcpy(&v, p, sizeof(V));
+  return v;
+}
+template <class V>
+__device__ __forceinline__ void store_any(void* p, const V& v) {
+  __builtin_memcpy(p, &v, sizeof(V));
+}
+
+// n / d for 0 <= n < 2^31 and a divisor d >= 1 fixed at launch: with l =
+// ceil(log2 d) and m = ceil(2^(31 + l) / d), n * m / 2^(31 + l) exceeds n / d
+// by less than n / 2^(31 + l) <= 1 / d, so the floor is exact.  d lies in
+// (2^(l - 1), 2^l], so m lies in [2^31, 2^32).
+struct FastDiv {
+  uint32_t m, shift, d;
+};
+inline FastDiv fast_div(uint32_t d) {
+  uint32_t l = 0;
+  while ((1ull << l) < d) ++l;
+  const uint32_t shift = 31 + l;
+  const uint64_t q = (static_cast<uint64_t>(1) << shift) / d, r = (static_cast<uint64_t>(1) << shift) % d;
+  return {static_cast<uint32_t>(q + (r ? 1 : 0)), shift, d};
+}
+__device__ __forceinline__ uint32_t div_by(uint32_t n, const FastDiv& f) {
+  return static_cast<uint32_t>((static_cast<uint64_t>(n) * f.m) >> f.shift);
+}
+
+// Sum, largest over the lanes l, l ^ 16, l ^ 32, l ^ 48: the swaps exchange
+// whole 16-lane rows, without LDS.
+__device__ __forceinline__ float rows_sum(float x) {
+  const uint32_t b = __float_as_uint(x);
+  const auto s = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  const float y = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+  const uint32_t c = __float_as_uint(y);
+  const auto t = __builtin_amdgcn_permlane16_swap(c, c, false, false);
+  return __uint_as_float(t[0]) + __uint_as_float(t[1]);
+}
+__device__ __forceinline__ float rows_max(float x) {
+  const uint32_t b = __float_as_uint(x);
+  const auto s = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  const float y = fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1]));
+  const uint32_t c = __float_as_uint(y);
+  const auto t = __builtin_amdgcn_permlane16_swap(c, c, false, false);
+  return fmaxf(__uint_as_float(t[0]), __uint_as_float(t[1]));
+}
+
+// Scale bytes of one cached row, four a word; bytes past nb are left 0.
+template <int WORDS>
+__device__ __forceinline__ void load_scales(uint32_t (&sc)[WORDS], const uint8_t* row, int nb) {
+#pragma unroll
+  for (int i = 0; i < WORDS; ++i) {
+    if (4 * i + 4 <= nb) {
+      sc[i] = load_any<uint32_t>(row + 4 * i);
+    } else {
+      uint32_t w = 0;
+      if (4 * i < nb) w = row[4 * i];
+      if (4 * i + 1 < nb) w |= static_cast<uint32_t>(row[4 * i + 1]) << 8;
+      if (4 * i + 2 < nb) w |= static_cast<uint32_t>(row[4 * i + 2]) << 16;
+      sc[i] = w;
+    }
+  }
+}
+
+// Largest scale byte of a row.
+template <int WORDS>
+__device__ __forceinline__ uint32_t scales_max(const uint32_t (&sc)[WORDS]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < WORDS; ++i) {
+    m = max(m, sc[i] & 255u);
+    m = max(m, (sc[i] >> 8) & 255u);
+    m = max(m, (sc[i] >> 16) & 255u);
+    m = max(m, sc[i] >> 24);
+  }
+  return m;
+}
+
+// Eight codes (two words) to eight values times `scale`, a power of two.
+// bf16 holds every value of the format exactly (4 significant bits; results
+// below 2^-133 round).
+__device__ __forceinline__ bf16x8 codes_bf16(uint32_t lo, uint32_t hi, float scale) {
+  const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false);
+  const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true);
+  const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false);
+  const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true);
+  return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+__device__ __forceinline__ f16x8 codes_f16(uint32_t lo, uint32_t hi, float scale) {
+  const f16x2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, scale, false);
+  const f16x2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, scale, true);
+  const f16x2 c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, scale, false);
+  const f16x2 d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, scale, true);
+  return f16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// The matrix operand types of a query type.  A key is brought to the query's
+// own type, so that products are exact in 32 bits:
+//   bf16  the key's values;
+//   fp16  the key's values over 2^(r - 127), r the row's largest scale byte:
+//         at most 448, and a block 2^15 and more below the row's largest
+//         loses bits only beneath 2^-33 of it.  The product is multiplied by
+//         2^(r - 127) afterwards.
+template <class T>
+struct Mat;
+template <>
+struct Mat<__bf16> {
+  typedef bf16x8 V8;
+  static constexpr bool kRowScale = false;
+  static __device__ __forceinline__ float scale(uint32_t byte, uint32_t) { return __uint_as_float(byte << 23); }
+  static __device__ __forceinline__ V8 keys(uint32_t lo, uint32_t hi, float s) { return codes_bf16(lo, hi, s); }
+  static __device__ __forceinline__ f32x4 mma(V8 a, V8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+  }
+};
+template <>
+struct Mat<_Float16> {
+  typedef f16x8 V8;
+  static constexpr bool kRowScale = true;
+  static __device__ __forceinline__ float scale(uint32_t byte, uint32_t top) {
+    const int e = static_cast<int>(byte) - static_cast<int>(top) + kScaleBias;
+    return __uint_as_float(static_cast<uint32_t>(e < 0 ? 0 : e) << 23);
+  }
+  static __device__ __forceinline__ V8 keys(uint32_t lo, uint32_t hi, float s) { return codes_f16(lo, hi, s); }
+  static __device__ __forceinline__ f32x4 mma(V8 a, V8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+  }
+};
+
+// Byte `i` (0 to 3, per lane) of a word.
+__device__ __forceinline__ uint32_t byte_of(uint32_t w, uint32_t shift) {
+  return __builtin_amdgcn_ubfe(w, shift, 8);
+}
+
+inline bool dtype_known(int32_t dtype) { return dtype == ETS_BF16 || dtype == ETS_FP16 || dtype == ETS_FP32; }
+
+// ETS_OK where the current device is a gfx950; the device's compute units.
+inline ets_status device_ready(int32_t* cu_count) {
+  int32_t xcd = 0, occ = 0;
+  return ets_device_limits(-1, cu_count, &xcd, &occ);
+}
+
+}  // namespace ets
+
+#endif  // ETS_CACHE_FORMAT_H
