@@ -9,7 +9,7 @@ import tempfile
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SOURCES = [os.path.join(PKG, "csrc", name) for name in
-           ("ets_topk.hip", "ets_rope_cache.hip", "ets_scores.hip", "ets_attend.hip")]
+           ("ets_topk.hip", "ets_rope_cache.hip", "ets_scores.hip", "ets_attend.hip", "ets_attend_wide.hip")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libets_topk.so")
 

@@ -1,0 +1,102 @@
+// What the attention kernels share: the launch's parameters and the finding of
+// a list's keys (gfx950).
+#ifndef ETS_ATTEND_H
+#define ETS_ATTEND_H
+
+#include "ets_cache_format.h"
+
+namespace ets {
+
+constexpr int kAttendThreads = 256;
+constexpr int kAttendWaves = 4;
+constexpr int kAttendTile = 32;  // keys of a step
+constexpr float kNegInf = -__builtin_inff();
+constexpr float kLn2 = 0.69314718055994530942f;
+
+struct AttendParams {
+  ets_attend_args a;
+  int G;             // query heads of a cache head
+  int rows;          // query rows that share a list of keys: G, or T * G where all tokens share it
+  int units;         // lists: (b, t, hk) or (b, hk)
+  int row_groups;    // of a unit
+  int splits;        // workgroups that share a list
+  int tree_tiles;
+  float scale_log2;  // log2(e) / sqrt(D)
+  FastDiv by_page, by_heads, by_tokens, by_groups, by_splits, by_G, by_rows;
+  int group_rows;    // query rows of a workgroup, a multiple of 16
+  float* part;       // [unit][row group][split][group_rows][Dv] sums
+  f32x2* stat;       // [unit][row group][split][group_rows] (reference, sum)
+};
+
+// Where a workgroup stands: its list, its query rows, its share of the keys.
+// Blocks are numbered split fastest, then row group, then unit.
+struct AttendSpot {
+  int split, row0, hk, b, t;  // t: the token of a selected list, 0 for paged ones
+  bool paged;
+  int n, main_tiles, tiles, first, last;
+};
+__device__ __forceinline__ AttendSpot attend_spot(const AttendParams& p) {
+  const ets_attend_args& a = p.a;
+  AttendSpot s;
+  const uint32_t ug = div_by(blockIdx.x, p.by_splits);
+  s.split = static_cast<int>(blockIdx.x - ug * p.splits);
+  const uint32_t unit = div_by(ug, p.by_groups);
+  s.row0 = static_cast<int>(ug - unit * p.row_groups) * p.group_rows;
+  s.paged = a.slots == nullptr;
+  const uint32_t bt = div_by(unit, p.by_heads);
+  s.hk = static_cast<int>(unit - bt * a.Hkv);
+  s.b = s.paged ? static_cast<int>(bt) : static_cast<int>(div_by(bt, p.by_tokens));
+  s.t = s.paged ? 0 : static_cast<int>(bt) - s.b * a.T;
+  s.n = s.paged ? min(max(a.seq_lens[s.b], 0), a.L) : a.K;
+  s.main_tiles = (s.n + kAttendTile - 1) / kAttendTile;
+  s.tiles = s.main_tiles + p.tree_tiles;
+  const int per = (s.tiles + p.splits - 1) / p.splits;
+  s.first = s.split * per;
+  s.last = min(s.first + per, s.tiles);
+  return s;
+}
+
+// Slot of key `at` (0 to 31) of tile i; -1 where there is none.  The tree's
+// tiles stand behind the main ones.  One token's list leaves out the drafted
+// tokens that it does not see, so nothing of them is read.
+__device__ __forceinline__ int32_t attend_slot(const AttendParams& p, const AttendSpot& s, int i, int at) {
+  const ets_attend_args& a = p.a;
+  int64_t slot = -1;
+  if (i < s.main_tiles) {
+    const int j = i * kAttendTile + at;
+    if (j < s.n) {
+      if (s.paged) {
+        const uint32_t page = div_by(j, p.by_page);
+        slot = static_cast<int64_t>(a.page_table[s.b * a.pt_b + page]) * a.page_size + (j - page * p.by_page.d);
+      } else {
+        slot = a.slots[s.b * a.slots_b + s.t * a.slots_t + j];
+      }
+    }
+  } else {
+    const int j = (i - s.main_tiles) * kAttendTile + at;
+    if (i < s.tiles && j < a.T && (s.paged || (a.tree_mask[s.b * a.mask_b + s.t] >> j & 1)))
+      slot = a.tree_slots[s.b * a.tree_b + j];
+  }
+  return slot >= 0 && slot < a.S ? static_cast<int32_t>(slot) : -1;
+}
+
+// (token, query head) of a workgroup's row r.
+__device__ __forceinline__ void attend_row(const AttendParams& p, const AttendSpot& s, int r, int* t, int* h) {
+  *t = s.paged ? static_cast<int>(div_by(r, p.by_G)) : s.t;
+  *h = s.hk * p.G + (s.paged ? r - *t * p.G : r);
+}
+
+__device__ __forceinline__ float attend_lse(float reference, float sum) {
+  return sum == 0.0f ? kNegInf : (reference + __builtin_amdgcn_logf(sum)) * kLn2;
+}
+__device__ __forceinline__ float attend_inverse(float sum) {
+  return sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+}
+
+// Bytes of LDS, and the launch, of the kernel for heads over 256 channels
+// (ets_attend_wide.hip); row_tiles: 4 or 8 tiles of 16 query rows.
+void launch_attend_wide(const AttendParams& p, int row_tiles, bool shared, hipStream_t s);
+
+}  // namespace ets
+
+#endif  // ETS_ATTEND_H

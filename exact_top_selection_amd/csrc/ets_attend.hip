@@ -1,30 +1,14 @@
 // ets_attend.hip -- attention of one or a few tokens a sequence over an 8-bit
 // cache: over selected slots or over whole paged sequences, plus a tree of
 // drafted tokens (gfx950).
-#include "ets_cache_format.h"
+#include "ets_attend.h"
 
 namespace ets {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWaves = 4;
-constexpr int kTile = 32;  // keys of a wave's step
-constexpr float kNegInf = -__builtin_inff();
-constexpr float kLn2 = 0.69314718055994530942f;
-
-struct AttendParams {
-  ets_attend_args a;
-  int G;             // query heads of a cache head
-  int rows;          // query rows that share a list of keys: G, or T * G where all tokens share it
-  int units;         // lists: (b, t, hk) or (b, hk)
-  int row_groups;    // of a unit
-  int splits;        // workgroups that share a list
-  int tree_tiles;
-  float scale_log2;  // log2(e) / sqrt(D)
-  FastDiv by_page, by_heads, by_tokens, by_groups, by_splits, by_G;
-  float* part;       // [unit][row group][split][16 * MT][Dv] sums
-  f32x2* stat;       // [unit][row group][split][16 * MT] (largest, sum)
-};
+constexpr int kThreads = kAttendThreads;
+constexpr int kWaves = kAttendWaves;
+constexpr int kTile = kAttendTile;
 
 // One wave goes over its tiles of 32 keys alone, with the running largest
 // score and sum of the softmax, and the four waves of a workgroup join at the
@@ -41,19 +25,17 @@ struct AttendParams {
 // Keys go from global memory straight into operands (16 consecutive codes a
 // lane and 64 channels).  Values are brought to bf16, which holds them
 // exactly, stored row by row in the wave's part of LDS, and read back
-// transposed (ds_read_b64_tr_b16).  With SHARED the values are the keys' first
-// Dv channels and are loaded once for both.
+// transposed (ds_read_b64_tr_b16).
 //
 // fp16 queries keep their probabilities as the sum of two bf16 numbers (16
 // bits), bf16 queries as one (8 bits: each is off by at most 2^-8 of itself,
 // the errors of different keys are independent, and the result is rounded to
 // 8 bits anyway).
-template <class T, int NP, int NV, bool SHARED, int MT>
+template <class T, int NP, int NV, int MT>
 __global__ __launch_bounds__(kThreads) void attend_kernel(AttendParams p) {
   typedef Mat<T> M;
   typedef typename M::V8 V8;
   constexpr int W = (NP + 1) / 2, WV = (NV + 1) / 2;
-  constexpr int NVR = SHARED ? 1 : NV, WVR = SHARED ? 1 : WV;
   constexpr int kPitch = NV * 128 + 32;  // bytes of a row of values in LDS
   constexpr bool kTwo = M::kRowScale;    // fp16: two-part probabilities
   extern __shared__ __align__(16) char lds[];
@@ -63,21 +45,8 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(AttendParams p) {
   char* values = lds + wave * (kTile * kPitch);
   f32x2* stats = reinterpret_cast<f32x2*>(lds + kWaves * kTile * kPitch);  // [wave][16 MT]
 
-  // blocks: split fastest, then row group, then unit
-  const uint32_t ug = div_by(blockIdx.x, p.by_splits);
-  const int split = static_cast<int>(blockIdx.x - ug * p.splits);
-  const uint32_t unit = div_by(ug, p.by_groups);
-  const int row0 = static_cast<int>(ug - unit * p.row_groups) * (16 * MT);
-  const bool paged = a.slots == nullptr;
-  const uint32_t bt = div_by(unit, p.by_heads);
-  const int hk = static_cast<int>(unit - bt * a.Hkv);
-  const int b = paged ? static_cast<int>(bt) : static_cast<int>(div_by(bt, p.by_tokens));
-  const int t_unit = paged ? 0 : static_cast<int>(bt) - b * a.T;
-
-  const int n = paged ? min(max(a.seq_lens[b], 0), a.L) : a.K;
-  const int main_tiles = (n + kTile - 1) / kTile, tiles = main_tiles + p.tree_tiles;
-  const int per = (tiles + p.splits - 1) / p.splits;
-  const int first = split * per, last = min(first + per, tiles);
+  const AttendSpot spot = attend_spot(p);
+  const int b = spot.b, hk = spot.hk, row0 = spot.row0, main_tiles = spot.main_tiles, last = spot.last;
 
   // queries: lane (head col, row g) holds channels 64 i + 16 g + 0..7, 8..15
   V8 q[MT][NP][2];
@@ -85,8 +54,8 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(AttendParams p) {
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     const int r = row0 + 16 * m + col;
-    const int t = paged ? static_cast<int>(div_by(r, p.by_G)) : t_unit;
-    const int h = hk * p.G + (paged ? r - t * p.G : r);
+    int t, h;
+    attend_row(p, spot, r, &t, &h);
     const char* src = static_cast<const char*>(a.q) + 2 * (b * a.q_b + t * a.q_t + h * a.q_h);
     tree_bits[m] = 0;
 #pragma unroll
@@ -106,35 +75,16 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(AttendParams p) {
     }
   }
 
-  // slot of the key that this lane loads: 16 s + col of tile i; -1 outside
-  auto slot_of = [&](int i, int s) -> int32_t {
-    int64_t slot = -1;
-    if (i < main_tiles) {
-      const int j = i * kTile + 16 * s + col;
-      if (j < n) {
-        if (paged) {
-          const uint32_t page = div_by(j, p.by_page);
-          slot = static_cast<int64_t>(a.page_table[b * a.pt_b + page]) * a.page_size + (j - page * p.by_page.d);
-        } else {
-          slot = a.slots[b * a.slots_b + t_unit * a.slots_t + j];
-        }
-      }
-    } else {
-      const int j = (i - main_tiles) * kTile + 16 * s + col;
-      // one token's list leaves out what the token does not see, so nothing of it is read
-      if (i < tiles && j < a.T && (paged || (a.tree_mask[b * a.mask_b + t_unit] >> j & 1)))
-        slot = a.tree_slots[b * a.tree_b + j];
-    }
-    return slot >= 0 && slot < a.S ? static_cast<int32_t>(slot) : -1;
-  };
+  // slot of the key that this lane loads: 16 s + col of tile i
+  auto slot_of = [&](int i, int s) { return attend_slot(p, spot, i, 16 * s + col); };
 
   const int nbk = a.D / kCacheBlock, nbv = a.Dv / kCacheBlock;
   const uint8_t* kc = a.k_codes + hk * a.k_h + 16 * g;
   const uint8_t* ks = a.k_scales + hk * a.ks_h;
   const uint8_t* vc = a.v_codes + hk * a.v_h + 16 * g;
   const uint8_t* vs = a.v_scales + hk * a.vs_h;
-  u32v4 kraw[2][NP], vraw[2][NVR];
-  uint32_t ksc[2][W], vsc[2][WVR];
+  u32v4 kraw[2][NP], vraw[2][NV];
+  uint32_t ksc[2][W], vsc[2][WV];
   uint32_t seen = 0;  // keys of the fetched tile that are inside the cache
   auto fetch = [&](const int32_t (&slot)[2]) {
     const uint64_t s0 = __ballot(slot[0] >= 0), s1 = __ballot(slot[1] >= 0);
@@ -146,21 +96,19 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(AttendParams p) {
 #pragma unroll
       for (int i = 0; i < W; ++i) ksc[s][i] = 0;
 #pragma unroll
-      for (int i = 0; i < NVR; ++i) vraw[s][i] = u32v4{0, 0, 0, 0};
+      for (int i = 0; i < NV; ++i) vraw[s][i] = u32v4{0, 0, 0, 0};
 #pragma unroll
-      for (int i = 0; i < WVR; ++i) vsc[s][i] = 0;
+      for (int i = 0; i < WV; ++i) vsc[s][i] = 0;
       if (slot[s] >= 0) {
         const int64_t at = slot[s];
 #pragma unroll
         for (int i = 0; i < NP; ++i)
           if (64 * i + 16 * g < a.D) kraw[s][i] = load_any<u32v4>(kc + at * a.k_s + 64 * i);
         load_scales<W>(ksc[s], ks + at * a.ks_s, nbk);
-        if constexpr (!SHARED) {
 #pragma unroll
-          for (int i = 0; i < NV; ++i)
-            if (64 * i + 16 * g < a.Dv) vraw[s][i] = load_any<u32v4>(vc + at * a.v_s + 64 * i);
-          load_scales<WV>(vsc[s], vs + at * a.vs_s, nbv);
-        }
+        for (int i = 0; i < NV; ++i)
+          if (64 * i + 16 * g < a.Dv) vraw[s][i] = load_any<u32v4>(vc + at * a.v_s + 64 * i);
+        load_scales<WV>(vsc[s], vs + at * a.vs_s, nbv);
       }
     }
   };
@@ -174,7 +122,7 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(AttendParams p) {
     for (int c = 0; c < 4 * NV; ++c) out[m][c] = f32x4{};
   }
 
-  int tile = first + wave;
+  int tile = spot.first + wave;
   int32_t slot[2] = {-1, -1};
   if (tile < last) {
     slot[0] = slot_of(tile, 0), slot[1] = slot_of(tile, 1);
@@ -204,27 +152,13 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(AttendParams p) {
           score[m][s] = M::mma(k0, q[m][i][0], score[m][s]);
           score[m][s] = M::mma(k1, q[m][i][1], score[m][s]);
         }
-        if constexpr (SHARED) {
-          if (i < NV) {
-            if constexpr (kTwo) {
-              const float fv = __uint_as_float(byte << 23);
-              store_any(__builtin_assume_aligned(dst + 128 * i, 16), codes_bf16(c[0], c[1], fv));
-              store_any(__builtin_assume_aligned(dst + 128 * i + 16, 16), codes_bf16(c[2], c[3], fv));
-            } else {
-              store_any(__builtin_assume_aligned(dst + 128 * i, 16), k0);
-              store_any(__builtin_assume_aligned(dst + 128 * i + 16, 16), k1);
-            }
-          }
-        }
       }
-      if constexpr (!SHARED) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          const float f = __uint_as_float(byte_of(vsc[s][i / 2], 16 * (i & 1) + 8 * (g >> 1)) << 23);
-          const u32v4 c = vraw[s][i];
-          store_any(__builtin_assume_aligned(dst + 128 * i, 16), codes_bf16(c[0], c[1], f));
-          store_any(__builtin_assume_aligned(dst + 128 * i + 16, 16), codes_bf16(c[2], c[3], f));
-        }
+      for (int i = 0; i < NV; ++i) {
+        const float f = __uint_as_float(byte_of(vsc[s][i / 2], 16 * (i & 1) + 8 * (g >> 1)) << 23);
+        const u32v4 c = vraw[s][i];
+        store_any(__builtin_assume_aligned(dst + 128 * i, 16), codes_bf16(c[0], c[1], f));
+        store_any(__builtin_assume_aligned(dst + 128 * i + 16, 16), codes_bf16(c[2], c[3], f));
       }
     }
     // the next tile's rows are on their way while this one is worked on
@@ -332,67 +266,79 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(AttendParams p) {
         store_any(p.part + at * dv + c, v);
         if (c == 0) p.stat[at] = s;
       } else {
-        const int t = paged ? static_cast<int>(div_by(r, p.by_G)) : t_unit;
-        const int64_t at = (static_cast<int64_t>(b) * a.T + t) * a.Hq + hk * p.G + (paged ? r - t * p.G : r);
-        const float inv = s[1] > 0.0f || s[1] != s[1] ? 1.0f / s[1] : 0.0f;
+        int t, h;
+        attend_row(p, spot, r, &t, &h);
+        const int64_t at = (static_cast<int64_t>(b) * a.T + t) * a.Hq + h;
+        const float inv = attend_inverse(s[1]);
         typedef T V4 __attribute__((ext_vector_type(4)));
         V4 y;
 #pragma unroll
         for (int e = 0; e < 4; ++e) y[e] = static_cast<T>(v[e] * inv);
         store_any(static_cast<T*>(a.out) + at * dv + c, y);
-        if (c == 0) a.lse[at] = s[1] == 0.0f ? kNegInf : (s[0] + __builtin_amdgcn_logf(s[1])) * kLn2;
+        if (c == 0) a.lse[at] = attend_lse(s[0], s[1]);
       }
     }
     __syncthreads();
   }
 }
 
-// Joins the splits of a list: one wave a row.
-template <class T, int MT>
+// Joins the splits of a list.  A workgroup takes one row; its lanes stand at
+// four channels each, in as many groups of splits as there is room for.
+template <class T>
 __global__ __launch_bounds__(kThreads) void join_kernel(AttendParams p) {
   const ets_attend_args& a = p.a;
-  const int lane = threadIdx.x & 63;
-  const uint32_t i = blockIdx.x * kWaves + (threadIdx.x >> 6);  // unit * row_groups * 16 MT rows
-  const uint32_t ug = i / (16 * MT);
-  const int in_group = static_cast<int>(i - ug * (16 * MT));
-  if (ug >= static_cast<uint32_t>(p.units) * p.row_groups) return;
+  __shared__ f32x4 sums[kThreads];
+  __shared__ f32x2 joined[kThreads];
+  const uint32_t ug = div_by(blockIdx.x, p.by_rows);
+  const int in_group = static_cast<int>(blockIdx.x - ug * p.group_rows);
   const uint32_t unit = div_by(ug, p.by_groups);
-  const int r = static_cast<int>(ug - unit * p.row_groups) * (16 * MT) + in_group;
+  const int r = static_cast<int>(ug - unit * p.row_groups) * p.group_rows + in_group;
   if (r >= p.rows) return;
   const bool paged = a.slots == nullptr;
   const uint32_t bt = div_by(unit, p.by_heads);
   const int hk = static_cast<int>(unit - bt * a.Hkv);
-  const int64_t at0 = static_cast<int64_t>(ug) * p.splits * (16 * MT) + in_group;
-  float high = kNegInf;
-  for (int s = lane; s < p.splits; s += 64) high = fmaxf(high, p.stat[at0 + s * (16 * MT)][0]);
-#pragma unroll
-  for (int o = 32; o; o >>= 1) high = fmaxf(high, __shfl_xor(high, o));
-  const float base = high == kNegInf ? 0.0f : high;
-  float total = 0.0f;
-  f32x4 v[3] = {};
-  for (int s = 0; s < p.splits; ++s) {
-    const int64_t at = at0 + s * (16 * MT);
-    const f32x2 st = p.stat[at];
-    const float f = __builtin_amdgcn_exp2f(st[0] - base);
-    total += st[1] * f;
-#pragma unroll
-    for (int j = 0; j < 3; ++j)
-      if (256 * j + 4 * lane < a.Dv) v[j] += load_any<f32x4>(p.part + at * a.Dv + 256 * j + 4 * lane) * f;
-  }
-  const int64_t row = paged ? (static_cast<int64_t>(bt) * a.T + div_by(r, p.by_G)) * a.Hq + hk * p.G + (r - div_by(r, p.by_G) * p.G)
-                            : static_cast<int64_t>(bt) * a.Hq + hk * p.G + r;
-  const float inv = total > 0.0f || total != total ? 1.0f / total : 0.0f;
-#pragma unroll
-  for (int j = 0; j < 3; ++j) {
-    if (256 * j + 4 * lane < a.Dv) {
-      typedef T V4 __attribute__((ext_vector_type(4)));
-      V4 y;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) y[e] = static_cast<T>(v[j][e] * inv);
-      store_any(static_cast<T*>(a.out) + row * a.Dv + 256 * j + 4 * lane, y);
+  const int64_t at0 = static_cast<int64_t>(ug) * p.splits * p.group_rows + in_group;
+  const int lanes = a.Dv / 4, groups = kThreads / lanes;
+  const int mine = static_cast<int>(threadIdx.x) / lanes, ch = 4 * (static_cast<int>(threadIdx.x) - mine * lanes);
+  float high = kNegInf, total = 0.0f;
+  f32x4 v = {};
+  if (mine < groups) {
+#pragma unroll 4
+    for (int s = mine; s < p.splits; s += groups) high = fmaxf(high, p.stat[at0 + static_cast<int64_t>(s) * p.group_rows][0]);
+    const float base = high == kNegInf ? 0.0f : high;
+#pragma unroll 4
+    for (int s = mine; s < p.splits; s += groups) {
+      const int64_t at = at0 + static_cast<int64_t>(s) * p.group_rows;
+      const f32x2 st = p.stat[at];
+      const float f = __builtin_amdgcn_exp2f(st[0] - base);
+      total += st[1] * f;
+      v += load_any<f32x4>(p.part + at * a.Dv + ch) * f;
     }
   }
-  if (lane == 0) a.lse[row] = total == 0.0f ? kNegInf : (high + __builtin_amdgcn_logf(total)) * kLn2;
+  sums[threadIdx.x] = v;
+  joined[threadIdx.x] = f32x2{high, total};
+  __syncthreads();
+  if (mine != 0) return;
+  const int last = groups < p.splits ? groups : p.splits;
+  for (int i = 1; i < last; ++i) high = fmaxf(high, joined[threadIdx.x + i * lanes][0]);
+  const float base = high == kNegInf ? 0.0f : high;
+  v = f32x4{};
+  total = 0.0f;
+  for (int i = 0; i < last; ++i) {
+    const f32x2 st = joined[threadIdx.x + i * lanes];
+    const float f = __builtin_amdgcn_exp2f(st[0] - base);
+    total += st[1] * f;
+    v += sums[threadIdx.x + i * lanes] * f;
+  }
+  const int t = paged ? static_cast<int>(div_by(r, p.by_G)) : 0;
+  const int64_t row = (static_cast<int64_t>(bt) * (paged ? a.T : 1) + t) * a.Hq + hk * p.G + (r - t * p.G);
+  const float inv = attend_inverse(total);
+  typedef T V4 __attribute__((ext_vector_type(4)));
+  V4 y;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) y[e] = static_cast<T>(v[e] * inv);
+  store_any(static_cast<T*>(a.out) + row * a.Dv + ch, y);
+  if (ch == 0) a.lse[row] = attend_lse(high, total);
 }
 
 // ---------------------------------------------------------------- host
@@ -428,16 +374,18 @@ ets_status make_plan(const ets_attend_args* a, Plan* plan) {
   p.G = a->Hq / a->Hkv;
   p.rows = paged ? a->T * p.G : p.G;
   p.units = a->B * a->Hkv * (paged ? 1 : a->T);
-  const int most = plan->width <= 2 ? 4 : plan->width <= 4 ? 2 : 1;
+  const int most = plan->width <= 2 ? 4 : 2;
   plan->mt = 1;
   while (plan->mt < most && 16 * plan->mt < p.rows) plan->mt *= 2;
-  p.row_groups = (p.rows + 16 * plan->mt - 1) / (16 * plan->mt);
+  if (plan->width == 9) plan->mt = 4;
+  p.group_rows = 16 * plan->mt;
+  p.row_groups = (p.rows + p.group_rows - 1) / p.group_rows;
   p.tree_tiles = a->tree_slots ? (a->T + kTile - 1) / kTile : 0;
   const int tiles = ((paged ? a->L : a->K) + kTile - 1) / kTile + p.tree_tiles;
   const int64_t lists = static_cast<int64_t>(p.units) * p.row_groups;
   // enough workgroups for two a compute unit, each wave with a tile at least
   int64_t splits = (2 * static_cast<int64_t>(cu) + lists - 1) / lists;
-  const int64_t cap = (tiles + kWaves - 1) / kWaves;
+  const int64_t cap = plan->width == 9 ? (tiles + 3) / 4 : (tiles + kWaves - 1) / kWaves;
   splits = splits > cap ? cap : splits;
   p.splits = static_cast<int>(splits < 1 ? 1 : splits);
   if (lists * p.splits > INT32_MAX / 16) return ETS_ERR_INVALID_ARG;
@@ -448,46 +396,42 @@ ets_status make_plan(const ets_attend_args* a, Plan* plan) {
   p.by_groups = fast_div(p.row_groups);
   p.by_splits = fast_div(p.splits);
   p.by_G = fast_div(p.G);
+  p.by_rows = fast_div(p.group_rows);
   if (p.splits > 1) plan->bytes = static_cast<size_t>(lists) * p.splits * 16 * plan->mt * (a->Dv * 4 + 8);
   return ETS_OK;
 }
 
-template <class T, int NP, int NV, bool SHARED, int MT>
-void launch_attend(const Plan& plan, hipStream_t s) {
-  const AttendParams& p = plan.p;
-  const size_t lds = kWaves * kTile * (NV * 128 + 32) + (kWaves + 1) * MT * 16 * sizeof(f32x2);
-  const int64_t lists = static_cast<int64_t>(p.units) * p.row_groups;
-  hipLaunchKernelGGL((attend_kernel<T, NP, NV, SHARED, MT>), dim3(static_cast<uint32_t>(lists * p.splits)),
-                     dim3(kThreads), lds, s, p);
-  if (p.splits > 1)
-    hipLaunchKernelGGL((join_kernel<T, MT>), dim3(static_cast<uint32_t>((lists * 16 * MT + kWaves - 1) / kWaves)),
-                       dim3(kThreads), 0, s, p);
+template <class T, int N, int MT>
+void launch_attend(const AttendParams& p, hipStream_t s) {
+  const size_t lds = kWaves * kTile * (N * 128 + 32) + (kWaves + 1) * MT * 16 * sizeof(f32x2);
+  const uint32_t grid = static_cast<uint32_t>(static_cast<int64_t>(p.units) * p.row_groups * p.splits);
+  hipLaunchKernelGGL((attend_kernel<T, N, N, MT>), dim3(grid), dim3(kThreads), lds, s, p);
 }
 
 template <class T, int N>
 void launch_width(const Plan& plan, hipStream_t s) {
   if (plan.mt == 1) {
-    launch_attend<T, N, N, false, 1>(plan, s);
+    launch_attend<T, N, 1>(plan.p, s);
   } else if (plan.mt == 2) {
-    launch_attend<T, N, N, false, 2>(plan, s);
+    launch_attend<T, N, 2>(plan.p, s);
   } else if constexpr (N <= 2) {
-    launch_attend<T, N, N, false, 4>(plan, s);
+    launch_attend<T, N, 4>(plan.p, s);
   }
 }
 
 template <class T>
 void launch_type(const Plan& plan, hipStream_t s) {
+  const AttendParams& p = plan.p;
   switch (plan.width) {
     case 1: launch_width<T, 1>(plan, s); break;
     case 2: launch_width<T, 2>(plan, s); break;
     case 3: launch_width<T, 3>(plan, s); break;
     case 4: launch_width<T, 4>(plan, s); break;
-    default:
-      if (plan.shared) {
-        launch_attend<T, 9, 8, true, 1>(plan, s);
-      } else {
-        launch_attend<T, 9, 9, false, 1>(plan, s);
-      }
+    default: launch_attend_wide(p, plan.mt, plan.shared, s);
+  }
+  if (p.splits > 1) {
+    const int64_t rows = static_cast<int64_t>(p.units) * p.row_groups * p.group_rows;
+    hipLaunchKernelGGL(join_kernel<T>, dim3(static_cast<uint32_t>(rows)), dim3(kThreads), 0, s, p);
   }
 }
 
