@@ -22,7 +22,8 @@ struct AttendParams {
   int splits;        // workgroups that share a list
   int tree_tiles;
   float scale_log2;  // log2(e) / sqrt(D)
-  FastDiv by_page, by_heads, by_tokens, by_groups, by_splits, by_G, by_rows;
+  FastDiv by_page, by_heads, by_tokens, by_groups, by_splits, by_G, by_rows, by_lanes, by_unit_rows;
+  int join_groups, join_rows;  // the join: shares of the splits, rows of a workgroup
   int group_rows;    // query rows of a workgroup, a multiple of 16
   float* part;       // [unit][row group][split][group_rows][Dv] sums
   f32x2* stat;       // [unit][row group][split][group_rows] (reference, sum)
@@ -34,6 +35,7 @@ struct AttendSpot {
   int split, row0, hk, b, t;  // t: the token of a selected list, 0 for paged ones
   bool paged;
   int n, main_tiles, tiles, first, last;
+  uint64_t tree;  // drafted tokens that stand in the list
 };
 __device__ __forceinline__ AttendSpot attend_spot(const AttendParams& p) {
   const ets_attend_args& a = p.a;
@@ -53,31 +55,40 @@ __device__ __forceinline__ AttendSpot attend_spot(const AttendParams& p) {
   const int per = (s.tiles + p.splits - 1) / p.splits;
   s.first = s.split * per;
   s.last = min(s.first + per, s.tiles);
+  // one token's list leaves out the drafted tokens that it does not see, so nothing of them is read
+  s.tree = ~0ull;
+  if (!s.paged && a.tree_slots) s.tree = static_cast<uint64_t>(a.tree_mask[s.b * a.mask_b + s.t]);
+  if (a.T < 64) s.tree &= (1ull << a.T) - 1;
   return s;
 }
 
-// Slot of key `at` (0 to 31) of tile i; -1 where there is none.  The tree's
-// tiles stand behind the main ones.  One token's list leaves out the drafted
-// tokens that it does not see, so nothing of them is read.
-__device__ __forceinline__ int32_t attend_slot(const AttendParams& p, const AttendSpot& s, int i, int at) {
+// The slot of key `at` (0 to 31) of tile i, in two parts: the first asks memory
+// for what it depends on, the second makes the slot of it (-1 where there is
+// none), so that the wait can stand far from the request.  Neither branches (a
+// load under way is waited for where branches meet): a key that is not there
+// reads the kernel's first query.  The tree's tiles stand behind the main ones.
+__device__ __forceinline__ bool attend_there(const AttendSpot& s, int i, int at) {
+  const int j = i * kAttendTile + at, k = (i - s.main_tiles) * kAttendTile + at;
+  return i < s.main_tiles ? j < s.n : i < s.tiles && (s.tree >> (k & 63) & 1);
+}
+__device__ __forceinline__ int32_t attend_ask(const AttendParams& p, const AttendSpot& s, int i, int at) {
+  typedef __attribute__((address_space(1))) const int32_t* Global4;
   const ets_attend_args& a = p.a;
-  int64_t slot = -1;
-  if (i < s.main_tiles) {
-    const int j = i * kAttendTile + at;
-    if (j < s.n) {
-      if (s.paged) {
-        const uint32_t page = div_by(j, p.by_page);
-        slot = static_cast<int64_t>(a.page_table[s.b * a.pt_b + page]) * a.page_size + (j - page * p.by_page.d);
-      } else {
-        slot = a.slots[s.b * a.slots_b + s.t * a.slots_t + j];
-      }
-    }
-  } else {
-    const int j = (i - s.main_tiles) * kAttendTile + at;
-    if (i < s.tiles && j < a.T && (s.paged || (a.tree_mask[s.b * a.mask_b + s.t] >> j & 1)))
-      slot = a.tree_slots[s.b * a.tree_b + j];
-  }
-  return slot >= 0 && slot < a.S ? static_cast<int32_t>(slot) : -1;
+  const int j = i * kAttendTile + at, k = (i - s.main_tiles) * kAttendTile + at;
+  const uint64_t list = s.paged ? reinterpret_cast<uint64_t>(a.page_table + s.b * a.pt_b)
+                                : reinterpret_cast<uint64_t>(a.slots + s.b * a.slots_b + s.t * a.slots_t);
+  const uint64_t tree = reinterpret_cast<uint64_t>(a.tree_slots + s.b * a.tree_b);
+  const uint32_t page = div_by(static_cast<uint32_t>(j) & 0x7fffffffu, p.by_page);
+  uint64_t from = i < s.main_tiles ? list + 4ull * (s.paged ? page : static_cast<uint32_t>(j)) : tree + 4ull * (k & 63);
+  from = attend_there(s, i, at) ? from : reinterpret_cast<uint64_t>(a.q) & ~3ull;
+  return *reinterpret_cast<Global4>(from);
+}
+__device__ __forceinline__ int32_t attend_slot(const AttendParams& p, const AttendSpot& s, int i, int at, int32_t asked) {
+  const int j = i * kAttendTile + at;
+  const uint32_t page = div_by(static_cast<uint32_t>(j) & 0x7fffffffu, p.by_page);
+  const int64_t paged = static_cast<int64_t>(asked) * p.a.page_size + (j - static_cast<int64_t>(page) * p.by_page.d);
+  const int64_t slot = s.paged && i < s.main_tiles ? paged : asked;
+  return attend_there(s, i, at) && asked >= 0 && slot < p.a.S ? static_cast<int32_t>(slot) : -1;
 }
 
 // (token, query head) of a workgroup's row r.
@@ -93,8 +104,11 @@ __device__ __forceinline__ float attend_inverse(float sum) {
   return sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
 }
 
-// Bytes of LDS, and the launch, of the kernel for heads over 256 channels
-// (ets_attend_wide.hip); row_tiles: 4 or 8 tiles of 16 query rows.
+// The launch of the kernel for heads over 256 channels (ets_attend_wide.hip);
+// row_tiles: tiles of 16 query rows of a workgroup, as attend_wide_rows gives.
+inline int attend_wide_rows(int rows, bool shared, bool bf16) {
+  return shared && bf16 && rows > 32 ? 4 : 2;
+}
 void launch_attend_wide(const AttendParams& p, int row_tiles, bool shared, hipStream_t s);
 
 }  // namespace ets

@@ -76,7 +76,7 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(AttendParams p) {
   }
 
   // slot of the key that this lane loads: 16 s + col of tile i
-  auto slot_of = [&](int i, int s) { return attend_slot(p, spot, i, 16 * s + col); };
+  auto slot_of = [&](int i, int s) { return attend_slot(p, spot, i, 16 * s + col, attend_ask(p, spot, i, 16 * s + col)); };
 
   const int nbk = a.D / kCacheBlock, nbv = a.Dv / kCacheBlock;
   const uint8_t* kc = a.k_codes + hk * a.k_h + 16 * g;
@@ -282,32 +282,32 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(AttendParams p) {
   }
 }
 
-// Joins the splits of a list.  A workgroup takes one row; its lanes stand at
-// four channels each, in as many groups of splits as there is room for.
+// Joins the splits of a list.  A lane stands at four channels of one row; Dv / 4
+// lanes by `groups` shares of the splits take the row, and a workgroup as many
+// rows as it has lanes for.
 template <class T>
 __global__ __launch_bounds__(kThreads) void join_kernel(AttendParams p) {
   const ets_attend_args& a = p.a;
   __shared__ f32x4 sums[kThreads];
   __shared__ f32x2 joined[kThreads];
-  const uint32_t ug = div_by(blockIdx.x, p.by_rows);
-  const int in_group = static_cast<int>(blockIdx.x - ug * p.group_rows);
-  const uint32_t unit = div_by(ug, p.by_groups);
-  const int r = static_cast<int>(ug - unit * p.row_groups) * p.group_rows + in_group;
-  if (r >= p.rows) return;
-  const bool paged = a.slots == nullptr;
-  const uint32_t bt = div_by(unit, p.by_heads);
-  const int hk = static_cast<int>(unit - bt * a.Hkv);
-  const int64_t at0 = static_cast<int64_t>(ug) * p.splits * p.group_rows + in_group;
-  const int lanes = a.Dv / 4, groups = kThreads / lanes;
-  const int mine = static_cast<int>(threadIdx.x) / lanes, ch = 4 * (static_cast<int>(threadIdx.x) - mine * lanes);
+  const int lanes = a.Dv / 4;
+  const int slot = static_cast<int>(div_by(threadIdx.x, p.by_lanes));  // row and share
+  const int ch = 4 * (static_cast<int>(threadIdx.x) - slot * lanes);
+  const int my_row = slot / p.join_groups, mine = slot - my_row * p.join_groups;
+  const int64_t index = static_cast<int64_t>(blockIdx.x) * p.join_rows + my_row;
+  const bool live = my_row < p.join_rows && index < static_cast<int64_t>(p.units) * p.rows;
+  const uint32_t unit = live ? div_by(static_cast<uint32_t>(index), p.by_unit_rows) : 0;
+  const int r = live ? static_cast<int>(index - static_cast<int64_t>(unit) * p.rows) : 0;
+  const int group = static_cast<int>(div_by(r, p.by_rows)), in_group = r - group * p.group_rows;
+  const int64_t at0 = (static_cast<int64_t>(unit) * p.row_groups + group) * p.splits * p.group_rows + in_group;
   float high = kNegInf, total = 0.0f;
   f32x4 v = {};
-  if (mine < groups) {
+  if (live) {
 #pragma unroll 4
-    for (int s = mine; s < p.splits; s += groups) high = fmaxf(high, p.stat[at0 + static_cast<int64_t>(s) * p.group_rows][0]);
+    for (int s = mine; s < p.splits; s += p.join_groups) high = fmaxf(high, p.stat[at0 + static_cast<int64_t>(s) * p.group_rows][0]);
     const float base = high == kNegInf ? 0.0f : high;
 #pragma unroll 4
-    for (int s = mine; s < p.splits; s += groups) {
+    for (int s = mine; s < p.splits; s += p.join_groups) {
       const int64_t at = at0 + static_cast<int64_t>(s) * p.group_rows;
       const f32x2 st = p.stat[at];
       const float f = __builtin_amdgcn_exp2f(st[0] - base);
@@ -315,21 +315,26 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttendParams p) {
       v += load_any<f32x4>(p.part + at * a.Dv + ch) * f;
     }
   }
-  sums[threadIdx.x] = v;
-  joined[threadIdx.x] = f32x2{high, total};
-  __syncthreads();
-  if (mine != 0) return;
-  const int last = groups < p.splits ? groups : p.splits;
-  for (int i = 1; i < last; ++i) high = fmaxf(high, joined[threadIdx.x + i * lanes][0]);
-  const float base = high == kNegInf ? 0.0f : high;
-  v = f32x4{};
-  total = 0.0f;
-  for (int i = 0; i < last; ++i) {
-    const f32x2 st = joined[threadIdx.x + i * lanes];
-    const float f = __builtin_amdgcn_exp2f(st[0] - base);
-    total += st[1] * f;
-    v += sums[threadIdx.x + i * lanes] * f;
+  if (p.join_groups > 1) {
+    sums[threadIdx.x] = v;
+    joined[threadIdx.x] = f32x2{high, total};
+    __syncthreads();
+    if (mine != 0) return;
+    for (int i = 1; i < p.join_groups; ++i) high = fmaxf(high, joined[threadIdx.x + i * lanes][0]);
+    const float base = high == kNegInf ? 0.0f : high;
+    v = f32x4{};
+    total = 0.0f;
+    for (int i = 0; i < p.join_groups; ++i) {
+      const f32x2 st = joined[threadIdx.x + i * lanes];
+      const float f = __builtin_amdgcn_exp2f(st[0] - base);
+      total += st[1] * f;
+      v += sums[threadIdx.x + i * lanes] * f;
+    }
   }
+  if (!live) return;
+  const bool paged = a.slots == nullptr;
+  const uint32_t bt = div_by(unit, p.by_heads);
+  const int hk = static_cast<int>(unit - bt * a.Hkv);
   const int t = paged ? static_cast<int>(div_by(r, p.by_G)) : 0;
   const int64_t row = (static_cast<int64_t>(bt) * (paged ? a.T : 1) + t) * a.Hq + hk * p.G + (r - t * p.G);
   const float inv = attend_inverse(total);
@@ -360,6 +365,9 @@ ets_status make_plan(const ets_attend_args* a, Plan* plan) {
   const bool paged = a->slots == nullptr;
   if (paged ? (a->L < 0 || a->page_size < 1) : a->K < 0) return ETS_ERR_INVALID_ARG;
   if (a->tree_slots && a->T > ETS_MAX_TREE) return ETS_ERR_INVALID_ARG;
+  // row strides are 32-bit numbers in the wide kernel; 4 GiB from slot to slot is no cache
+  if (a->k_s < 0 || a->ks_s < 0 || a->v_s < 0 || a->vs_s < 0 || (a->k_s | a->ks_s | a->v_s | a->vs_s) > UINT32_MAX)
+    return ETS_ERR_INVALID_ARG;
   *plan = Plan{};
   AttendParams& p = plan->p;
   p.a = *a;
@@ -377,14 +385,14 @@ ets_status make_plan(const ets_attend_args* a, Plan* plan) {
   const int most = plan->width <= 2 ? 4 : 2;
   plan->mt = 1;
   while (plan->mt < most && 16 * plan->mt < p.rows) plan->mt *= 2;
-  if (plan->width == 9) plan->mt = 4;
+  if (plan->width == 9) plan->mt = attend_wide_rows(p.rows, plan->shared, a->dtype == ETS_BF16);
   p.group_rows = 16 * plan->mt;
   p.row_groups = (p.rows + p.group_rows - 1) / p.group_rows;
   p.tree_tiles = a->tree_slots ? (a->T + kTile - 1) / kTile : 0;
   const int tiles = ((paged ? a->L : a->K) + kTile - 1) / kTile + p.tree_tiles;
   const int64_t lists = static_cast<int64_t>(p.units) * p.row_groups;
-  // enough workgroups for two a compute unit, each wave with a tile at least
-  int64_t splits = (2 * static_cast<int64_t>(cu) + lists - 1) / lists;
+  // enough workgroups for two a compute unit (one of the wide kernel's), each wave with a tile at least
+  int64_t splits = ((plan->width == 9 ? 1 : 2) * static_cast<int64_t>(cu) + lists - 1) / lists;
   const int64_t cap = plan->width == 9 ? (tiles + 3) / 4 : (tiles + kWaves - 1) / kWaves;
   splits = splits > cap ? cap : splits;
   p.splits = static_cast<int>(splits < 1 ? 1 : splits);
@@ -397,6 +405,11 @@ ets_status make_plan(const ets_attend_args* a, Plan* plan) {
   p.by_splits = fast_div(p.splits);
   p.by_G = fast_div(p.G);
   p.by_rows = fast_div(p.group_rows);
+  const int lanes = a->Dv / 4;
+  p.join_groups = kThreads / lanes < p.splits / 4 ? kThreads / lanes : p.splits / 4 > 1 ? p.splits / 4 : 1;
+  p.join_rows = kThreads / (lanes * p.join_groups);
+  p.by_lanes = fast_div(lanes);
+  p.by_unit_rows = fast_div(p.rows);
   if (p.splits > 1) plan->bytes = static_cast<size_t>(lists) * p.splits * 16 * plan->mt * (a->Dv * 4 + 8);
   return ETS_OK;
 }
@@ -430,8 +443,8 @@ void launch_type(const Plan& plan, hipStream_t s) {
     default: launch_attend_wide(p, plan.mt, plan.shared, s);
   }
   if (p.splits > 1) {
-    const int64_t rows = static_cast<int64_t>(p.units) * p.row_groups * p.group_rows;
-    hipLaunchKernelGGL(join_kernel<T>, dim3(static_cast<uint32_t>(rows)), dim3(kThreads), 0, s, p);
+    const int64_t rows = static_cast<int64_t>(p.units) * p.rows;
+    hipLaunchKernelGGL(join_kernel<T>, dim3(static_cast<uint32_t>((rows + p.join_rows - 1) / p.join_rows)), dim3(kThreads), 0, s, p);
   }
 }
 

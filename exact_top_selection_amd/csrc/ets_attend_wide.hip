@@ -1,336 +1,380 @@
 // ets_attend_wide.hip -- attention over an 8-bit cache for heads of 257 to 576
 // channels, one latent head shared by many query heads above all (gfx950).
+#include <type_traits>
+
 #include "ets_attend.h"
 
 namespace ets {
 namespace {
 
-constexpr int kPairs = 9;              // 64-channel steps of a key
-constexpr int kPitch = kPairs * 64;    // bytes of a row of codes in LDS
-constexpr int kBlocks = 2 * kPairs;    // scale bytes of a row
+constexpr int kThreads = 512;
 constexpr int kTile = kAttendTile;
-constexpr int kChunks = 5;             // 16-byte pieces of a tile that a lane brings: ceil(32 * 36 / 256)
-constexpr float kSlack = 8.0f;         // how far (log2) a score may pass the reference before sums are rescaled
+constexpr int kPairs = 9;            // 64-channel steps of a key
+constexpr int kPieces = 36;          // 16-code pieces of a key
+constexpr int kPlane = 16 * kPieces; // bytes of one half of each decoded piece of a row
+// Bytes of a decoded row in LDS: first the lower halves of its pieces, then
+// the upper ones, so that lanes write next to each other; rows lie 36 banks
+// apart, so that the 16 rows of an operand load fill all 64.
+constexpr int kPitch = 2 * kPlane + 16;
+constexpr int kDepth = 2;            // tiles on their way from memory
+constexpr float kSlack = 8.0f;       // how far (log2) a score may pass its reference
 
-// Position of 16-byte piece c of row k in LDS: rows lie 576 bytes (16 banks)
-// apart, and the exchange of pieces inside each 64 bytes spreads the 16 rows
-// that one operand load touches over all 64 banks.
-__device__ __forceinline__ int place(int k, int c) {
-  return k * kPitch + 16 * (c ^ ((k >> 2) & 3));
-}
+// Read in the place of a row that is not there.
+__device__ const u32v4 kNothing[kPieces] = {};
 
-template <int RT, int NC, bool SHARED, bool TWO>
-struct WideLds {
-  uint8_t k[3][kTile * kPitch];
-  uint8_t v[SHARED ? 1 : 3][SHARED ? 16 : kTile * kPitch];
-  float ks[3][kBlocks][kTile];                                             // scale of a block of a key, by key
-  float vs[SHARED && !TWO ? 1 : 3][SHARED && !TWO ? 1 : kBlocks][kTile];
-  float rs[TWO ? 3 : 1][kTile];                                            // fp16: scale of a key's whole row
-  u32v4 prob[2][TWO ? 2 : 1][RT][64];
-  float fade[2][RT][16];
-  int fading[2][RT];
-  int32_t slot[8][kTile];
-  f32x2 stat[RT * 16];
+// Pieces of a tile on their way through a lane, and their scale bytes.
+template <int N>
+struct Pieces {
+  static constexpr int n = N;
+  u32v4 w[N];
+  uint32_t byte[N];
 };
 
-// A workgroup takes 16 RT query rows (all 128 heads of a latent cache with RT
-// = 8) through its share of the keys, 32 a step, so that a row of the cache is
-// brought once.  Codes go to LDS as they are, through registers, two steps
-// ahead.  Scores are formed as K Q^T by the wave that owns the query rows (16
-// or 32 of them, in registers); the probabilities go through LDS, and each
-// wave then takes a quarter of the channels of out^T = V^T P^T for all rows:
-// a value is decoded once, by the wave that uses it, out of the transposed
-// byte load (ds_read_b64_tr_b8), whose lanes hold one channel of 8 keys and
-// multiply each by its own scale.  One barrier a step; the products of step i
-// stand next to the scores of step i + 1.
+template <int RT, bool SHARED, bool TWO>
+struct WideLds {
+  uint8_t k[SHARED ? 3 : 2][kTile * kPitch];
+  uint8_t v[SHARED ? 1 : 2][SHARED ? 16 : kTile * kPitch];
+  u32v2 prob[2][TWO ? 2 : 1][2][RT][64];  // [parity][part][team]
+  float ref[2][2][RT * 16];               // [parity][team]
+  int32_t slot[4][kTile];  // -1: not there
+  uint32_t seen[8];                          // which keys of a tile are there
+  f32x2 stat[2][RT * 16];
+};
+
+// A workgroup takes 16 RT query rows through its share of the keys, 32 a step.
+// Codes come through registers, two steps ahead (rows lie anywhere in the
+// cache, so a row takes 1 to 2 us to arrive), and are decoded to bf16, which
+// holds them exactly, on their way into LDS: once for all query rows, and once
+// for keys and values where the values are the keys' first channels (SHARED).
 //
-// The softmax is taken relative to a reference that follows the largest score
-// only when that passes it by more than 2^8: sums in 32 bits lose nothing by
-// it, and the 64 to 256 registers of sums are rescaled once or twice a list.
+// Waves 0 to 3 form scores as K Q^T: half of the query rows, in registers, by
+// half of the step's keys (a "team").  Their probabilities go through LDS to
+// waves 4 to 7, which hold the sums out^T = V^T P^T, a quarter of the channels
+// each, with V^T out of transposed loads (ds_read_b64_tr_b16).  Each SIMD has
+// one wave of either kind, scores run one step ahead of the sums, and a step
+// has one barrier; within it one wave lays out rows while the other multiplies.
+//
+// The softmax is taken relative to a whole-numbered reference that each team
+// raises only when a score passes it by more than 2^8, and that follows the
+// other team's of the step before.  Where a reference has changed, or the two
+// differ, sums and probabilities are brought together by powers of two, which
+// is exact; that happens a few times a list.
+//
+// fp16 queries and probabilities (TWO) are sums of two bf16 numbers each: the
+// query exactly, the probability to 16 bits.
 template <class T, int RT, int NC, bool SHARED>
-__global__ __launch_bounds__(kAttendThreads) void attend_wide_kernel(AttendParams p) {
-  typedef Mat<T> M;
-  typedef typename M::V8 V8;
-  constexpr bool kTwo = M::kRowScale;
-  constexpr int MQ = RT / kAttendWaves;  // 16-row tiles whose scores a wave forms
-  typedef WideLds<RT, NC, SHARED, kTwo> Lds;
+__global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendParams p) {
+  constexpr bool kTwo = Mat<T>::kRowScale;
+  constexpr int MQ = RT / 2;  // 16-row tiles of a score wave
+  typedef WideLds<RT, SHARED, kTwo> Lds;
+  typedef T T8 __attribute__((ext_vector_type(8)));
+  typedef __bf16 B4 __attribute__((ext_vector_type(4)));
   extern __shared__ __align__(16) char lds_raw[];
   Lds& lds = *reinterpret_cast<Lds*>(lds_raw);
   const ets_attend_args& a = p.a;
   const AttendSpot spot = attend_spot(p);
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, col = lane & 15, g = lane >> 4;
-  const int steps = max(spot.last - spot.first, 0);
+  const int tid = threadIdx.x, lane = tid & 63, col = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int tiles = max(spot.last - spot.first, 0);
+  const int steps = (tiles + 1) & ~1;  // pairs: the staging registers of either parity keep their places
 
-  // rows shorter than 576 leave pieces and scales that are never brought
-  for (int i = tid; i < static_cast<int>(sizeof(Lds) / 16); i += kAttendThreads)
-    reinterpret_cast<u32v4*>(lds_raw)[i] = u32v4{0, 0, 0, 0};
-
-  V8 q[MQ][kPairs][2];
-  uint64_t tree_bits[MQ];
+  // The 1152 pieces of a tile: waves 4 to 7 bring four a lane, waves 0 and 1 the
+  // last 128 (waves 0 to 3 need their registers for operands on their way).
+  const bool sums = wave >= 4;
+  const int piece0 = sums ? tid - 256 : 1024 + tid;
+  // addresses as numbers: a row that is not there is read from kNothing, without a branch
+  typedef __attribute__((address_space(1))) const u32v4* Global16;
+  typedef __attribute__((address_space(1))) const uint8_t* Global1;
+  const uint64_t nothing = reinterpret_cast<uint64_t>(&kNothing[0]);
+  auto bring = [&](auto& set, int i, uint64_t codes, uint32_t row, uint64_t scales, uint32_t scale_row, int pieces) {
+    const int32_t* slots = lds.slot[i & 3];
+    constexpr int N = std::remove_reference_t<decltype(set)>::n;
+    int32_t slot[N];
 #pragma unroll
-  for (int m = 0; m < MQ; ++m) {
-    const int r = spot.row0 + 16 * (wave * MQ + m) + col;
-    int t, h;
-    attend_row(p, spot, r, &t, &h);
-    const char* src = static_cast<const char*>(a.q) + 2 * (spot.b * a.q_b + t * a.q_t + h * a.q_h);
-    tree_bits[m] = 0;
+    for (int j = 0; j < N; ++j) slot[j] = slots[(piece0 + 256 * j) / kPieces];
 #pragma unroll
-    for (int i = 0; i < kPairs; ++i) {
-      q[m][i][0] = V8{};
-      q[m][i][1] = V8{};
-      if (r < p.rows && 64 * i + 16 * g < a.D) {
-        q[m][i][0] = load_any<V8>(src + 128 * i + 32 * g);
-        q[m][i][1] = load_any<V8>(src + 128 * i + 32 * g + 16);
-      }
+    for (int j = 0; j < N; ++j) {
+      const int at = (piece0 + 256 * j) % kPieces;
+      const bool there = slot[j] >= 0 && at < pieces;
+      const uint64_t w = codes + static_cast<uint64_t>(static_cast<uint32_t>(slot[j])) * row + 16 * at;
+      const uint64_t b = scales + static_cast<uint64_t>(static_cast<uint32_t>(slot[j])) * scale_row + (at >> 1);
+      set.w[j] = *reinterpret_cast<Global16>(there ? w : nothing);
+      set.byte[j] = *reinterpret_cast<Global1>(there ? b : nothing);
     }
-    if (r < p.rows && a.tree_slots) tree_bits[m] = static_cast<uint64_t>(a.tree_mask[spot.b * a.mask_b + t]);
-  }
+  };
+  auto lay = [&](const auto& set, uint8_t* tile) {
+#pragma unroll
+    for (int j = 0; j < set.n; ++j) {
+      const int c = piece0 + 256 * j;
+      const float f = __uint_as_float(set.byte[j] << 23);
+      uint8_t* dst = tile + c / kPieces * kPitch + 16 * (c % kPieces);
+      *reinterpret_cast<bf16x8*>(dst) = codes_bf16(set.w[j][0], set.w[j][1], f);
+      *reinterpret_cast<bf16x8*>(dst + kPlane) = codes_bf16(set.w[j][2], set.w[j][3], f);
+    }
+  };
+  const uint64_t kc = reinterpret_cast<uint64_t>(a.k_codes + spot.hk * a.k_h);
+  const uint64_t ks = reinterpret_cast<uint64_t>(a.k_scales + spot.hk * a.ks_h);
+  const uint64_t vc = reinterpret_cast<uint64_t>(a.v_codes + spot.hk * a.v_h);
+  const uint64_t vs = reinterpret_cast<uint64_t>(a.v_scales + spot.hk * a.vs_h);
+  const uint32_t k_row = static_cast<uint32_t>(a.k_s), ks_row = static_cast<uint32_t>(a.ks_s);
+  const uint32_t v_row = static_cast<uint32_t>(a.v_s), vs_row = static_cast<uint32_t>(a.vs_s);
+  auto bring_k = [&](auto& set, int i) { bring(set, i, kc, k_row, ks, ks_row, a.D / 16); };
+  auto bring_v = [&](auto& set, int i) { bring(set, i, vc, v_row, vs, vs_row, a.Dv / 16); };
+  // the slots of tile i, by 32 lanes: first what they depend on, later themselves
+  auto ask = [&](int i) { return attend_ask(p, spot, spot.first + i, tid & 31); };
+  auto keep = [&](int i, int32_t asked) {
+    const int32_t slot = attend_slot(p, spot, spot.first + i, tid & 31, asked);
+    const bool there = slot >= 0 && i < tiles;
+    lds.slot[i & 3][tid & 31] = there ? slot : -1;
+    const uint64_t seen = __ballot(there);
+    if ((tid & 31) == 0) lds.seen[i & 7] = static_cast<uint32_t>(seen >> (tid & 32));
+  };
+
+  if (tid < 4 * kTile) keep(tid >> 5, ask(tid >> 5));
   __syncthreads();
-
-  // the pieces of a tile that this lane brings: key (high half) and piece of its row
-  const int nbk = a.D / kCacheBlock, nbv = a.Dv / kCacheBlock;
-  int piece[kChunks], piece_v[SHARED ? 1 : kChunks];
-#pragma unroll
-  for (int j = 0; j < kChunks; ++j) {
-    const int c = tid + kAttendThreads * j;
-    piece[j] = c < kTile * 2 * nbk ? ((c / (2 * nbk)) << 16) | (c % (2 * nbk)) : -1;
-    if constexpr (!SHARED) piece_v[j] = c < kTile * 2 * nbv ? ((c / (2 * nbv)) << 16) | (c % (2 * nbv)) : -1;
-  }
-  const uint8_t* kc = a.k_codes + spot.hk * a.k_h;
-  const uint8_t* ks = a.k_scales + spot.hk * a.ks_h;
-  const uint8_t* vc = a.v_codes + spot.hk * a.v_h;
-  const uint8_t* vs = a.v_scales + spot.hk * a.vs_h;
-  u32v4 kreg[kChunks], vreg[SHARED ? 1 : kChunks];
-  uint32_t kword = 0, vword = 0;
-  // word w of the scale bytes of a row: lanes 8 k .. 8 k + 7 hold key k's
-  auto scale_word = [&](const uint8_t* row, int nb) -> uint32_t {
-    const int w = 4 * (tid & 7);
-    if (w + 4 <= nb) return load_any<uint32_t>(row + w);
-    uint32_t x = 0;
-    if (w < nb) x = row[w];
-    if (w + 1 < nb) x |= static_cast<uint32_t>(row[w + 1]) << 8;
-    if (w + 2 < nb) x |= static_cast<uint32_t>(row[w + 2]) << 16;
-    return x;
-  };
-  auto bring = [&](int i) {  // tile i of the workgroup's share into registers
-    const int32_t* slots = lds.slot[i & 7];
-#pragma unroll
-    for (int j = 0; j < kChunks; ++j) {
-      kreg[j] = u32v4{0, 0, 0, 0};
-      if (piece[j] >= 0) {
-        const int64_t slot = slots[piece[j] >> 16];
-        if (slot >= 0) kreg[j] = load_any<u32v4>(kc + slot * a.k_s + 16 * (piece[j] & 0xffff));
-      }
-      if constexpr (!SHARED) {
-        vreg[j] = u32v4{0, 0, 0, 0};
-        if (piece_v[j] >= 0) {
-          const int64_t slot = slots[piece_v[j] >> 16];
-          if (slot >= 0) vreg[j] = load_any<u32v4>(vc + slot * a.v_s + 16 * (piece_v[j] & 0xffff));
-        }
-      }
+  auto begin = [&](auto& kset, auto& vset) {  // before the first step: tiles 0 and 1 in LDS (values: 0)
+    bring_k(kset[0], 0);
+    bring_k(kset[1], 1);
+    if constexpr (!SHARED) {
+      bring_v(vset[0], 0);
+      bring_v(vset[1], 1);
     }
-    const int64_t slot = slots[tid >> 3];
-    kword = 0, vword = 0;
-    if (slot >= 0) {
-      kword = scale_word(ks + slot * a.ks_s, nbk);
-      if constexpr (!SHARED) vword = scale_word(vs + slot * a.vs_s, nbv);
+    lay(kset[0], lds.k[0]);
+    bring_k(kset[0], 2);
+    lay(kset[1], lds.k[1]);
+    bring_k(kset[1], 3);
+    if constexpr (!SHARED) {
+      lay(vset[0], lds.v[0]);
+      bring_v(vset[0], 2);
     }
   };
-  auto lay = [&](int i) {  // registers into LDS, as tile i
-    const int at = i % 3;
-#pragma unroll
-    for (int j = 0; j < kChunks; ++j) {
-      if (piece[j] >= 0) *reinterpret_cast<u32v4*>(lds.k[at] + place(piece[j] >> 16, piece[j] & 0xffff)) = kreg[j];
-      if constexpr (!SHARED)
-        if (piece_v[j] >= 0) *reinterpret_cast<u32v4*>(lds.v[at] + place(piece_v[j] >> 16, piece_v[j] & 0xffff)) = vreg[j];
-    }
-    uint32_t top = 0;
-    if constexpr (kTwo) {
-      const uint32_t one[1] = {kword};
-      top = scales_max<1>(one);
-      for (int o = 1; o < 8; o <<= 1) top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), o)));
-      if ((tid & 7) == 0) lds.rs[at][tid >> 3] = __uint_as_float(top << 23);
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int b = 4 * (tid & 7) + e;
-      if (b < kBlocks) {
-        const uint32_t byte = byte_of(kword, 8 * e);
-        lds.ks[at][b][tid >> 3] = M::scale(byte, top);
-        if constexpr (SHARED && kTwo) lds.vs[at][b][tid >> 3] = __uint_as_float(byte << 23);
-        if constexpr (!SHARED) lds.vs[at][b][tid >> 3] = __uint_as_float(byte_of(vword, 8 * e) << 23);
-      }
+  // step i: tile i + 2 into LDS (values: i + 1), tile i + 4 (i + 3) asked for; `odd` is i % 2, `to` the place of tile i + 2
+  auto stage = [&](auto& kset, auto& vset, auto odd, int i, int to) {
+    constexpr int O = decltype(odd)::value;
+    lay(kset[O], lds.k[to]);
+    bring_k(kset[O], i + 4);
+    if constexpr (!SHARED) {
+      lay(vset[O ^ 1], lds.v[O ^ 1]);
+      bring_v(vset[O ^ 1], i + 3);
     }
   };
-  auto find = [&](int i) {  // slots of tile i, by the first 32 lanes
-    return i < steps ? attend_slot(p, spot, spot.first + i, tid & 31) : -1;
+  // Runs step(odd, i, places of tiles i, i + 1, i + 2).  Nothing in it depends
+  // on i by a branch: a load that is under way where branches meet is waited for.
+  auto run = [&](auto step) {
+    int at = 0, next = 1;
+    for (int i = 0; i < steps; i += 2) {
+      const int after = SHARED ? 3 - at - next : at;
+      step(std::integral_constant<int, 0>{}, i, at, next, after);
+      __syncthreads();
+      step(std::integral_constant<int, 1>{}, i + 1, next, after, SHARED ? at : next);
+      __syncthreads();
+      const int a0 = after, a1 = SHARED ? at : next;
+      at = a0, next = a1;
+    }
   };
 
-  float ref[MQ], sum[MQ];
-#pragma unroll
-  for (int m = 0; m < MQ; ++m) ref[m] = kNegInf, sum[m] = 0.0f;
-  // scores and probabilities of tile i
-  auto scores = [&](int i) {
-    const int at = i % 3, half = i & 1, tile = spot.first + i;
-    f32x4 x[MQ][2];
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-#pragma unroll
-      for (int m = 0; m < MQ; ++m) x[m][s] = f32x4{};
-#pragma unroll
-      for (int c = 0; c < kPairs; ++c) {
-        const u32v4 w = *reinterpret_cast<const u32v4*>(lds.k[at] + place(16 * s + col, 4 * c + g));
-        const float f = lds.ks[at][2 * c + (g >> 1)][16 * s + col];
-        const V8 k0 = M::keys(w[0], w[1], f), k1 = M::keys(w[2], w[3], f);
-#pragma unroll
-        for (int m = 0; m < MQ; ++m) {
-          x[m][s] = M::mma(k0, q[m][c][0], x[m][s]);
-          x[m][s] = M::mma(k1, q[m][c][1], x[m][s]);
-        }
-      }
-    }
-    if constexpr (kTwo) {
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const f32x4 f = *reinterpret_cast<const f32x4*>(&lds.rs[at][16 * s + 4 * g]);
-#pragma unroll
-        for (int m = 0; m < MQ; ++m)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[m][s][e] *= f[e];
-      }
-    }
-    const uint32_t seen = static_cast<uint32_t>(__ballot(lds.slot[i & 7][lane & 31] >= 0));
+  if (wave < 4) {
+    // ---- scores
+    const int hg = wave & 1, team = wave >> 1;
+    bf16x8 q[MQ][kPairs][2], q_rest[kTwo ? MQ : 1][kPairs][2];
+    uint64_t tree_bits[MQ];
 #pragma unroll
     for (int m = 0; m < MQ; ++m) {
-      uint32_t vis = seen;
-      if (tile >= spot.main_tiles) vis &= static_cast<uint32_t>(tree_bits[m] >> (kTile * (tile - spot.main_tiles)));
-      vis >>= 4 * g;
-      float y[8], high = kNegInf;
+      const int r = spot.row0 + 16 * (MQ * hg + m) + col;
+      int t, h;
+      attend_row(p, spot, r, &t, &h);
+      const char* src = static_cast<const char*>(a.q) + 2 * (spot.b * a.q_b + t * a.q_t + h * a.q_h);
+      tree_bits[m] = 0;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        y[j] = (vis >> (16 * (j >> 2) + (j & 3))) & 1 ? x[m][j >> 2][j & 3] * p.scale_log2 : kNegInf;
-        high = fmaxf(high, y[j]);
-      }
-      high = rows_max(high);
-      const int row = wave * MQ + m;
-      const bool pass = high > (ref[m] == kNegInf ? kNegInf : ref[m] + kSlack);
-      const bool any = __any(pass);
-      if (any) {
-        const float next = pass ? high : ref[m];
-        const float fade = ref[m] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(ref[m] - next);
-        ref[m] = next;
-        sum[m] *= fade;
-        if (g == 0) lds.fade[half][row][col] = fade;
-      }
-      if (lane == 0) lds.fading[half][row] = any;
-      const float base = ref[m] == kNegInf ? 0.0f : ref[m];
-      bf16x8 prob, rest;
+      for (int i = 0; i < kPairs; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        y[j] = __builtin_amdgcn_exp2f(y[j] - base);
-        sum[m] += y[j];
-        prob[j] = static_cast<__bf16>(y[j]);
-        if constexpr (kTwo) rest[j] = static_cast<__bf16>(y[j] - static_cast<float>(prob[j]));
-      }
-      lds.prob[half][0][row][lane] = __builtin_bit_cast(u32v4, prob);
-      if constexpr (kTwo) lds.prob[half][1][row][lane] = __builtin_bit_cast(u32v4, rest);
+        for (int j = 0; j < 2; ++j) {
+          const bool there = r < p.rows && 64 * i + 16 * g < a.D;
+          const T8 x = load_any<T8>(there ? src + 128 * i + 32 * g + 16 * j : reinterpret_cast<const char*>(&kNothing));
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            q[m][i][j][e] = static_cast<__bf16>(static_cast<float>(x[e]));
+            if constexpr (kTwo)
+              q_rest[m][i][j][e] = static_cast<__bf16>(static_cast<float>(x[e]) - static_cast<float>(q[m][i][j][e]));
+          }
+        }
+      if (r < p.rows && a.tree_slots) tree_bits[m] = static_cast<uint64_t>(a.tree_mask[spot.b * a.mask_b + t]);
     }
-  };
-
-  f32x4 out[RT][NC];
+    float ref[MQ], sum[MQ];
 #pragma unroll
-  for (int m = 0; m < RT; ++m)
+    for (int m = 0; m < MQ; ++m) ref[m] = kNegInf, sum[m] = 0.0f;
+
+    auto scores = [&](int i, const uint8_t* tile) {
+      f32x4 x[MQ], x1[MQ];  // two sums each: half as long a chain of products
+#pragma unroll
+      for (int m = 0; m < MQ; ++m) x[m] = f32x4{}, x1[m] = f32x4{};
+      const uint8_t* row = tile + (16 * team + col) * kPitch + 16 * g;
+      constexpr int kAhead = 6;  // operands asked for ahead of their products
+      bf16x8 k[kAhead];
+      auto operand = [&](int n) { return *reinterpret_cast<const bf16x8*>(row + (n & 1) * kPlane + 64 * (n >> 1)); };
+#pragma unroll
+      for (int n = 0; n < kAhead; ++n) k[n] = operand(n);
+#pragma unroll
+      for (int n = 0; n < 2 * kPairs; ++n) {
+#pragma unroll
+        for (int m = 0; m < MQ; ++m) {
+          f32x4& sum = n & 1 ? x1[m] : x[m];
+          sum = Mat<__bf16>::mma(k[n % kAhead], q[m][n >> 1][n & 1], sum);
+          if constexpr (kTwo) sum = Mat<__bf16>::mma(k[n % kAhead], q_rest[m][n >> 1][n & 1], sum);
+        }
+        if (n + kAhead < 2 * kPairs) k[n % kAhead] = operand(n + kAhead);
+      }
+      const int at = spot.first + i, half = i & 1;
+      const uint32_t seen = lds.seen[i & 7] >> (16 * team);
+#pragma unroll
+      for (int m = 0; m < MQ; ++m) {
+        const int rt = MQ * hg + m;
+        uint32_t vis = seen;
+        if (at >= spot.main_tiles) vis &= static_cast<uint32_t>(tree_bits[m] >> (kTile * (at - spot.main_tiles) + 16 * team));
+        vis >>= 4 * g;
+        float y[4], high = kNegInf;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          y[e] = (vis >> e) & 1 ? (x[m][e] + x1[m][e]) * p.scale_log2 : kNegInf;
+          high = fmaxf(high, y[e]);
+        }
+        high = rows_max(high);
+        float next = i ? fmaxf(ref[m], lds.ref[half ^ 1][team ^ 1][rt * 16 + col]) : ref[m];
+        if (high > next + kSlack || next == kNegInf) next = ceilf(high);
+        sum[m] *= ref[m] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(ref[m] - next);
+        ref[m] = next;
+        if (g == 0) lds.ref[half][team][rt * 16 + col] = next;
+        const float base = next == kNegInf ? 0.0f : next;
+        B4 prob, rest;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          y[e] = __builtin_amdgcn_exp2f(y[e] - base);
+          sum[m] += y[e];
+          prob[e] = static_cast<__bf16>(y[e]);
+          if constexpr (kTwo) rest[e] = static_cast<__bf16>(y[e] - static_cast<float>(prob[e]));
+        }
+        lds.prob[half][0][team][rt][lane] = __builtin_bit_cast(u32v2, prob);
+        if constexpr (kTwo) lds.prob[half][1][team][rt][lane] = __builtin_bit_cast(u32v2, rest);
+      }
+    };
+
+    if (wave < 2) {
+      Pieces<1> kset[kDepth], vset[SHARED ? 1 : kDepth];
+      begin(kset, vset);
+      __syncthreads();
+      scores(0, lds.k[0]);
+      __syncthreads();
+      run([&](auto odd, int i, int, int next, int after) {
+        scores(i + 1, lds.k[next]);
+        stage(kset, vset, odd, i, after);
+      });
+    } else {  // these two find the rows (both the same ones)
+      int32_t asked = ask(4);
+      __syncthreads();
+      keep(4, asked);
+      asked = ask(5);
+      scores(0, lds.k[0]);
+      __syncthreads();
+      run([&](auto, int i, int, int next, int) {
+        keep(i + 5, asked);
+        asked = ask(i + 6);
+        scores(i + 1, lds.k[next]);
+      });
+    }
+#pragma unroll
+    for (int m = 0; m < MQ; ++m) {
+      sum[m] = rows_sum(sum[m]);
+      if (g == 0) lds.stat[team][(MQ * hg + m) * 16 + col] = f32x2{ref[m], sum[m]};
+    }
+    __syncthreads();
+    return;
+  }
+
+  // ---- sums
+  const int quarter = wave - 4;
+  f32x4 out[RT][NC];
+  float base[RT];
+#pragma unroll
+  for (int m = 0; m < RT; ++m) {
+    base[m] = kNegInf;
 #pragma unroll
     for (int c = 0; c < NC; ++c) out[m][c] = f32x4{};
-  const uint8_t* codes_at = SHARED ? &lds.k[0][0] : &lds.v[0][0];
-  // products of tile i with the wave's channels
-  auto products = [&](int i) {
-    const int at = i % 3, half = i & 1;
-    bf16x8 prob[RT], rest[kTwo ? RT : 1];
+  }
+  auto products = [&](int i, const uint8_t* tile) {
+    const int half = i & 1;
+    constexpr int kParts = kTwo ? 2 : 1;
+    bf16x8 prob[kParts][RT];
+    auto join = [](u32v2 lo, u32v2 hi) { return __builtin_bit_cast(bf16x8, u32v4{lo[0], lo[1], hi[0], hi[1]}); };
+    bool moved = false;
+    float r0[RT], r1[RT];
 #pragma unroll
     for (int m = 0; m < RT; ++m) {
-      if (__builtin_amdgcn_readfirstlane(lds.fading[half][m])) {
-        const float fade = lds.fade[half][m][col];
+      r0[m] = lds.ref[half][0][16 * m + col];
+      r1[m] = lds.ref[half][1][16 * m + col];
+      moved = moved || r0[m] != base[m] || r1[m] != base[m];
 #pragma unroll
-        for (int c = 0; c < NC; ++c) out[m][c] *= fade;
-      }
-      prob[m] = __builtin_bit_cast(bf16x8, lds.prob[half][0][m][lane]);
-      if constexpr (kTwo) rest[m] = __builtin_bit_cast(bf16x8, lds.prob[half][1][m][lane]);
+      for (int k = 0; k < kParts; ++k)
+        prob[k][m] = join(lds.prob[half][k][0][m][lane], lds.prob[half][k][1][m][lane]);
     }
-    // lanes 2 j, 2 j + 1 of 16 stand at the row of the group's key j: 4 g + j, then 16 + 4 g + j - 4
-    const int row = 4 * g + ((col >> 1) & 3) + 16 * (col >> 3);
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      typedef int i32x2 __attribute__((ext_vector_type(2)));
-      typedef __attribute__((address_space(3))) i32x2* Lds2;
-      const int ch = wave * NC + c;
-      const i32x2 w = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-          (Lds2)(codes_at + at * (kTile * kPitch) + place(row, ch) + 8 * (col & 1)));
-      const float* f = SHARED && !kTwo ? &lds.ks[at][ch >> 1][0] : &lds.vs[at][ch >> 1][0];
-      const f32x4 f0 = *reinterpret_cast<const f32x4*>(f + 4 * g), f1 = *reinterpret_cast<const f32x4*>(f + 16 + 4 * g);
-      bf16x8 v;
-      v[0] = static_cast<__bf16>(__builtin_amdgcn_cvt_scalef32_f32_fp8(w[0], f0[0], 0));
-      v[1] = static_cast<__bf16>(__builtin_amdgcn_cvt_scalef32_f32_fp8(w[0], f0[1], 1));
-      v[2] = static_cast<__bf16>(__builtin_amdgcn_cvt_scalef32_f32_fp8(w[0], f0[2], 2));
-      v[3] = static_cast<__bf16>(__builtin_amdgcn_cvt_scalef32_f32_fp8(w[0], f0[3], 3));
-      v[4] = static_cast<__bf16>(__builtin_amdgcn_cvt_scalef32_f32_fp8(w[1], f1[0], 0));
-      v[5] = static_cast<__bf16>(__builtin_amdgcn_cvt_scalef32_f32_fp8(w[1], f1[1], 1));
-      v[6] = static_cast<__bf16>(__builtin_amdgcn_cvt_scalef32_f32_fp8(w[1], f1[2], 2));
-      v[7] = static_cast<__bf16>(__builtin_amdgcn_cvt_scalef32_f32_fp8(w[1], f1[3], 3));
+    if (__any(moved)) {
 #pragma unroll
       for (int m = 0; m < RT; ++m) {
-        out[m][c] = Mat<__bf16>::mma(v, prob[m], out[m][c]);
-        if constexpr (kTwo) out[m][c] = Mat<__bf16>::mma(v, rest[m], out[m][c]);
+        const float next = fmaxf(base[m], fmaxf(r0[m], r1[m])), zero = next == kNegInf ? 0.0f : next;
+        const float fade = __builtin_amdgcn_exp2f(base[m] - zero);
+        const float f0 = __builtin_amdgcn_exp2f(r0[m] - zero), f1 = __builtin_amdgcn_exp2f(r1[m] - zero);
+        base[m] = next;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) out[m][c] *= fade;
+#pragma unroll
+        for (int k = 0; k < kParts; ++k)
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            prob[k][m][e] = static_cast<__bf16>(static_cast<float>(prob[k][m][e]) * (e < 4 ? f0 : f1));
       }
+    }
+    // 16 channels by 4 keys a load: lane (key col / 4, four channels col % 4) of the upper or lower halves
+    const uint8_t* rows = tile + (4 * g + (col >> 2)) * kPitch + kPlane * ((col >> 1) & 1) + 8 * (col & 1) + 16 * (quarter * NC);
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      typedef __attribute__((address_space(3))) s16x4* Lds4;
+      typedef short s16x8 __attribute__((ext_vector_type(8)));
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds4)(rows + 16 * c));
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds4)(rows + 16 * kPitch + 16 * c));
+      const bf16x8 v = __builtin_bit_cast(bf16x8, s16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
+#pragma unroll
+      for (int m = 0; m < RT; ++m)
+#pragma unroll
+        for (int k = 0; k < kParts; ++k) out[m][c] = Mat<__bf16>::mma(v, prob[k][m], out[m][c]);
     }
   };
 
-  // Tile i is brought from memory in step i - 3, laid out in step i - 2, scored
-  // in step i - 1 and multiplied in step i; its slots are found in step i - 5
-  // and written in step i - 4.  A step ends at its barrier.
-  if (steps > 0) {
-    if (tid < 128) lds.slot[tid >> 5][tid & 31] = find(tid >> 5);
-    __syncthreads();
-    bring(0);
-    lay(0);
-    bring(1);
-    __syncthreads();
-    scores(0);
-    lay(1);
-    bring(2);
-    int32_t found = find(4);
-    __syncthreads();
-    for (int i = 0; i < steps; ++i) {
-      lay(i + 2);
-      if (tid < 32) lds.slot[(i + 4) & 7][tid] = found;
-      bring(i + 3);
-      found = find(i + 5);
-      products(i);
-      if (i + 1 < steps) scores(i + 1);
-      __syncthreads();
-    }
-  }
-
-#pragma unroll
-  for (int m = 0; m < MQ; ++m) {
-    sum[m] = rows_sum(sum[m]);
-    if (g == 0) lds.stat[(wave * MQ + m) * 16 + col] = f32x2{ref[m], sum[m]};
-  }
+  Pieces<4> kset[kDepth], vset[SHARED ? 1 : kDepth];
+  begin(kset, vset);
   __syncthreads();
+  __syncthreads();
+  run([&](auto odd, int i, int at, int, int after) {
+    stage(kset, vset, odd, i, after);
+    products(i, SHARED ? lds.k[at] : lds.v[decltype(odd)::value]);
+  });
+  __syncthreads();
+
   const int64_t block = blockIdx.x;
 #pragma unroll
   for (int m = 0; m < RT; ++m) {
     const int r = spot.row0 + 16 * m + col;
     if (r >= p.rows) continue;
-    const f32x2 s = lds.stat[16 * m + col];
+    const f32x2 s0 = lds.stat[0][16 * m + col], s1 = lds.stat[1][16 * m + col];
+    const float zero = base[m] == kNegInf ? 0.0f : base[m];
+    const f32x2 s = {base[m], s0[1] * __builtin_amdgcn_exp2f(s0[0] - zero) + s1[1] * __builtin_amdgcn_exp2f(s1[0] - zero)};
+    const bool first = quarter == 0 && g == 0;
     if (p.splits > 1) {
       const int64_t at = block * (16 * RT) + 16 * m + col;
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        const int ch = 16 * (wave * NC + c) + 4 * g;
+        const int ch = 16 * (quarter * NC + c) + 4 * g;
         if (ch < a.Dv) store_any(p.part + at * a.Dv + ch, out[m][c]);
       }
-      if (wave == 0 && g == 0) p.stat[at] = s;
+      if (first) p.stat[at] = s;
     } else {
       int t, h;
       attend_row(p, spot, r, &t, &h);
@@ -339,13 +383,13 @@ __global__ __launch_bounds__(kAttendThreads) void attend_wide_kernel(AttendParam
       typedef T V4 __attribute__((ext_vector_type(4)));
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        const int ch = 16 * (wave * NC + c) + 4 * g;
+        const int ch = 16 * (quarter * NC + c) + 4 * g;
         V4 y;
 #pragma unroll
         for (int e = 0; e < 4; ++e) y[e] = static_cast<T>(out[m][c][e] * inv);
         if (ch < a.Dv) store_any(static_cast<T*>(a.out) + at * a.Dv + ch, y);
       }
-      if (wave == 0 && g == 0) a.lse[at] = attend_lse(s[0], s[1]);
+      if (first) a.lse[at] = attend_lse(s[0], s[1]);
     }
   }
 }
@@ -353,20 +397,20 @@ __global__ __launch_bounds__(kAttendThreads) void attend_wide_kernel(AttendParam
 template <class T, int RT, int NC, bool SHARED>
 void launch(const AttendParams& p, hipStream_t s) {
   const uint32_t grid = static_cast<uint32_t>(static_cast<int64_t>(p.units) * p.row_groups * p.splits);
-  hipLaunchKernelGGL((attend_wide_kernel<T, RT, NC, SHARED>), dim3(grid), dim3(kAttendThreads),
-                     sizeof(WideLds<RT, NC, SHARED, Mat<T>::kRowScale>), s, p);
+  hipLaunchKernelGGL((attend_wide_kernel<T, RT, NC, SHARED>), dim3(grid), dim3(kThreads),
+                     sizeof(WideLds<RT, SHARED, Mat<T>::kRowScale>), s, p);
 }
 
 }  // namespace
 
 void launch_attend_wide(const AttendParams& p, int row_tiles, bool shared, hipStream_t s) {
   const bool bf16 = p.a.dtype == ETS_BF16;
-  if (row_tiles == 8) {
-    shared ? launch<__bf16, 8, 8, true>(p, s) : launch<__bf16, 8, 8, false>(p, s);
+  if (row_tiles == 4) {
+    launch<__bf16, 4, 8, true>(p, s);
   } else if (shared) {
-    bf16 ? launch<__bf16, 4, 8, true>(p, s) : launch<_Float16, 4, 8, true>(p, s);
+    bf16 ? launch<__bf16, 2, 8, true>(p, s) : launch<_Float16, 2, 8, true>(p, s);
   } else {
-    bf16 ? launch<__bf16, 4, 9, false>(p, s) : launch<_Float16, 4, 9, false>(p, s);
+    bf16 ? launch<__bf16, 2, 9, false>(p, s) : launch<_Float16, 2, 9, false>(p, s);
   }
 }
 
