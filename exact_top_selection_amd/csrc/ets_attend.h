@@ -13,6 +13,9 @@ constexpr int kAttendTile = 32;  // keys of a step
 constexpr float kNegInf = -__builtin_inff();
 constexpr float kLn2 = 0.69314718055994530942f;
 
+// Read in the place of a row that is not there (576 zeros).
+static __device__ const u32v4 kNothing[ETS_MAX_HEAD_DIM / 16] = {};
+
 struct AttendParams {
   ets_attend_args a;
   int G;             // query heads of a cache head
@@ -20,19 +23,27 @@ struct AttendParams {
   int units;         // lists: (b, t, hk) or (b, hk)
   int row_groups;    // of a unit
   int splits;        // workgroups that share a list
+  int heads;         // heads of a workgroup: 1, 2 or 4
   int tree_tiles;
   float scale_log2;  // log2(e) / sqrt(D)
-  FastDiv by_page, by_heads, by_tokens, by_groups, by_splits, by_G, by_rows, by_lanes, by_unit_rows;
-  int join_groups, join_rows;  // the join: shares of the splits, rows of a workgroup
+  FastDiv by_page, by_heads, by_tokens, by_groups, by_splits, by_G, by_rows, by_inner, by_lanes, by_parts, by_unit_rows;
+  int join_lanes, join_groups, join_parts;  // the join: lanes of a part of a row, shares of its splits, parts of a workgroup
   int group_rows;    // query rows of a workgroup, a multiple of 16
   float* part;       // [unit][row group][split][group_rows][Dv] sums
   f32x2* stat;       // [unit][row group][split][group_rows] (reference, sum)
 };
 
 // Where a workgroup stands: its list, its query rows, its share of the keys.
-// Blocks are numbered split fastest, then row group, then unit.
+// Workgroups are dealt out to the 8 XCDs in turn.  Those that read the same
+// slots (the row groups and the heads of one share: 128 bytes of scales hold
+// all heads of a slot, and often several slots) follow each other on one XCD,
+// so that its L2 brings a line once: block = ((share / 8 * heads + head) *
+// groups + group) * 8 + share % 8, where a "head" is what one workgroup takes.
 struct AttendSpot {
-  int split, row0, hk, b, t;  // t: the token of a selected list, 0 for paged ones
+  bool live;
+  int split, group, row0, b, t;  // t: the token of a selected list, 0 for paged ones
+  int hk;                        // the first of its heads
+  uint32_t bt;
   bool paged;
   int n, main_tiles, tiles, first, last;
   uint64_t tree;  // drafted tokens that stand in the list
@@ -40,15 +51,19 @@ struct AttendSpot {
 __device__ __forceinline__ AttendSpot attend_spot(const AttendParams& p) {
   const ets_attend_args& a = p.a;
   AttendSpot s;
-  const uint32_t ug = div_by(blockIdx.x, p.by_splits);
-  s.split = static_cast<int>(blockIdx.x - ug * p.splits);
-  const uint32_t unit = div_by(ug, p.by_groups);
-  s.row0 = static_cast<int>(ug - unit * p.row_groups) * p.group_rows;
   s.paged = a.slots == nullptr;
-  const uint32_t bt = div_by(unit, p.by_heads);
-  s.hk = static_cast<int>(unit - bt * a.Hkv);
+  const uint32_t y = blockIdx.x >> 3, eight = div_by(y, p.by_inner), in = y - eight * p.by_inner.d;
+  const uint32_t share = eight * 8 + (blockIdx.x & 7), bt = div_by(share, p.by_splits);
+  s.bt = bt;
+  s.split = static_cast<int>(share - bt * p.splits);
+  const int heads = static_cast<int>(div_by(in, p.by_groups));
+  s.hk = heads * p.heads;
+  s.group = static_cast<int>(in) - heads * p.row_groups;
+  s.row0 = s.group * p.group_rows;
+  s.live = bt * a.Hkv < static_cast<uint32_t>(p.units);
   s.b = s.paged ? static_cast<int>(bt) : static_cast<int>(div_by(bt, p.by_tokens));
   s.t = s.paged ? 0 : static_cast<int>(bt) - s.b * a.T;
+  if (!s.live) return s;
   s.n = s.paged ? min(max(a.seq_lens[s.b], 0), a.L) : a.K;
   s.main_tiles = (s.n + kAttendTile - 1) / kAttendTile;
   s.tiles = s.main_tiles + p.tree_tiles;
@@ -72,7 +87,6 @@ __device__ __forceinline__ bool attend_there(const AttendSpot& s, int i, int at)
   return i < s.main_tiles ? j < s.n : i < s.tiles && (s.tree >> (k & 63) & 1);
 }
 __device__ __forceinline__ int32_t attend_ask(const AttendParams& p, const AttendSpot& s, int i, int at) {
-  typedef __attribute__((address_space(1))) const int32_t* Global4;
   const ets_attend_args& a = p.a;
   const int j = i * kAttendTile + at, k = (i - s.main_tiles) * kAttendTile + at;
   const uint64_t list = s.paged ? reinterpret_cast<uint64_t>(a.page_table + s.b * a.pt_b)
@@ -81,7 +95,7 @@ __device__ __forceinline__ int32_t attend_ask(const AttendParams& p, const Atten
   const uint32_t page = div_by(static_cast<uint32_t>(j) & 0x7fffffffu, p.by_page);
   uint64_t from = i < s.main_tiles ? list + 4ull * (s.paged ? page : static_cast<uint32_t>(j)) : tree + 4ull * (k & 63);
   from = attend_there(s, i, at) ? from : reinterpret_cast<uint64_t>(a.q) & ~3ull;
-  return *reinterpret_cast<Global4>(from);
+  return load_global<int32_t>(from);
 }
 __device__ __forceinline__ int32_t attend_slot(const AttendParams& p, const AttendSpot& s, int i, int at, int32_t asked) {
   const int j = i * kAttendTile + at;
@@ -91,10 +105,15 @@ __device__ __forceinline__ int32_t attend_slot(const AttendParams& p, const Atte
   return attend_there(s, i, at) && asked >= 0 && slot < p.a.S ? static_cast<int32_t>(slot) : -1;
 }
 
-// (token, query head) of a workgroup's row r.
-__device__ __forceinline__ void attend_row(const AttendParams& p, const AttendSpot& s, int r, int* t, int* h) {
+// (token, query head) of row r of head hk.
+__device__ __forceinline__ void attend_row(const AttendParams& p, const AttendSpot& s, int hk, int r, int* t, int* h) {
   *t = s.paged ? static_cast<int>(div_by(r, p.by_G)) : s.t;
-  *h = s.hk * p.G + (s.paged ? r - *t * p.G : r);
+  *h = hk * p.G + (s.paged ? r - *t * p.G : r);
+}
+
+// Place of head hk's partial sums: [unit][row group][split].
+__device__ __forceinline__ int64_t attend_place(const AttendParams& p, const AttendSpot& s, int hk) {
+  return ((static_cast<int64_t>(s.bt) * p.a.Hkv + hk) * p.row_groups + s.group) * p.splits + s.split;
 }
 
 __device__ __forceinline__ float attend_lse(float reference, float sum) {
@@ -102,6 +121,11 @@ __device__ __forceinline__ float attend_lse(float reference, float sum) {
 }
 __device__ __forceinline__ float attend_inverse(float sum) {
   return sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+}
+
+inline uint32_t attend_grid(const AttendParams& p) {
+  const int64_t shares = static_cast<int64_t>(p.units / p.a.Hkv) * p.splits;
+  return static_cast<uint32_t>((shares + 7) / 8 * 8 * (p.a.Hkv / p.heads) * p.row_groups);
 }
 
 // The launch of the kernel for heads over 256 channels (ets_attend_wide.hip);

@@ -10,6 +10,20 @@ constexpr int kThreads = kAttendThreads;
 constexpr int kWaves = kAttendWaves;
 constexpr int kTile = kAttendTile;
 
+constexpr int kChunk = 16;  // tiles whose slots are brought at a time
+
+// Keeps what is made of loaded values behind this point: made earlier, it would wait for the load there.
+template <class V, int A, int B>
+__device__ __forceinline__ void hold(V (&x)[A][B]) {
+#pragma unroll
+  for (int i = 0; i < A; ++i)
+#pragma unroll
+    for (int j = 0; j < B; ++j) asm volatile("" : "+v"(x[i][j]));
+}
+
+// Bytes of half a decoded row of 64 nv channels.
+constexpr int value_plane(int nv) { return 64 * nv + (nv % 4 ? 0 : 64); }
+
 // One wave goes over its tiles of 32 keys alone, with the running largest
 // score and sum of the softmax, and the four waves of a workgroup join at the
 // end.
@@ -32,21 +46,26 @@ constexpr int kTile = kAttendTile;
 // the errors of different keys are independent, and the result is rounded to
 // 8 bits anyway).
 template <class T, int NP, int NV, int MT>
-__global__ __launch_bounds__(kThreads) void attend_kernel(AttendParams p) {
+__global__ __launch_bounds__(kThreads, MT == 1 && NP <= 2 ? 3 : 1) void attend_kernel(AttendParams p) {
   typedef Mat<T> M;
   typedef typename M::V8 V8;
-  constexpr int W = (NP + 1) / 2, WV = (NV + 1) / 2;
-  constexpr int kPitch = NV * 128 + 32;  // bytes of a row of values in LDS
-  constexpr bool kTwo = M::kRowScale;    // fp16: two-part probabilities
+  // decoded values in LDS: rows of two planes, the lower and the upper halves of
+  // their 16-channel pieces; rows lie 4 banks apart, planes not a multiple of 64
+  constexpr int kPlane = value_plane(NV), kPitch = 2 * kPlane + 16;
+  constexpr bool kTwo = M::kRowScale;  // fp16: two-part probabilities
   extern __shared__ __align__(16) char lds[];
   const ets_attend_args& a = p.a;
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, g = lane >> 4;
   char* values = lds + wave * (kTile * kPitch);
-  f32x2* stats = reinterpret_cast<f32x2*>(lds + kWaves * kTile * kPitch);  // [wave][16 MT]
+  f32x2* stats = reinterpret_cast<f32x2*>(lds + kWaves * kTile * kPitch);  // [wave][16 MT], then [head][16]
+  int32_t* slots = reinterpret_cast<int32_t*>(stats + kWaves * 16 * (MT + 1));  // [3][kChunk * kTile]
 
   const AttendSpot spot = attend_spot(p);
-  const int b = spot.b, hk = spot.hk, row0 = spot.row0, main_tiles = spot.main_tiles, last = spot.last;
+  if (!spot.live) return;
+  const int b = spot.b, row0 = spot.row0, main_tiles = spot.main_tiles, last = spot.last;
+  // a wave's head, and the team of waves that share the head's keys
+  const int hk = spot.hk + wave % p.heads, team = wave / p.heads, teams = kWaves / p.heads;
 
   // queries: lane (head col, row g) holds channels 64 i + 16 g + 0..7, 8..15
   V8 q[MT][NP][2];
@@ -55,7 +74,7 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(AttendParams p) {
   for (int m = 0; m < MT; ++m) {
     const int r = row0 + 16 * m + col;
     int t, h;
-    attend_row(p, spot, r, &t, &h);
+    attend_row(p, spot, hk, r, &t, &h);
     const char* src = static_cast<const char*>(a.q) + 2 * (b * a.q_b + t * a.q_t + h * a.q_h);
     tree_bits[m] = 0;
 #pragma unroll
@@ -75,40 +94,66 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(AttendParams p) {
     }
   }
 
-  // slot of the key that this lane loads: 16 s + col of tile i
-  auto slot_of = [&](int i, int s) { return attend_slot(p, spot, i, 16 * s + col, attend_ask(p, spot, i, 16 * s + col)); };
+  // A tile's rows on their way: lane (key col of either half, row g) brings codes 64 i + 16 g .. + 15 and their
+  // scale byte.  Rows and channels that are not there come from kNothing, without a branch.
+  const uint64_t nothing = reinterpret_cast<uint64_t>(&kNothing[0]);
+  const uint64_t kc = reinterpret_cast<uint64_t>(a.k_codes + hk * a.k_h + 16 * g);
+  const uint64_t ks = reinterpret_cast<uint64_t>(a.k_scales + hk * a.ks_h + (g >> 1));
+  const uint64_t vc = reinterpret_cast<uint64_t>(a.v_codes + hk * a.v_h + 16 * g);
+  const uint64_t vs = reinterpret_cast<uint64_t>(a.v_scales + hk * a.vs_h + (g >> 1));
+  const uint32_t k_row = static_cast<uint32_t>(a.k_s), ks_row = static_cast<uint32_t>(a.ks_s);
+  const uint32_t v_row = static_cast<uint32_t>(a.v_s), vs_row = static_cast<uint32_t>(a.vs_s);
+  struct Rows {
+    u32v4 k[2][NP], v[2][NV];
+    uint32_t kbyte[2][NP], vbyte[2][NV];
+    uint32_t seen;  // keys that are there
+  };
 
-  const int nbk = a.D / kCacheBlock, nbv = a.Dv / kCacheBlock;
-  const uint8_t* kc = a.k_codes + hk * a.k_h + 16 * g;
-  const uint8_t* ks = a.k_scales + hk * a.ks_h;
-  const uint8_t* vc = a.v_codes + hk * a.v_h + 16 * g;
-  const uint8_t* vs = a.v_scales + hk * a.vs_h;
-  u32v4 kraw[2][NP], vraw[2][NV];
-  uint32_t ksc[2][W], vsc[2][WV];
-  uint32_t seen = 0;  // keys of the fetched tile that are inside the cache
-  auto fetch = [&](const int32_t (&slot)[2]) {
+  // Slots come through LDS, kChunk tiles at a time, asked for two chunks ahead
+  // by all lanes, so that the steps' own loads stay in one straight line.
+  constexpr int kEach = kChunk * kTile / kThreads;
+  int32_t asked[kEach];
+  auto ask = [&](int c) {
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+      const int key = threadIdx.x + j * kThreads;
+      asked[j] = attend_ask(p, spot, spot.first + c * kChunk + key / kTile, key % kTile);
+    }
+  };
+  auto keep = [&](int c) {
+    int32_t* to = slots + c % 3 * (kChunk * kTile);
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+      const int key = threadIdx.x + j * kThreads, tile = spot.first + c * kChunk + key / kTile;
+      to[key] = tile < last ? attend_slot(p, spot, tile, key % kTile, asked[j]) : -1;
+    }
+  };
+  auto fetch = [&](Rows& rows, int i) {  // tile i of the workgroup's share
+    const int32_t* from = slots + i / kChunk % 3 * (kChunk * kTile) + i % kChunk * kTile + col;
+    const int32_t slot[2] = {from[0], from[16]};
     const uint64_t s0 = __ballot(slot[0] >= 0), s1 = __ballot(slot[1] >= 0);
-    seen = static_cast<uint32_t>(s0 & 0xffff) | static_cast<uint32_t>(s1 & 0xffff) << 16;
+    rows.seen = static_cast<uint32_t>(s0 & 0xffff) | static_cast<uint32_t>(s1 & 0xffff) << 16;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
+      const bool there = slot[s] >= 0;
+      const uint64_t at = static_cast<uint32_t>(slot[s]);
+      // formed first and chosen then: an expression inside the choice would become a branch
+      const uint64_t k0 = kc + at * k_row, k1 = ks + at * ks_row, v0 = vc + at * v_row, v1 = vs + at * vs_row;
+      const uint64_t k = there ? k0 : nothing, kb = there ? k1 : nothing;
+      const uint64_t v = there ? v0 : nothing, vb = there ? v1 : nothing;
 #pragma unroll
-      for (int i = 0; i < NP; ++i) kraw[s][i] = u32v4{0, 0, 0, 0};
+      for (int i = 0; i < NP; ++i) {
+        const bool in = 64 * i + 16 * g < a.D;
+        const uint64_t c = k + 64 * i, b = kb + 2 * i;
+        rows.k[s][i] = load_global<u32v4>(in ? c : nothing);
+        rows.kbyte[s][i] = load_global<uint8_t>(in ? b : nothing);
+      }
 #pragma unroll
-      for (int i = 0; i < W; ++i) ksc[s][i] = 0;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) vraw[s][i] = u32v4{0, 0, 0, 0};
-#pragma unroll
-      for (int i = 0; i < WV; ++i) vsc[s][i] = 0;
-      if (slot[s] >= 0) {
-        const int64_t at = slot[s];
-#pragma unroll
-        for (int i = 0; i < NP; ++i)
-          if (64 * i + 16 * g < a.D) kraw[s][i] = load_any<u32v4>(kc + at * a.k_s + 64 * i);
-        load_scales<W>(ksc[s], ks + at * a.ks_s, nbk);
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-          if (64 * i + 16 * g < a.Dv) vraw[s][i] = load_any<u32v4>(vc + at * a.v_s + 64 * i);
-        load_scales<WV>(vsc[s], vs + at * a.vs_s, nbv);
+      for (int i = 0; i < NV; ++i) {
+        const bool in = 64 * i + 16 * g < a.Dv;
+        const uint64_t c = v + 64 * i, b = vb + 2 * i;
+        rows.v[s][i] = load_global<u32v4>(in ? c : nothing);
+        rows.vbyte[s][i] = load_global<uint8_t>(in ? b : nothing);
       }
     }
   };
@@ -122,30 +167,28 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(AttendParams p) {
     for (int c = 0; c < 4 * NV; ++c) out[m][c] = f32x4{};
   }
 
-  int tile = spot.first + wave;
-  int32_t slot[2] = {-1, -1};
-  if (tile < last) {
-    slot[0] = slot_of(tile, 0), slot[1] = slot_of(tile, 1);
-    fetch(slot);
-    slot[0] = slot_of(tile + kWaves, 0), slot[1] = slot_of(tile + kWaves, 1);
-  }
-  for (; tile < last; tile += kWaves) {
+  auto work = [&](Rows& now, int step) {  // one tile; its rows' registers are asked to be filled again
+    const int tile = spot.first + step;
     // keys to operands, values to LDS
     f32x4 score[MT][2];
     float row_scale[2];
-    const uint32_t seen_now = seen;
+    const uint32_t seen_now = now.seen;
+    hold(now.k), hold(now.kbyte);
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      const uint32_t r = M::kRowScale ? scales_max<W>(ksc[s]) : 0;
+      uint32_t r = 0;
+      if constexpr (M::kRowScale) {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) r = max(r, now.kbyte[s][i]);
+        r = __float_as_uint(rows_max(__uint_as_float(r << 23))) >> 23;  // bytes as powers of two keep their order
+      }
       row_scale[s] = __uint_as_float(r << 23);
 #pragma unroll
       for (int m = 0; m < MT; ++m) score[m][s] = f32x4{};
-      char* dst = values + (16 * s + col) * kPitch + 32 * g;
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
-        const uint32_t byte = byte_of(ksc[s][i / 2], 16 * (i & 1) + 8 * (g >> 1));
-        const float f = M::scale(byte, r);
-        const u32v4 c = kraw[s][i];
+        const float f = M::scale(now.kbyte[s][i], r);
+        const u32v4 c = now.k[s][i];
         const V8 k0 = M::keys(c[0], c[1], f), k1 = M::keys(c[2], c[3], f);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
@@ -153,19 +196,21 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(AttendParams p) {
           score[m][s] = M::mma(k1, q[m][i][1], score[m][s]);
         }
       }
+    }
+    hold(now.v), hold(now.vbyte);
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      char* dst = values + (16 * s + col) * kPitch + 16 * g;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const float f = __uint_as_float(byte_of(vsc[s][i / 2], 16 * (i & 1) + 8 * (g >> 1)) << 23);
-        const u32v4 c = vraw[s][i];
-        store_any(__builtin_assume_aligned(dst + 128 * i, 16), codes_bf16(c[0], c[1], f));
-        store_any(__builtin_assume_aligned(dst + 128 * i + 16, 16), codes_bf16(c[2], c[3], f));
+        const float f = __uint_as_float(now.vbyte[s][i] << 23);
+        const u32v4 c = now.v[s][i];
+        *reinterpret_cast<bf16x8*>(dst + 64 * i) = codes_bf16(c[0], c[1], f);
+        *reinterpret_cast<bf16x8*>(dst + kPlane + 64 * i) = codes_bf16(c[2], c[3], f);
       }
     }
-    // the next tile's rows are on their way while this one is worked on
-    if (tile + kWaves < last) {
-      fetch(slot);
-      slot[0] = slot_of(tile + 2 * kWaves, 0), slot[1] = slot_of(tile + 2 * kWaves, 1);
-    }
+    // the next tile's rows are on their way while this one is worked on; past the end they are zeros
+    fetch(now, step + teams);
     if constexpr (M::kRowScale) {
 #pragma unroll
       for (int s = 0; s < 2; ++s)
@@ -181,7 +226,7 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(AttendParams p) {
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       uint32_t vis = seen_now;
-      if (tile >= main_tiles) vis &= static_cast<uint32_t>(tree_bits[m] >> (kTile * (tile - main_tiles)));
+      if (tile >= main_tiles) vis &= static_cast<uint32_t>(tree_bits[m] >> (kTile * (tile - main_tiles) & 63));
       vis >>= 4 * g;  // bits 0..3: keys 4 g + e; bits 16..19: keys 16 + 4 g + e
       float x[8], high = kNegInf;
 #pragma unroll
@@ -208,12 +253,12 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(AttendParams p) {
       }
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    const char* src = values + (4 * g + (col >> 2)) * kPitch + 8 * (col & 3);
+    const char* src = values + (4 * g + (col >> 2)) * kPitch + kPlane * ((col >> 1) & 1) + 8 * (col & 1);
 #pragma unroll
     for (int c = 0; c < 4 * NV; ++c) {
       typedef __attribute__((address_space(3))) s16x4* Lds4;
-      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds4)(src + 32 * c));
-      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds4)(src + 16 * kPitch + 32 * c));
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds4)(src + 16 * c));
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds4)(src + 16 * kPitch + 16 * c));
       typedef short s16x8 __attribute__((ext_vector_type(8)));
       const bf16x8 v = __builtin_bit_cast(bf16x8, s16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
 #pragma unroll
@@ -223,6 +268,26 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(AttendParams p) {
       }
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  };
+
+  // Every wave takes as many steps (the barriers are shared); those past the end see nothing.
+  const int steps = last - spot.first;
+  if (steps > 0) {
+    ask(0);
+    keep(0);
+    ask(1);
+    __syncthreads();
+    Rows rows;
+    fetch(rows, team);
+    hold(rows.kbyte), hold(rows.vbyte);  // else the loop carries 8-bit values and widens them as soon as they are loaded
+    for (int step = team; step < steps + team; step += teams) {
+      if (step % kChunk == team) {
+        keep(step / kChunk + 1);
+        ask(step / kChunk + 2);
+        __syncthreads();
+      }
+      work(rows, step);
+    }
   }
 
   // join the waves
@@ -232,72 +297,75 @@ __global__ __launch_bounds__(kThreads) void attend_kernel(AttendParams p) {
     if (g == 0) stats[(wave * MT + m) * 16 + col] = f32x2{top[m], sum[m]};
   }
   __syncthreads();
-  const int64_t block = blockIdx.x;
   const int dv = a.Dv;
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
-    float high = kNegInf, total = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) high = fmaxf(high, stats[(w * MT + m) * 16 + col][0]);
-    const float base = high == kNegInf ? 0.0f : high;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      const f32x2 s = stats[(w * MT + m) * 16 + col];
-      total += s[1] * __builtin_amdgcn_exp2f(s[0] - base);
-    }
-    const float fade = __builtin_amdgcn_exp2f(top[m] - base);
+    // over the waves of the same head: wave % heads, that plus heads, ...
+    auto joined = [&](int of) {
+      float high = kNegInf, total = 0.0f;
+      for (int w = of; w < kWaves; w += p.heads) high = fmaxf(high, stats[(w * MT + m) * 16 + col][0]);
+      const float base = high == kNegInf ? 0.0f : high;
+      for (int w = of; w < kWaves; w += p.heads) {
+        const f32x2 s = stats[(w * MT + m) * 16 + col];
+        total += s[1] * __builtin_amdgcn_exp2f(s[0] - base);
+      }
+      return f32x2{high, total};
+    };
+    const f32x2 of_head = joined(wave % p.heads);
+    const float fade = __builtin_amdgcn_exp2f(top[m] - (of_head[0] == kNegInf ? 0.0f : of_head[0]));
     // the wave's sums, [head][64 NV] floats, over its own values
     f32x4* mine = reinterpret_cast<f32x4*>(values) + col * (16 * NV) + g;
 #pragma unroll
     for (int c = 0; c < 4 * NV; ++c) mine[4 * c] = out[m][c] * fade;
-    if (wave == 0 && g == 0) stats[(kWaves * MT + m) * 16 + col] = f32x2{high, total};
+    f32x2* final = stats + kWaves * MT * 16;  // [head][16]
+    if (team == 0 && g == 0) final[(wave % p.heads) * 16 + col] = of_head;
     __syncthreads();
-    for (int i = threadIdx.x; i < 16 * 16 * NV; i += kThreads) {
-      const int head = i / (16 * NV), c = (i - head * (16 * NV)) * 4;
-      const int r = row0 + 16 * m + head;
+    for (int i = threadIdx.x; i < p.heads * 256 * NV; i += kThreads) {
+      const int of = i / (256 * NV), at = i - of * (256 * NV), row = at / (16 * NV), c = (at - row * (16 * NV)) * 4;
+      const int r = row0 + 16 * m + row;
       if (r >= p.rows || c >= dv) continue;
       f32x4 v = {};
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w)
-        v += reinterpret_cast<const f32x4*>(lds + w * (kTile * kPitch))[i];
-      const f32x2 s = stats[(kWaves * MT + m) * 16 + head];
+      for (int w = of; w < kWaves; w += p.heads)
+        v += reinterpret_cast<const f32x4*>(lds + w * (kTile * kPitch))[at];
+      const f32x2 s = final[of * 16 + row];
       if (p.splits > 1) {
-        const int64_t at = block * (16 * MT) + 16 * m + head;
-        store_any(p.part + at * dv + c, v);
-        if (c == 0) p.stat[at] = s;
+        const int64_t place = attend_place(p, spot, spot.hk + of) * (16 * MT) + 16 * m + row;
+        store_any(p.part + place * dv + c, v);
+        if (c == 0) p.stat[place] = s;
       } else {
         int t, h;
-        attend_row(p, spot, r, &t, &h);
-        const int64_t at = (static_cast<int64_t>(b) * a.T + t) * a.Hq + h;
+        attend_row(p, spot, spot.hk + of, r, &t, &h);
+        const int64_t place = (static_cast<int64_t>(b) * a.T + t) * a.Hq + h;
         const float inv = attend_inverse(s[1]);
         typedef T V4 __attribute__((ext_vector_type(4)));
         V4 y;
 #pragma unroll
         for (int e = 0; e < 4; ++e) y[e] = static_cast<T>(v[e] * inv);
-        store_any(static_cast<T*>(a.out) + at * dv + c, y);
-        if (c == 0) a.lse[at] = attend_lse(s[0], s[1]);
+        store_any(static_cast<T*>(a.out) + place * dv + c, y);
+        if (c == 0) a.lse[place] = attend_lse(s[0], s[1]);
       }
     }
     __syncthreads();
   }
 }
 
-// Joins the splits of a list.  A lane stands at four channels of one row; Dv / 4
-// lanes by `groups` shares of the splits take the row, and a workgroup as many
-// rows as it has lanes for.
+// Joins the splits of a list.  A lane stands at four channels of one row;
+// join_lanes of them by join_groups shares of the splits take a part of the
+// row, and a workgroup as many parts as it has lanes for.
 template <class T>
 __global__ __launch_bounds__(kThreads) void join_kernel(AttendParams p) {
   const ets_attend_args& a = p.a;
   __shared__ f32x4 sums[kThreads];
   __shared__ f32x2 joined[kThreads];
-  const int lanes = a.Dv / 4;
-  const int slot = static_cast<int>(div_by(threadIdx.x, p.by_lanes));  // row and share
-  const int ch = 4 * (static_cast<int>(threadIdx.x) - slot * lanes);
-  const int my_row = slot / p.join_groups, mine = slot - my_row * p.join_groups;
-  const int64_t index = static_cast<int64_t>(blockIdx.x) * p.join_rows + my_row;
-  const bool live = my_row < p.join_rows && index < static_cast<int64_t>(p.units) * p.rows;
-  const uint32_t unit = live ? div_by(static_cast<uint32_t>(index), p.by_unit_rows) : 0;
-  const int r = live ? static_cast<int>(index - static_cast<int64_t>(unit) * p.rows) : 0;
+  const int lanes = p.join_lanes;
+  const int slot = static_cast<int>(div_by(threadIdx.x, p.by_lanes));  // part and share
+  const int my_part = slot / p.join_groups, mine = slot - my_part * p.join_groups;
+  const int64_t index = static_cast<int64_t>(blockIdx.x) * p.join_parts + my_part;
+  const int64_t row_index = static_cast<int64_t>(div_by(static_cast<uint32_t>(index), p.by_parts));
+  const int ch = 4 * (static_cast<int>(index - row_index * p.by_parts.d) * lanes + static_cast<int>(threadIdx.x) - slot * lanes);
+  const bool live = my_part < p.join_parts && row_index < static_cast<int64_t>(p.units) * p.rows;
+  const uint32_t unit = live ? div_by(static_cast<uint32_t>(row_index), p.by_unit_rows) : 0;
+  const int r = live ? static_cast<int>(row_index - static_cast<int64_t>(unit) * p.rows) : 0;
   const int group = static_cast<int>(div_by(r, p.by_rows)), in_group = r - group * p.group_rows;
   const int64_t at0 = (static_cast<int64_t>(unit) * p.row_groups + group) * p.splits * p.group_rows + in_group;
   float high = kNegInf, total = 0.0f;
@@ -391,12 +459,22 @@ ets_status make_plan(const ets_attend_args* a, Plan* plan) {
   p.tree_tiles = a->tree_slots ? (a->T + kTile - 1) / kTile : 0;
   const int tiles = ((paged ? a->L : a->K) + kTile - 1) / kTile + p.tree_tiles;
   const int64_t lists = static_cast<int64_t>(p.units) * p.row_groups;
-  // enough workgroups for two a compute unit (one of the wide kernel's), each wave with a tile at least
-  int64_t splits = ((plan->width == 9 ? 1 : 2) * static_cast<int64_t>(cu) + lists - 1) / lists;
-  const int64_t cap = plan->width == 9 ? (tiles + 3) / 4 : (tiles + kWaves - 1) / kWaves;
+  // workgroups to fill the device with: a compute unit holds one of the wide kernel's and up to three of the
+  // narrow one's, but two read faster than three (8 sequences of 32768: 134 us against 145)
+  const int64_t room = static_cast<int64_t>(cu) * (plan->width == 9 ? 1 : 2);
+  // Heads of one slot lie next to each other in memory: a workgroup of the narrow
+  // kernel takes up to 4, a wave each, so that a slot's lines are read together (16
+  // sequences of 7 tokens, 1024 slots: 69 us against 80 with one).  Where a wave has
+  // few tiles, the 4 times as many splits cost more at their join (one sequence of
+  // 32771: 35 us against 31).
+  p.heads = plan->width == 9 || tiles * lists <= 8 * room * kWaves ? 1 : a->Hkv % 4 == 0 ? 4 : a->Hkv % 2 == 0 ? 2 : 1;
+  const int64_t groups = lists / p.heads;
+  // each wave with a tile at least
+  int64_t splits = (room + groups - 1) / groups;
+  const int64_t cap = plan->width == 9 ? (tiles + 3) / 4 : (tiles + kWaves / p.heads - 1) / (kWaves / p.heads);
   splits = splits > cap ? cap : splits;
   p.splits = static_cast<int>(splits < 1 ? 1 : splits);
-  if (lists * p.splits > INT32_MAX / 16) return ETS_ERR_INVALID_ARG;
+  if (lists * (p.splits + 8) > INT32_MAX / 16) return ETS_ERR_INVALID_ARG;
   p.scale_log2 = static_cast<float>(1.4426950408889634074 / __builtin_sqrt(static_cast<double>(a->D)));
   p.by_page = fast_div(paged ? a->page_size : 1);
   p.by_heads = fast_div(a->Hkv);
@@ -404,11 +482,15 @@ ets_status make_plan(const ets_attend_args* a, Plan* plan) {
   p.by_groups = fast_div(p.row_groups);
   p.by_splits = fast_div(p.splits);
   p.by_G = fast_div(p.G);
+  p.by_inner = fast_div(a->Hkv / p.heads * p.row_groups);
   p.by_rows = fast_div(p.group_rows);
-  const int lanes = a->Dv / 4;
-  p.join_groups = kThreads / lanes < p.splits / 4 ? kThreads / lanes : p.splits / 4 > 1 ? p.splits / 4 : 1;
-  p.join_rows = kThreads / (lanes * p.join_groups);
-  p.by_lanes = fast_div(lanes);
+  // the join: whole rows to a workgroup, or 32-channel parts where there are few rows with many splits
+  p.join_lanes = static_cast<int64_t>(p.units) * p.rows < 2 * cu && p.splits > 16 ? 8 : a->Dv / 4;
+  const int most_groups = kThreads / p.join_lanes;
+  p.join_groups = p.splits / 4 < most_groups ? (p.splits / 4 > 1 ? p.splits / 4 : 1) : most_groups;
+  p.join_parts = kThreads / (p.join_lanes * p.join_groups);
+  p.by_lanes = fast_div(p.join_lanes);
+  p.by_parts = fast_div(a->Dv / 4 / p.join_lanes);
   p.by_unit_rows = fast_div(p.rows);
   if (p.splits > 1) plan->bytes = static_cast<size_t>(lists) * p.splits * 16 * plan->mt * (a->Dv * 4 + 8);
   return ETS_OK;
@@ -416,8 +498,8 @@ ets_status make_plan(const ets_attend_args* a, Plan* plan) {
 
 template <class T, int N, int MT>
 void launch_attend(const AttendParams& p, hipStream_t s) {
-  const size_t lds = kWaves * kTile * (N * 128 + 32) + (kWaves + 1) * MT * 16 * sizeof(f32x2);
-  const uint32_t grid = static_cast<uint32_t>(static_cast<int64_t>(p.units) * p.row_groups * p.splits);
+  const size_t lds = kWaves * kTile * (2 * value_plane(N) + 16) + kWaves * (MT + 1) * 16 * sizeof(f32x2) + 3 * kChunk * kTile * 4;
+  const uint32_t grid = attend_grid(p);
   hipLaunchKernelGGL((attend_kernel<T, N, N, MT>), dim3(grid), dim3(kThreads), lds, s, p);
 }
 
@@ -443,8 +525,8 @@ void launch_type(const Plan& plan, hipStream_t s) {
     default: launch_attend_wide(p, plan.mt, plan.shared, s);
   }
   if (p.splits > 1) {
-    const int64_t rows = static_cast<int64_t>(p.units) * p.rows;
-    hipLaunchKernelGGL(join_kernel<T>, dim3(static_cast<uint32_t>((rows + p.join_rows - 1) / p.join_rows)), dim3(kThreads), 0, s, p);
+    const int64_t parts = static_cast<int64_t>(p.units) * p.rows * p.by_parts.d;
+    hipLaunchKernelGGL(join_kernel<T>, dim3(static_cast<uint32_t>((parts + p.join_parts - 1) / p.join_parts)), dim3(kThreads), 0, s, p);
   }
 }
 

@@ -19,9 +19,6 @@ constexpr int kPitch = 2 * kPlane + 16;
 constexpr int kDepth = 2;            // tiles on their way from memory
 constexpr float kSlack = 8.0f;       // how far (log2) a score may pass its reference
 
-// Read in the place of a row that is not there.
-__device__ const u32v4 kNothing[kPieces] = {};
-
 // Pieces of a tile on their way through a lane, and their scale bytes.
 template <int N>
 struct Pieces {
@@ -73,6 +70,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendParams p
   Lds& lds = *reinterpret_cast<Lds*>(lds_raw);
   const ets_attend_args& a = p.a;
   const AttendSpot spot = attend_spot(p);
+  if (!spot.live) return;
   const int tid = threadIdx.x, lane = tid & 63, col = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int tiles = max(spot.last - spot.first, 0);
@@ -83,8 +81,6 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendParams p
   const bool sums = wave >= 4;
   const int piece0 = sums ? tid - 256 : 1024 + tid;
   // addresses as numbers: a row that is not there is read from kNothing, without a branch
-  typedef __attribute__((address_space(1))) const u32v4* Global16;
-  typedef __attribute__((address_space(1))) const uint8_t* Global1;
   const uint64_t nothing = reinterpret_cast<uint64_t>(&kNothing[0]);
   auto bring = [&](auto& set, int i, uint64_t codes, uint32_t row, uint64_t scales, uint32_t scale_row, int pieces) {
     const int32_t* slots = lds.slot[i & 3];
@@ -98,8 +94,8 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendParams p
       const bool there = slot[j] >= 0 && at < pieces;
       const uint64_t w = codes + static_cast<uint64_t>(static_cast<uint32_t>(slot[j])) * row + 16 * at;
       const uint64_t b = scales + static_cast<uint64_t>(static_cast<uint32_t>(slot[j])) * scale_row + (at >> 1);
-      set.w[j] = *reinterpret_cast<Global16>(there ? w : nothing);
-      set.byte[j] = *reinterpret_cast<Global1>(there ? b : nothing);
+      set.w[j] = load_global<u32v4>(there ? w : nothing);
+      set.byte[j] = load_global<uint8_t>(there ? b : nothing);
     }
   };
   auto lay = [&](const auto& set, uint8_t* tile) {
@@ -182,7 +178,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendParams p
     for (int m = 0; m < MQ; ++m) {
       const int r = spot.row0 + 16 * (MQ * hg + m) + col;
       int t, h;
-      attend_row(p, spot, r, &t, &h);
+      attend_row(p, spot, spot.hk, r, &t, &h);
       const char* src = static_cast<const char*>(a.q) + 2 * (spot.b * a.q_b + t * a.q_t + h * a.q_h);
       tree_bits[m] = 0;
 #pragma unroll
@@ -358,7 +354,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendParams p
   });
   __syncthreads();
 
-  const int64_t block = blockIdx.x;
+  const int64_t block = attend_place(p, spot, spot.hk);
 #pragma unroll
   for (int m = 0; m < RT; ++m) {
     const int r = spot.row0 + 16 * m + col;
@@ -377,7 +373,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendParams p
       if (first) p.stat[at] = s;
     } else {
       int t, h;
-      attend_row(p, spot, r, &t, &h);
+      attend_row(p, spot, spot.hk, r, &t, &h);
       const int64_t at = (static_cast<int64_t>(spot.b) * a.T + t) * a.Hq + h;
       const float inv = attend_inverse(s[1]);
       typedef T V4 __attribute__((ext_vector_type(4)));
@@ -396,7 +392,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendParams p
 
 template <class T, int RT, int NC, bool SHARED>
 void launch(const AttendParams& p, hipStream_t s) {
-  const uint32_t grid = static_cast<uint32_t>(static_cast<int64_t>(p.units) * p.row_groups * p.splits);
+  const uint32_t grid = attend_grid(p);
   hipLaunchKernelGGL((attend_wide_kernel<T, RT, NC, SHARED>), dim3(grid), dim3(kThreads),
                      sizeof(WideLds<RT, SHARED, Mat<T>::kRowScale>), s, p);
 }

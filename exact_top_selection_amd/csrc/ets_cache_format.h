@@ -37,6 +37,14 @@ __device__ __forceinline__ void store_any(void* p, const V& v) {
   __builtin_memcpy(p, &v, sizeof(V));
 }
 
+// A load from a global address held as a number (so that an address can be
+// chosen without a branch and the load stays a global one), at any alignment.
+template <class V>
+__device__ __forceinline__ V load_global(uint64_t address) {
+  struct __attribute__((packed)) Any { V v; };
+  return reinterpret_cast<const __attribute__((address_space(1))) Any*>(address)->v;
+}
+
 // n / d for 0 <= n < 2^31 and a divisor d >= 1 fixed at launch: with l =
 // ceil(log2 d) and m = ceil(2^(31 + l) / d), n * m / 2^(31 + l) exceeds n / d
 // by less than n / 2^(31 + l) <= 1 / d, so the floor is exact.  d lies in
