@@ -13,9 +13,6 @@ constexpr int kAttendTile = 32;  // keys of a step
 constexpr float kNegInf = -__builtin_inff();
 constexpr float kLn2 = 0.69314718055994530942f;
 
-// Read in the place of a row that is not there (576 zeros).
-static __device__ const u32v4 kNothing[ETS_MAX_HEAD_DIM / 16] = {};
-
 struct AttendParams {
   ets_attend_args a;
   int G;             // query heads of a cache head

@@ -12,15 +12,6 @@ constexpr int kTile = kAttendTile;
 
 constexpr int kChunk = 16;  // tiles whose slots are brought at a time
 
-// Keeps what is made of loaded values behind this point: made earlier, it would wait for the load there.
-template <class V, int A, int B>
-__device__ __forceinline__ void hold(V (&x)[A][B]) {
-#pragma unroll
-  for (int i = 0; i < A; ++i)
-#pragma unroll
-    for (int j = 0; j < B; ++j) asm volatile("" : "+v"(x[i][j]));
-}
-
 // Bytes of half a decoded row of 64 nv channels.
 constexpr int value_plane(int nv) { return 64 * nv + (nv % 4 ? 0 : 64); }
 

@@ -45,6 +45,18 @@ __device__ __forceinline__ V load_global(uint64_t address) {
   return reinterpret_cast<const __attribute__((address_space(1))) Any*>(address)->v;
 }
 
+// Read in the place of a row that is not there (576 zeros).
+static __device__ const u32v4 kNothing[ETS_MAX_HEAD_DIM / 16] = {};
+
+// Keeps what is made of loaded values behind this point: made earlier, it would wait for the load there.
+template <class V, int A, int B>
+__device__ __forceinline__ void hold(V (&x)[A][B]) {
+#pragma unroll
+  for (int i = 0; i < A; ++i)
+#pragma unroll
+    for (int j = 0; j < B; ++j) asm volatile("" : "+v"(x[i][j]));
+}
+
 // n / d for 0 <= n < 2^31 and a divisor d >= 1 fixed at launch: with l =
 // ceil(log2 d) and m = ceil(2^(31 + l) / d), n * m / 2^(31 + l) exceeds n / d
 // by less than n / 2^(31 + l) <= 1 / d, so the floor is exact.  d lies in
@@ -80,37 +92,6 @@ __device__ __forceinline__ float rows_max(float x) {
   const uint32_t c = __float_as_uint(y);
   const auto t = __builtin_amdgcn_permlane16_swap(c, c, false, false);
   return fmaxf(__uint_as_float(t[0]), __uint_as_float(t[1]));
-}
-
-// Scale bytes of one cached row, four a word; bytes past nb are left 0.
-template <int WORDS>
-__device__ __forceinline__ void load_scales(uint32_t (&sc)[WORDS], const uint8_t* row, int nb) {
-#pragma unroll
-  for (int i = 0; i < WORDS; ++i) {
-    if (4 * i + 4 <= nb) {
-      sc[i] = load_any<uint32_t>(row + 4 * i);
-    } else {
-      uint32_t w = 0;
-      if (4 * i < nb) w = row[4 * i];
-      if (4 * i + 1 < nb) w |= static_cast<uint32_t>(row[4 * i + 1]) << 8;
-      if (4 * i + 2 < nb) w |= static_cast<uint32_t>(row[4 * i + 2]) << 16;
-      sc[i] = w;
-    }
-  }
-}
-
-// Largest scale byte of a row.
-template <int WORDS>
-__device__ __forceinline__ uint32_t scales_max(const uint32_t (&sc)[WORDS]) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < WORDS; ++i) {
-    m = max(m, sc[i] & 255u);
-    m = max(m, (sc[i] >> 8) & 255u);
-    m = max(m, (sc[i] >> 16) & 255u);
-    m = max(m, sc[i] >> 24);
-  }
-  return m;
 }
 
 // Eight codes (two words) to eight values times `scale`, a power of two.
@@ -163,11 +144,6 @@ struct Mat<_Float16> {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
   }
 };
-
-// Byte `i` (0 to 3, per lane) of a word.
-__device__ __forceinline__ uint32_t byte_of(uint32_t w, uint32_t shift) {
-  return __builtin_amdgcn_ubfe(w, shift, 8);
-}
 
 inline bool dtype_known(int32_t dtype) { return dtype == ETS_BF16 || dtype == ETS_FP16 || dtype == ETS_FP32; }
 

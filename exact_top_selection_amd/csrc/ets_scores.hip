@@ -9,7 +9,9 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWaves = 4;
 constexpr int kTile = 64;           // keys of a wave's step, held in registers
-constexpr int kChunkMax = 1024;     // keys of a workgroup
+constexpr int kUnit = kWaves * kTile;  // keys by which the work is dealt out
+constexpr int kPiece = 2048;        // keys of a workgroup between barriers
+constexpr int kFill = 1024;         // positions past a length that are filled at a time
 constexpr int kQueryBytes = 65536;  // queries that a workgroup keeps in LDS
 constexpr float kNegInf = -__builtin_inff();
 
@@ -18,16 +20,16 @@ struct ScoreParams {
   int64_t q_b, q_t, q_h;  // bytes
   const float* w;
   int64_t w_b, w_t;
-  int T, H, D, L;
+  int B, T, H, D, L;
   int tokens, head_tiles;  // tokens of a workgroup; 16-row tiles of a token
-  int chunk;               // keys of a workgroup
   const uint8_t* codes;
   const uint8_t* scales;
-  int64_t codes_s, scales_s, S;
+  uint32_t codes_s, scales_s;
+  int64_t S;
   const int32_t* table;
   int64_t pt_b;
   const int32_t* lens;
-  FastDiv by_page;
+  FastDiv by_page, by_fills;
   float* out;
   int64_t out_stride;
 };
@@ -39,98 +41,157 @@ struct ScoreParams {
 // 16-row query tiles from LDS one by one, each feeding 4 * D / 32 matrix
 // instructions.  Rows of the result are heads, columns keys, so the weighted
 // sum over heads runs down a lane's registers and over four lanes at the end.
-template <class T, int NP>
-__global__ __launch_bounds__(kThreads, 2) void scores_kernel(ScoreParams p) {
+//
+// The lengths are known on the device only.  All keys, in units of 256, are
+// numbered through the batch and dealt out to the workgroups in equal runs: a
+// grid by sequence and chunk left a quarter of it idle with lengths between L
+// / 2 and L (64 x 32768: 61 us against 45).  FULL: D is 64 NP.
+template <class T, int NP, bool FULL>
+__global__ __launch_bounds__(kThreads, NP <= 2 ? 3 : NP == 3 ? 2 : 1) void scores_kernel(ScoreParams p) {
   typedef Mat<T> M;
   typedef typename M::V8 V8;
-  constexpr int W = (NP + 1) / 2;
   extern __shared__ __align__(16) char lds[];
   const int tiles_max = p.tokens * p.head_tiles;
-  V8* qs = reinterpret_cast<V8*>(lds);                                      // [tile][pair][half][lane]
-  float* ws = reinterpret_cast<float*>(lds + tiles_max * NP * 2048);        // [tile][16]
-  int32_t* slots = reinterpret_cast<int32_t*>(ws + tiles_max * 16);         // [chunk]
+  V8* qs = reinterpret_cast<V8*>(lds);                                // [tile][pair][half][lane]
+  float* ws = reinterpret_cast<float*>(lds + tiles_max * NP * 2048);  // [tile][16]
+  int32_t* slots = reinterpret_cast<int32_t*>(ws + tiles_max * 16);   // [kPiece]
+  float* held = reinterpret_cast<float*>(slots + kPiece);             // [wave][token][lane]
+  __shared__ int64_t found[2 + kWaves];
 
-  const int b = blockIdx.y, t0 = blockIdx.z * p.tokens;
+  const int t0 = blockIdx.y * p.tokens;
   const int tokens = min(p.tokens, p.T - t0), tiles = tokens * p.head_tiles;
-  const int k0 = static_cast<int>(blockIdx.x) * p.chunk, keys = min(p.chunk, p.L - k0);
-  const int n = min(max(p.lens[b], 0), p.L);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, g = lane >> 4;
+  auto length = [&](int b) { return min(max(p.lens[b], 0), p.L); };
+  auto units = [&](int b) { return (length(b) + kUnit - 1) / kUnit; };
 
-  if (k0 >= n) {  // nothing but the padding
-    for (int t = 0; t < tokens; ++t)
-      for (int i = threadIdx.x; i < keys; i += kThreads)
-        p.out[(static_cast<int64_t>(b) * p.T + t0 + t) * p.out_stride + k0 + i] = kNegInf;
-    return;
+  // positions past the lengths
+  for (int64_t i = blockIdx.x; i < static_cast<int64_t>(p.B) * p.by_fills.d; i += gridDim.x) {
+    const int b = static_cast<int>(div_by(static_cast<uint32_t>(i), p.by_fills));
+    const int from = static_cast<int>(i - static_cast<int64_t>(b) * p.by_fills.d) * kFill, n = length(b);
+    const int to = min(from + kFill, p.L);
+    if (n < to)
+      for (int t = 0; t < tokens; ++t)
+        for (int k = max(from, n) + threadIdx.x; k < to; k += kThreads)
+          p.out[(static_cast<int64_t>(b) * p.T + t0 + t) * p.out_stride + k] = kNegInf;
   }
 
-  for (int i = threadIdx.x; i < p.chunk; i += kThreads) {
-    int32_t slot = -1;
-    if (k0 + i < n) {
-      const uint32_t page = div_by(k0 + i, p.by_page);
-      const int64_t s = static_cast<int64_t>(p.table[b * p.pt_b + page]) * p.by_page.d + (k0 + i - page * p.by_page.d);
-      slot = s >= 0 && s < p.S ? static_cast<int32_t>(s) : -1;
-    }
-    slots[i] = slot;
+  // this workgroup's run of units: lane i counts sequences i * each ..; the one in whose count the run starts says where
+  const int each = (p.B + kThreads - 1) / kThreads, b0 = static_cast<int>(threadIdx.x) * each;
+  int64_t mine = 0;
+  for (int b = b0; b < min(b0 + each, p.B); ++b) mine += units(b);
+  int64_t upto = mine;  // through this lane
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int64_t x = __shfl_up(upto, o);
+    if (lane >= o) upto += x;
   }
-  for (int i = threadIdx.x; i < tiles * NP * 128; i += kThreads) {
-    const int l = i & 63, half = (i >> 6) & 1, tp = i >> 7;
-    const int tile = tp / NP, pair = tp - tile * NP, t = tile / p.head_tiles;
-    const int h = (tile - t * p.head_tiles) * 16 + (l & 15), d = 64 * pair + 16 * (l >> 4) + 8 * half;
-    V8 v = {};
-    if (h < p.H && d < p.D)
-      v = load_any<V8>(p.q + b * p.q_b + (t0 + t) * p.q_t + h * p.q_h + static_cast<int64_t>(d) * 2);
-    qs[i] = v;
+  if (lane == 63) found[2 + wave] = upto;
+  __syncthreads();
+  int64_t all = 0;
+  for (int w = 0; w < kWaves; ++w) {
+    if (w < wave) upto += found[2 + w];
+    all += found[2 + w];
   }
-  for (int i = threadIdx.x; i < tiles * 16; i += kThreads) {
-    const int t = (i >> 4) / p.head_tiles, h = i - t * p.head_tiles * 16;
-    ws[i] = h < p.H ? p.w[b * p.w_b + (t0 + t) * p.w_t + h] : 0.0f;
+  const int64_t run = (all + gridDim.x - 1) / gridDim.x, start = run * blockIdx.x;
+  if (start >= all) return;
+  if (start >= upto - mine && start < upto) {
+    int64_t left = start - (upto - mine);
+    int b = b0;
+    for (int u = units(b); left >= u; u = units(b)) left -= u, ++b;
+    found[0] = b, found[1] = left;
   }
   __syncthreads();
+  int b = __builtin_amdgcn_readfirstlane(static_cast<int>(found[0])), k0 = __builtin_amdgcn_readfirstlane(static_cast<int>(found[1])) * kUnit;
+  int64_t todo = all - start < run ? all - start : run;
 
-  const int nb = p.D / kCacheBlock;
+  // a step's rows on their way: lane (key col of each 16, row g) brings codes 64 i + 16 g .. + 15 and their scale
+  // byte; rows and channels that are not there come from kNothing, without a branch
+  const uint64_t nothing = reinterpret_cast<uint64_t>(&kNothing[0]);
+  const uint64_t kc = reinterpret_cast<uint64_t>(p.codes) + 16 * g, ks = reinterpret_cast<uint64_t>(p.scales) + (g >> 1);
   u32v4 raw[4][NP];
-  uint32_t sc[4][W];
+  uint32_t byte[4][NP];
   auto fetch = [&](int k) {
+    int32_t slot[4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) slot[s] = slots[min(k, kPiece - kTile) + 16 * s + col];
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      const int32_t slot = slots[k + 16 * s + col];
+      const bool there = slot[s] >= 0 && k < kPiece;
+      const uint64_t at = static_cast<uint32_t>(slot[s]), c0 = kc + at * p.codes_s, b0 = ks + at * p.scales_s;
+      const uint64_t c1 = there ? c0 : nothing, b1 = there ? b0 : nothing;
 #pragma unroll
-      for (int i = 0; i < NP; ++i) raw[s][i] = u32v4{0, 0, 0, 0};
-#pragma unroll
-      for (int i = 0; i < W; ++i) sc[s][i] = 0;
-      if (slot >= 0) {
-        const uint8_t* row = p.codes + slot * p.codes_s + 16 * g;
-#pragma unroll
-        for (int i = 0; i < NP; ++i)
-          if (64 * i + 16 * g < p.D) raw[s][i] = load_any<u32v4>(row + 64 * i);
-        load_scales<W>(sc[s], p.scales + slot * p.scales_s, nb);
+      for (int i = 0; i < NP; ++i) {
+        const bool in = FULL || 64 * i + 16 * g < p.D;
+        const uint64_t c = c1 + 64 * i, b = b1 + 2 * i;
+        raw[s][i] = load_global<u32v4>(in ? c : nothing);
+        byte[s][i] = load_global<uint8_t>(in ? b : nothing);
       }
     }
   };
 
-  const int last = min(keys, n - k0);  // keys of the chunk that have a score
-  int k = wave * kTile;
-  if (k < last) fetch(k);
-  for (; k < keys; k += kWaves * kTile) {
-    float* out = p.out + (static_cast<int64_t>(b) * p.T + t0) * p.out_stride + k0 + k + lane;
-    if (k >= last) {
-      for (int t = 0; t < tokens; ++t)
-        if (k + lane < keys) out[t * p.out_stride] = kNegInf;
+  for (bool new_b = true; todo > 0;) {
+    const int n = length(b);
+    if (k0 >= n) {
+      ++b, k0 = 0, new_b = true;
       continue;
     }
+    const int keys = min(static_cast<int>(min(todo * kUnit, static_cast<int64_t>(kPiece))), n - k0);
+    __syncthreads();  // the piece before has been read
+    for (int i = threadIdx.x; i < kPiece; i += kThreads) {
+      const int j = min(k0 + i, n - 1);  // past the piece's keys: any of its slots, not used
+      const uint32_t page = div_by(j, p.by_page);
+      const int64_t s = static_cast<int64_t>(p.table[b * p.pt_b + page]) * p.by_page.d + (j - page * p.by_page.d);
+      slots[i] = i < keys && s >= 0 && s < p.S ? static_cast<int32_t>(s) : -1;
+    }
+    if (new_b) {
+      for (int i = threadIdx.x; i < tiles * NP * 128; i += kThreads) {
+        const int l = i & 63, half = (i >> 6) & 1, tp = i >> 7;
+        const int tile = tp / NP, pair = tp - tile * NP, t = tile / p.head_tiles;
+        const int h = (tile - t * p.head_tiles) * 16 + (l & 15), d = 64 * pair + 16 * (l >> 4) + 8 * half;
+        V8 v = {};
+        if (h < p.H && d < p.D)
+          v = load_any<V8>(p.q + b * p.q_b + (t0 + t) * p.q_t + h * p.q_h + static_cast<int64_t>(d) * 2);
+        qs[i] = v;
+      }
+      for (int i = threadIdx.x; i < tiles * 16; i += kThreads) {
+        const int t = (i >> 4) / p.head_tiles, h = i - t * p.head_tiles * 16;
+        ws[i] = h < p.H ? p.w[b * p.w_b + (t0 + t) * p.w_t + h] : 0.0f;
+      }
+    }
+    new_b = false;
+    __syncthreads();
+
+  int k = wave * kTile;
+  fetch(k);
+  hold(byte);  // else the loop carries 8-bit values and widens them as soon as they are loaded
+  // Sums leave a step later, before the next rows are asked for: a store behind them would be waited for with them.
+  float* own = held + wave * p.tokens * kTile + lane;
+  float* out = p.out + (static_cast<int64_t>(b) * p.T + t0) * p.out_stride + k0 + lane;
+  auto leave = [&](int at) {
+    if (at >= 0 && at + lane < keys)
+      for (int t = 0; t < tokens; ++t) out[t * p.out_stride + at] = own[t * kTile];
+  };
+  for (; k < keys; k += kWaves * kTile) {
     V8 key[4][NP][2];
     uint32_t top[4];
+    hold(raw), hold(byte);
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      top[s] = M::kRowScale ? scales_max<W>(sc[s]) : 0;
+      top[s] = 0;
+      if constexpr (M::kRowScale) {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) top[s] = max(top[s], byte[s][i]);
+        top[s] = __float_as_uint(rows_max(__uint_as_float(top[s] << 23))) >> 23;  // bytes as powers of two keep their order
+      }
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
-        const float f = M::scale(byte_of(sc[s][i / 2], 16 * (i & 1) + 8 * (g >> 1)), top[s]);
+        const float f = M::scale(byte[s][i], top[s]);
         key[s][i][0] = M::keys(raw[s][i][0], raw[s][i][1], f);
         key[s][i][1] = M::keys(raw[s][i][2], raw[s][i][3], f);
       }
     }
-    if (k + kWaves * kTile < last) fetch(k + kWaves * kTile);
+    leave(k - kWaves * kTile);
+    fetch(k + kWaves * kTile);
     const bool seen = slots[k + lane] >= 0;
     float size = 1.0f;
     if (M::kRowScale) {
@@ -165,21 +226,34 @@ __global__ __launch_bounds__(kThreads, 2) void scores_kernel(ScoreParams p) {
       const float y = __uint_as_float(c[0]) + __uint_as_float(c[1]);
       const auto e = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(y), false, false);
       const float sum = (__uint_as_float(e[0]) + __uint_as_float(e[1])) * size;
-      if (k + lane < keys) out[t * p.out_stride] = seen ? sum : kNegInf;
+      own[t * kTile] = seen ? sum : kNegInf;
     }
+  }
+  leave(k - kWaves * kTile);
+    todo -= (keys + kUnit - 1) / kUnit;
+    k0 += keys;
+  }
+}
+
+template <class T, int NP>
+void launch_pairs(const ScoreParams& p, dim3 grid, size_t lds, hipStream_t s) {
+  if (p.D == 64 * NP) {
+    hipLaunchKernelGGL((scores_kernel<T, NP, true>), grid, dim3(kThreads), lds, s, p);
+  } else {
+    hipLaunchKernelGGL((scores_kernel<T, NP, false>), grid, dim3(kThreads), lds, s, p);
   }
 }
 
 template <class T>
 void launch_scores(const ScoreParams& p, int np, dim3 grid, size_t lds, hipStream_t s) {
   if (np == 1) {
-    hipLaunchKernelGGL((scores_kernel<T, 1>), grid, dim3(kThreads), lds, s, p);
+    launch_pairs<T, 1>(p, grid, lds, s);
   } else if (np == 2) {
-    hipLaunchKernelGGL((scores_kernel<T, 2>), grid, dim3(kThreads), lds, s, p);
+    launch_pairs<T, 2>(p, grid, lds, s);
   } else if (np == 3) {
-    hipLaunchKernelGGL((scores_kernel<T, 3>), grid, dim3(kThreads), lds, s, p);
+    launch_pairs<T, 3>(p, grid, lds, s);
   } else {
-    hipLaunchKernelGGL((scores_kernel<T, 4>), grid, dim3(kThreads), lds, s, p);
+    launch_pairs<T, 4>(p, grid, lds, s);
   }
 }
 
@@ -197,7 +271,8 @@ ets_status ets_index_scores(const void* q, int64_t q_b, int64_t q_t, int64_t q_h
   using namespace ets;
   if (B < 0 || T < 0 || H < 1 || H > ETS_MAX_INDEX_HEADS || D < kCacheBlock || D % kCacheBlock ||
       D > ETS_MAX_INDEX_DIM || S < 0 || S > INT32_MAX || page_size < 1 || L < 0 || out_stride < L ||
-      (dtype != ETS_BF16 && dtype != ETS_FP16) || B > 65535)
+      (dtype != ETS_BF16 && dtype != ETS_FP16) ||
+      codes_s < 0 || codes_s > UINT32_MAX || scales_s < 0 || scales_s > UINT32_MAX || static_cast<int64_t>(B) * ((static_cast<int64_t>(L) + kFill - 1) / kFill) > INT32_MAX)
     return ETS_ERR_INVALID_ARG;
   if (B == 0 || T == 0 || L == 0) return ETS_OK;
   if (!q || !weights || !page_table || !seq_lens || !out || (S && (!codes || !scales))) return ETS_ERR_INVALID_ARG;
@@ -207,21 +282,22 @@ ets_status ets_index_scores(const void* q, int64_t q_b, int64_t q_t, int64_t q_h
   ScoreParams p{};
   p.q = static_cast<const char*>(q), p.q_b = 2 * q_b, p.q_t = 2 * q_t, p.q_h = 2 * q_h;
   p.w = weights, p.w_b = w_b, p.w_t = w_t;
-  p.T = T, p.H = H, p.D = D, p.L = L;
+  p.B = B, p.T = T, p.H = H, p.D = D, p.L = L;
   p.head_tiles = (H + 15) / 16;
   const int room = kQueryBytes / (np * 2048) / p.head_tiles;
   p.tokens = T < room ? T : room;
   const int groups = (T + p.tokens - 1) / p.tokens;
   if (groups > 65535) return ETS_ERR_INVALID_ARG;
-  p.codes = codes, p.codes_s = codes_s, p.scales = scales, p.scales_s = scales_s, p.S = S;
+  p.codes = codes, p.codes_s = static_cast<uint32_t>(codes_s), p.scales = scales, p.scales_s = static_cast<uint32_t>(scales_s), p.S = S;
   p.table = page_table, p.pt_b = pt_b, p.lens = seq_lens;
   p.by_page = fast_div(page_size);
   p.out = out, p.out_stride = out_stride;
-  p.chunk = kChunkMax;
-  while (p.chunk > kWaves * kTile && (static_cast<int64_t>(L) + p.chunk - 1) / p.chunk * B * groups < 8 * cu) p.chunk /= 2;
+  p.by_fills = fast_div(static_cast<uint32_t>((static_cast<int64_t>(L) + kFill - 1) / kFill));
+  // as many workgroups as the device holds at once, over the groups of tokens
+  const int64_t most = (static_cast<int64_t>(L) + kUnit - 1) / kUnit * B, fits = (3 * cu + groups - 1) / groups;
   const int tiles = p.tokens * p.head_tiles;
-  const size_t lds = static_cast<size_t>(tiles) * np * 2048 + tiles * 64 + p.chunk * 4;
-  const dim3 grid((static_cast<int64_t>(L) + p.chunk - 1) / p.chunk, B, groups);
+  const size_t lds = static_cast<size_t>(tiles) * np * 2048 + tiles * 64 + kPiece * 4 + p.tokens * kThreads * 4;
+  const dim3 grid(static_cast<uint32_t>(most < fits ? most : fits), groups);
   auto s = static_cast<hipStream_t>(stream);
   if (dtype == ETS_BF16) {
     launch_scores<__bf16>(p, np, grid, lds, s);
