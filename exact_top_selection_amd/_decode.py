@@ -79,6 +79,26 @@ def _floats(t: torch.Tensor, name: str, dim: int, types: str = "bf16, fp16 or fp
     return kind
 
 
+def _vector(t: torch.Tensor, name: str, n: int, index: int) -> int:
+    """Address of a contiguous int32 [n] on device `index`: one test where all is well, the binding's messages where not."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.shape == (n,) and t.get_device() == index
+            and (n < 2 or t.stride(0) == 1)):
+        _vec(t, name, n)
+        _same_device(index, (t, name))
+    return t.data_ptr()
+
+
+def _run(index: int, what: str, fn, *args) -> None:
+    """fn(*args, current stream of device `index`) with that device current; raises on a status."""
+    if torch._C._cuda_getDevice() == index:
+        st = fn(*args, _stream(index))
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, _stream(index))
+    if st:
+        _check(st, what)
+
+
 def _no_grad(t: torch.Tensor, name: str, what: str) -> None:
     if t.requires_grad and torch.is_grad_enabled():
         raise ValueError("%s has no gradient: detach %s, or call it under torch.no_grad()" % (what, name))
@@ -130,33 +150,37 @@ def rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, layou
     if x.requires_grad and torch.is_grad_enabled():
         raise ValueError("rope records no gradient: detach x, and take its gradient as rope(grad, ..., inverse=True)")
     N, H, D = x.shape
+    strides = x.stride()
     index = x.get_device()
-    _vec(positions, "positions", N)
-    _require(inv_freq, "inv_freq", torch.float64, 1)
+    at = _vector(positions, "positions", N, index)
+    if not (isinstance(inv_freq, torch.Tensor) and inv_freq.dtype is torch.float64 and inv_freq.ndim == 1
+            and inv_freq.get_device() == index):
+        _require(inv_freq, "inv_freq", torch.float64, 1)
+        _same_device(index, (inv_freq, "inv_freq"))
     R = 2 * inv_freq.shape[0]
     if R > 2 and inv_freq.stride(0) != 1:
         raise ValueError("inv_freq must be contiguous")
-    _same_device(index, (positions, "positions"), (inv_freq, "inv_freq"))
-    if layout not in _LAYOUTS:
+    pairs = _LAYOUTS.get(layout)
+    if pairs is None:
         raise ValueError("layout must be 'interleaved' or 'half', got %r" % (layout,))
     if D < 1 or D > MAX_ROPE_DIM:
         raise ValueError("x must have 1 to %d channels, got %d" % (MAX_ROPE_DIM, D))
     if offset < 0 or offset + R > D:
         raise ValueError("channels [%d, %d) do not lie inside the %d of x" % (offset, offset + R, D))
     if out is None:
-        out = torch.empty((N, H, D), dtype=x.dtype, device=x.device)
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+        to_n, to_h = H * D, D
     else:
         _floats(out, "out", 3)
         if out.shape != x.shape or out.dtype is not x.dtype or out.get_device() != index:
             raise ValueError("out must have the shape, type and device of x")
         if _overlaps(out):
             raise ValueError("rows of out must not overlap")
-        if out.data_ptr() == x.data_ptr() and out.stride() != x.stride():
+        if out.data_ptr() == x.data_ptr() and out.stride() != strides:
             raise ValueError("out may be x itself, or memory apart from it")
-    st = _on(index, _lib().ets_rope, x.data_ptr(), x.stride(0), x.stride(1), out.data_ptr(), out.stride(0), out.stride(1),
-             N, H, D, positions.data_ptr(), inv_freq.data_ptr(), R, offset, _LAYOUTS[layout], scale, 1 if inverse else 0,
-             kind, _stream(index))
-    _check(st, "ets_rope")
+        to_n, to_h, _ = out.stride()
+    _run(index, "ets_rope", _lib().ets_rope, x.data_ptr(), strides[0], strides[1], out.data_ptr(), to_n, to_h, N, H, D, at,
+         inv_freq.data_ptr(), R, offset, pairs, scale, 1 if inverse else 0, kind)
     return out
 
 
@@ -173,14 +197,15 @@ def cache_write(x: torch.Tensor, slots: torch.Tensor, codes: torch.Tensor, scale
     if x.shape[1] != H or x.shape[2] != D:
         raise ValueError("x must have shape [N, %d, %d], got %s" % (H, D, tuple(x.shape)))
     index = x.get_device()
-    _vec(slots, "slots", N)
-    _same_device(index, (slots, "slots"), (codes, "codes"), (scales, "scales"))
+    at = _vector(slots, "slots", N, index)
+    _same_device(index, (codes, "codes"), (scales, "scales"))
     if _overlaps(codes) or _overlaps(scales):
         raise ValueError("rows of codes and scales must not overlap")
-    st = _on(index, _lib().ets_cache_write, x.data_ptr(), x.stride(0), x.stride(1), N, H, D, slots.data_ptr(),
-             codes.data_ptr(), codes.stride(0), codes.stride(1), scales.data_ptr(), scales.stride(0), scales.stride(1), S,
-             kind, _stream(index))
-    _check(st, "ets_cache_write")
+    from_n, from_h, _ = x.stride()
+    codes_s, codes_h, _ = codes.stride()
+    scales_s, scales_h, _ = scales.stride()
+    _run(index, "ets_cache_write", _lib().ets_cache_write, x.data_ptr(), from_n, from_h, N, H, D, at, codes.data_ptr(), codes_s,
+         codes_h, scales.data_ptr(), scales_s, scales_h, S, kind)
 
 
 def cache_read(codes: torch.Tensor, scales: torch.Tensor, slots: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
@@ -188,20 +213,22 @@ def cache_read(codes: torch.Tensor, scales: torch.Tensor, slots: torch.Tensor, d
     """The values of the cache's rows ``slots`` (int32 [N]) as [N, H, D] of ``dtype``; zeros for slots outside [0, S)."""
     S, H, D = _cache(codes, scales, "")
     index = codes.get_device()
-    _require(slots, "slots", torch.int32, 1)
+    if not isinstance(slots, torch.Tensor) or slots.ndim != 1:
+        _require(slots, "slots", torch.int32, 1)
     N = slots.shape[0]
-    _vec(slots, "slots", N)
-    _same_device(index, (slots, "slots"), (scales, "scales"))
-    if dtype not in _DTYPES:
+    at = _vector(slots, "slots", N, index)
+    _same_device(index, (scales, "scales"))
+    kind = _DTYPES.get(dtype)
+    if kind is None:
         raise TypeError("dtype must be torch.bfloat16, torch.float16 or torch.float32, got %s" % (dtype,))
     if out is None:
-        out = torch.empty((N, H, D), dtype=dtype, device=codes.device)
+        out = codes.new_empty((N, H, D), dtype=dtype)
     elif out.dtype is not dtype or out.shape != (N, H, D) or out.get_device() != index or not out.is_contiguous():
         raise ValueError("out must be contiguous %s [%d, %d, %d] on cuda:%d" % (dtype, N, H, D, index))
-    st = _on(index, _lib().ets_cache_read, codes.data_ptr(), codes.stride(0), codes.stride(1), scales.data_ptr(),
-             scales.stride(0), scales.stride(1), S, slots.data_ptr(), N, H, D, out.data_ptr(), _DTYPES[dtype],
-             _stream(index))
-    _check(st, "ets_cache_read")
+    codes_s, codes_h, _ = codes.stride()
+    scales_s, scales_h, _ = scales.stride()
+    _run(index, "ets_cache_read", _lib().ets_cache_read, codes.data_ptr(), codes_s, codes_h, scales.data_ptr(), scales_s,
+         scales_h, S, at, N, H, D, out.data_ptr(), kind)
     return out
 
 
@@ -252,11 +279,11 @@ def index_scores(q: torch.Tensor, weights: torch.Tensor, codes: torch.Tensor, sc
             raise ValueError("out must be float32 [%d, %d] on cuda:%d" % (B * T, L, index))
         if B * T > 1 and out.stride(0) < L:
             raise ValueError("rows of out must not overlap")
-    st = _on(index, _lib().ets_index_scores, q.data_ptr(), q.stride(0), q.stride(1), q.stride(2), weights.data_ptr(),
-             weights.stride(0), weights.stride(1), B, T, H, D, codes.data_ptr(), codes.stride(0), scales.data_ptr(),
-             scales.stride(0), S, page_table.data_ptr(), _rows(page_table, "page_table"), seq_lens.data_ptr(), page_size,
-             L, out.data_ptr(), _rows(out, "out"), kind, _stream(index))
-    _check(st, "ets_index_scores")
+    q_b, q_t, q_h, _ = q.stride()
+    w_b, w_t, _ = weights.stride()
+    _run(index, "ets_index_scores", _lib().ets_index_scores, q.data_ptr(), q_b, q_t, q_h, weights.data_ptr(), w_b, w_t, B, T,
+         H, D, codes.data_ptr(), codes.stride(0), scales.data_ptr(), scales.stride(0), S, page_table.data_ptr(),
+         _rows(page_table, "page_table"), seq_lens.data_ptr(), page_size, L, out.data_ptr(), _rows(out, "out"), kind)
     return out
 
 
@@ -288,37 +315,42 @@ def _attend(what, q, k_codes, k_scales, v_codes, v_scales, tree_slots, tree_mask
             raise ValueError("a tree has at most %d tokens, got %d" % (MAX_TREE, T))
         if tree_slots.shape != (B, T) or tree_mask.shape != (B, T):
             raise ValueError("tree_slots and tree_mask must have shape %s" % ((B, T),))
-    args = _AttendArgs(
-        B, T, Hq, Hkv, D, Dv, kind, slots.shape[2] if slots is not None else 0, L, page_size, S,
-        q.data_ptr(), q.stride(0), q.stride(1), q.stride(2),
-        k_codes.data_ptr(), k_codes.stride(0), k_codes.stride(1), k_scales.data_ptr(), k_scales.stride(0), k_scales.stride(1),
-        v_codes.data_ptr(), v_codes.stride(0), v_codes.stride(1), v_scales.data_ptr(), v_scales.stride(0), v_scales.stride(1))
+    out = q.new_empty((B, T, Hq, Dv))
+    lse = q.new_empty((B, T, Hq), dtype=torch.float32)
+    sel, sel_b, sel_t, K, table, pt_b, lens = None, 0, 0, 0, None, 0, None
     if slots is not None:
         # an empty list is a list: its address stands for the form of the call
-        args.slots, args.slots_b, args.slots_t = slots.data_ptr() or q.data_ptr(), slots.stride(0), slots.stride(1)
+        sel, K, (sel_b, sel_t, _) = slots.data_ptr() or q.data_ptr(), slots.shape[2], slots.stride()
     else:
-        args.page_table, args.pt_b, args.seq_lens = page_table.data_ptr(), _rows(page_table, "page_table"), seq_lens.data_ptr()
+        table, pt_b, lens = page_table.data_ptr(), _rows(page_table, "page_table"), seq_lens.data_ptr()
+    tree, tree_b, mask, mask_b = None, 0, None, 0
     if tree_slots is not None:
-        args.tree_slots, args.tree_b = tree_slots.data_ptr(), _rows(tree_slots, "tree_slots")
-        args.tree_mask, args.mask_b = tree_mask.data_ptr(), _rows(tree_mask, "tree_mask")
-    out = torch.empty((B, T, Hq, Dv), dtype=q.dtype, device=q.device)
-    lse = torch.empty((B, T, Hq), dtype=torch.float32, device=q.device)
-    args.out, args.lse = out.data_ptr(), lse.data_ptr()
+        tree, tree_b = tree_slots.data_ptr(), _rows(tree_slots, "tree_slots")
+        mask, mask_b = tree_mask.data_ptr(), _rows(tree_mask, "tree_mask")
+    args = ctypes.byref(_AttendArgs(
+        B, T, Hq, Hkv, D, Dv, kind, K, L, page_size, S, q.data_ptr(), *q.stride()[:3],
+        k_codes.data_ptr(), *k_codes.stride()[:2], k_scales.data_ptr(), *k_scales.stride()[:2],
+        v_codes.data_ptr(), *v_codes.stride()[:2], v_scales.data_ptr(), *v_scales.stride()[:2],
+        sel, sel_b, sel_t, table, pt_b, lens, tree, tree_b, mask, mask_b, out.data_ptr(), lse.data_ptr()))
     lib = _lib()
     need = _sz(0)
-    _check(_on(index, lib.ets_attend_workspace_size, ctypes.byref(args), ctypes.byref(need)), what)
+    if torch._C._cuda_getDevice() == index:
+        st = lib.ets_attend_workspace_size(args, ctypes.byref(need))
+    else:
+        st = _on(index, lib.ets_attend_workspace_size, args, ctypes.byref(need))
+    if st:
+        _check(st, what)
+    nbytes = need.value
     if workspace is not None:
         if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or not workspace.is_contiguous():
             raise TypeError("workspace must be a contiguous torch.Tensor on a HIP device")
         _same_device(index, (workspace, "workspace"))
-        if workspace.numel() * workspace.element_size() < need.value:
-            raise ValueError("workspace must hold at least %d bytes" % need.value)
-    elif need.value:
+        if workspace.numel() * workspace.element_size() < nbytes:
+            raise ValueError("workspace must hold at least %d bytes" % nbytes)
+    elif nbytes:
         # torch's allocator orders it on this stream, and keeps it for a graph that is being captured
-        workspace = torch.empty(need.value, dtype=torch.uint8, device=q.device)
-    st = _on(index, lib.ets_attend, ctypes.byref(args), workspace.data_ptr() if workspace is not None else None,
-             workspace.numel() * workspace.element_size() if workspace is not None else 0, _stream(index))
-    _check(st, what)
+        workspace = q.new_empty(nbytes, dtype=torch.uint8)
+    _run(index, what, lib.ets_attend, args, workspace.data_ptr() if nbytes else None, nbytes)
     return out, lse
 
 

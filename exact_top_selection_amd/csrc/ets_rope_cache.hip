@@ -10,6 +10,11 @@ constexpr int kThreads = 256;
 constexpr int kRopeTable = 2048;  // (cos, sin) pairs of a workgroup's tokens, in LDS (16 KiB)
 constexpr int kRopeStage = 32768; // bytes of rows that the staged form holds in LDS
 constexpr int kBatch = 4;         // vectors a lane has in flight
+// vectors of a lane of the read: one more load under way hides the slot's; 4 and more took longer (131072 x 576: 46 us with
+// 2, 47 with 1, 50 with 4, 56 with 8, whose few workgroups end unevenly)
+constexpr int kReadBatch = 2;
+// Outputs over this size pass the L2s by (they hold 32 MiB in all): the rows being read keep their place there.
+constexpr int64_t kStream = 32 << 20;
 
 enum RopeMode { kInterleaved = 0, kHalf = 1, kStaged = 2 };
 
@@ -23,6 +28,7 @@ struct RopeParams {
   const double* inv_freq;
   double scale;
   int tokens, heads;  // of a workgroup
+  bool stream;
   int head_groups;
   FastDiv by_items, by_heads, by_pairs, by_groups;
 };
@@ -32,6 +38,16 @@ struct Vec {
   static constexpr int n = 16 / sizeof(T);
   typedef T type __attribute__((ext_vector_type(16 / sizeof(T))));
 };
+
+template <class V>
+__device__ __forceinline__ void put(char* to, const V& v, bool stream) {
+  typedef u32v4 Any __attribute__((aligned(2)));
+  if (stream) {
+    __builtin_nontemporal_store(__builtin_bit_cast(u32v4, v), reinterpret_cast<Any*>(to));
+  } else {
+    store_any(to, v);
+  }
+}
 
 // Rotary positions.  A workgroup takes `tokens` tokens and `heads` of their
 // heads.  The cosines and sines of a token serve all its heads: they are
@@ -183,10 +199,10 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeParams p) {
             y[j] = static_cast<T>(v * c[0] - w * c[1]);
             z[j] = static_cast<T>(w * c[0] + v * c[1]);
           }
-          store_any(dst, y);
-          store_any(dst + static_cast<int64_t>(pairs) * sizeof(T), z);
+          put(dst, y, p.stream);
+          put(dst + static_cast<int64_t>(pairs) * sizeof(T), z, p.stream);
         } else {
-          store_any(dst, a[u]);
+          put(dst, a[u], p.stream);
         }
       } else {
         VT y = a[u];
@@ -200,7 +216,7 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeParams p) {
             y[j + 1] = static_cast<T>(w * c[0] + v * c[1]);
           }
         }
-        store_any(dst, y);
+        put(dst, y, p.stream);
       }
     }
   }
@@ -215,6 +231,7 @@ struct CacheParams {
   uint8_t* scales;
   int64_t codes_s, codes_h, scales_s, scales_h, S;
   uint32_t items;  // of this launch
+  bool stream;
   FastDiv by_row, by_heads;
 };
 
@@ -272,11 +289,11 @@ template <class T>
 __global__ __launch_bounds__(kThreads) void cache_read_kernel(CacheParams p) {
   constexpr int V = Vec<T>::n;
   typedef typename Vec<T>::type VT;
-  const uint32_t base = blockIdx.x * (kBatch * kThreads) + threadIdx.x;
-  u32v2 code[kBatch];
-  uint32_t byte[kBatch];
+  const uint32_t base = blockIdx.x * (kReadBatch * kThreads) + threadIdx.x;
+  u32v2 code[kReadBatch];
+  uint32_t byte[kReadBatch];
 #pragma unroll
-  for (int u = 0; u < kBatch; ++u) {
+  for (int u = 0; u < kReadBatch; ++u) {
     const uint32_t i = base + u * kThreads;
     code[u] = u32v2{0, 0};
     byte[u] = 0;
@@ -294,7 +311,7 @@ __global__ __launch_bounds__(kThreads) void cache_read_kernel(CacheParams p) {
     byte[u] = p.scales[slot * p.scales_s + h * p.scales_h + v * V / kCacheBlock];
   }
 #pragma unroll
-  for (int u = 0; u < kBatch; ++u) {
+  for (int u = 0; u < kReadBatch; ++u) {
     const uint32_t i = base + u * kThreads;
     if (i >= p.items) continue;
     VT y;
@@ -306,7 +323,7 @@ __global__ __launch_bounds__(kThreads) void cache_read_kernel(CacheParams p) {
       y[j] = static_cast<T>(ldexpf(f[0], e));
       y[j + 1] = static_cast<T>(ldexpf(f[1], e));
     }
-    store_any(p.out + static_cast<int64_t>(i) * 16, y);
+    put(p.out + static_cast<int64_t>(i) * 16, y, p.stream);
   }
 }
 
@@ -360,6 +377,7 @@ ets_status ets_rope(const void* x, int64_t x_n, int64_t x_h, void* out, int64_t 
   p.out = static_cast<char*>(out);
   p.x_n = x_n * size, p.x_h = x_h * size, p.out_n = out_n * size, p.out_h = out_h * size;
   p.N = N, p.H = H, p.D = D, p.R = R, p.offset = offset, p.layout = layout, p.inverse = inverse;
+  p.stream = N * H * D * size > kStream;
   p.positions = positions, p.inv_freq = inv_freq, p.scale = scale;
   // vectors of a workgroup: one a lane where the whole call has few, up to kBatch
   // a lane where it fills the device
@@ -449,12 +467,13 @@ ets_status ets_cache_read(const uint8_t* codes, int64_t codes_s, int64_t codes_h
     CacheParams p{};
     p.out = static_cast<char*>(out) + n * H * D * size;
     p.slots = slots + n;
+    p.stream = N * H * D * size > kStream;
     p.codes = const_cast<uint8_t*>(codes), p.codes_s = codes_s, p.codes_h = codes_h;
     p.scales = const_cast<uint8_t*>(scales), p.scales_s = scales_s, p.scales_h = scales_h, p.S = S;
     p.items = static_cast<uint32_t>(count * H * row);
     p.by_row = fast_div(row);
     p.by_heads = fast_div(H);
-    const uint32_t grid = (p.items + kBatch * kThreads - 1) / (kBatch * kThreads);
+    const uint32_t grid = (p.items + kReadBatch * kThreads - 1) / (kReadBatch * kThreads);
     if (dtype == ETS_BF16) {
       hipLaunchKernelGGL(cache_read_kernel<__bf16>, dim3(grid), dim3(kThreads), 0, s, p);
     } else if (dtype == ETS_FP16) {

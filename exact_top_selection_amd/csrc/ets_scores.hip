@@ -269,7 +269,7 @@ ets_status ets_index_scores(const void* q, int64_t q_b, int64_t q_t, int64_t q_h
                             const int32_t* seq_lens, int32_t page_size, int32_t L, float* out,
                             int64_t out_stride, int32_t dtype, void* stream) {
   using namespace ets;
-  if (B < 0 || T < 0 || H < 1 || H > ETS_MAX_INDEX_HEADS || D < kCacheBlock || D % kCacheBlock ||
+  if (B < 0 || B > 65535 || T < 0 || H < 1 || H > ETS_MAX_INDEX_HEADS || D < kCacheBlock || D % kCacheBlock ||
       D > ETS_MAX_INDEX_DIM || S < 0 || S > INT32_MAX || page_size < 1 || L < 0 || out_stride < L ||
       (dtype != ETS_BF16 && dtype != ETS_FP16) ||
       codes_s < 0 || codes_s > UINT32_MAX || scales_s < 0 || scales_s > UINT32_MAX || static_cast<int64_t>(B) * ((static_cast<int64_t>(L) + kFill - 1) / kFill) > INT32_MAX)
