@@ -392,8 +392,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendParams p
 
 template <class T, int RT, int NC, bool SHARED>
 void launch(const AttendParams& p, hipStream_t s) {
-  const uint32_t grid = attend_grid(p);
-  hipLaunchKernelGGL((attend_wide_kernel<T, RT, NC, SHARED>), dim3(grid), dim3(kThreads),
+  hipLaunchKernelGGL((attend_wide_kernel<T, RT, NC, SHARED>), dim3(attend_grid(p)), dim3(kThreads),
                      sizeof(WideLds<RT, SHARED, Mat<T>::kRowScale>), s, p);
 }
 

@@ -8,8 +8,9 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = 4;
-constexpr int kTile = 64;           // keys of a wave's step, held in registers
-constexpr int kUnit = kWaves * kTile;  // keys by which the work is dealt out
+constexpr int kSub = 2;             // 16-key tiles of a wave's step
+constexpr int kTile = 16 * kSub;    // keys of a wave's step, held in registers
+constexpr int kUnit = 256;          // keys by which the work is dealt out
 constexpr int kPiece = 2048;        // keys of a workgroup between barriers
 constexpr int kFill = 1024;         // positions past a length that are filled at a time
 constexpr int kQueryBytes = 65536;  // queries that a workgroup keeps in LDS
@@ -29,25 +30,26 @@ struct ScoreParams {
   const int32_t* table;
   int64_t pt_b;
   const int32_t* lens;
-  FastDiv by_page, by_fills;
+  FastDiv by_page, by_fills, by_head_tiles;
   float* out;
   int64_t out_stride;
 };
 
-// The keys stay, the queries stream: a wave brings 64 keys from global memory
+// The keys stay, the queries stream: a wave brings 32 keys from global memory
 // straight into matrix operands (lane l holds 16 consecutive codes of key l %
 // 16 for every 64 channels; the order of the channels inside a product is
 // free, and the queries are laid out in LDS in the same one), then takes the
-// 16-row query tiles from LDS one by one, each feeding 4 * D / 32 matrix
-// instructions.  Rows of the result are heads, columns keys, so the weighted
+// 16-row query tiles from LDS one by one, each feeding 2 * D / 32 matrix
+// instructions (64 keys a step halve the LDS reads, but leave three waves a SIMD
+// in the place of four: 60 us against 58).  Rows of the result are heads, columns keys, so the weighted
 // sum over heads runs down a lane's registers and over four lanes at the end.
 //
 // The lengths are known on the device only.  All keys, in units of 256, are
 // numbered through the batch and dealt out to the workgroups in equal runs: a
 // grid by sequence and chunk left a quarter of it idle with lengths between L
-// / 2 and L (64 x 32768: 61 us against 45).  FULL: D is 64 NP.
+// / 2 and L.  FULL: D is 64 NP.
 template <class T, int NP, bool FULL>
-__global__ __launch_bounds__(kThreads, NP <= 2 ? 3 : NP == 3 ? 2 : 1) void scores_kernel(ScoreParams p) {
+__global__ __launch_bounds__(kThreads, NP <= 2 ? 4 : NP == 3 ? 3 : 2) void scores_kernel(ScoreParams p) {
   typedef Mat<T> M;
   typedef typename M::V8 V8;
   extern __shared__ __align__(16) char lds[];
@@ -108,14 +110,14 @@ __global__ __launch_bounds__(kThreads, NP <= 2 ? 3 : NP == 3 ? 2 : 1) void score
   // byte; rows and channels that are not there come from kNothing, without a branch
   const uint64_t nothing = reinterpret_cast<uint64_t>(&kNothing[0]);
   const uint64_t kc = reinterpret_cast<uint64_t>(p.codes) + 16 * g, ks = reinterpret_cast<uint64_t>(p.scales) + (g >> 1);
-  u32v4 raw[4][NP];
-  uint32_t byte[4][NP];
+  u32v4 raw[kSub][NP];
+  uint32_t byte[kSub][NP];
   auto fetch = [&](int k) {
-    int32_t slot[4];
+    int32_t slot[kSub];
 #pragma unroll
-    for (int s = 0; s < 4; ++s) slot[s] = slots[min(k, kPiece - kTile) + 16 * s + col];
+    for (int s = 0; s < kSub; ++s) slot[s] = slots[min(k, kPiece - kTile) + 16 * s + col];
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
+    for (int s = 0; s < kSub; ++s) {
       const bool there = slot[s] >= 0 && k < kPiece;
       const uint64_t at = static_cast<uint32_t>(slot[s]), c0 = kc + at * p.codes_s, b0 = ks + at * p.scales_s;
       const uint64_t c1 = there ? c0 : nothing, b1 = there ? b0 : nothing;
@@ -137,26 +139,41 @@ __global__ __launch_bounds__(kThreads, NP <= 2 ? 3 : NP == 3 ? 2 : 1) void score
     }
     const int keys = min(static_cast<int>(min(todo * kUnit, static_cast<int64_t>(kPiece))), n - k0);
     __syncthreads();  // the piece before has been read
-    for (int i = threadIdx.x; i < kPiece; i += kThreads) {
-      const int j = min(k0 + i, n - 1);  // past the piece's keys: any of its slots, not used
-      const uint32_t page = div_by(j, p.by_page);
-      const int64_t s = static_cast<int64_t>(p.table[b * p.pt_b + page]) * p.by_page.d + (j - page * p.by_page.d);
-      slots[i] = i < keys && s >= 0 && s < p.S ? static_cast<int32_t>(s) : -1;
+    // all of a lane's loads first: one wait in the place of eight (four for the queries)
+    constexpr int kEach = kPiece / kThreads;
+    int32_t page_id[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int j = min(k0 + static_cast<int>(threadIdx.x) + i * kThreads, n - 1);  // past the piece's keys: any page of its, not used
+      page_id[i] = p.table[b * p.pt_b + div_by(j, p.by_page)];
     }
     if (new_b) {
-      for (int i = threadIdx.x; i < tiles * NP * 128; i += kThreads) {
-        const int l = i & 63, half = (i >> 6) & 1, tp = i >> 7;
-        const int tile = tp / NP, pair = tp - tile * NP, t = tile / p.head_tiles;
-        const int h = (tile - t * p.head_tiles) * 16 + (l & 15), d = 64 * pair + 16 * (l >> 4) + 8 * half;
-        V8 v = {};
-        if (h < p.H && d < p.D)
-          v = load_any<V8>(p.q + b * p.q_b + (t0 + t) * p.q_t + h * p.q_h + static_cast<int64_t>(d) * 2);
-        qs[i] = v;
+      constexpr int kQueries = 4;
+      for (int base = threadIdx.x; base < tiles * NP * 128; base += kQueries * kThreads) {
+        V8 v[kQueries];
+#pragma unroll
+        for (int u = 0; u < kQueries; ++u) {
+          const int i = base + u * kThreads, l = i & 63, half = (i >> 6) & 1, tp = i >> 7;
+          const int tile = tp / NP, pair = tp - tile * NP, t = static_cast<int>(div_by(tile, p.by_head_tiles));
+          const int h = (tile - t * p.head_tiles) * 16 + (l & 15), d = 64 * pair + 16 * (l >> 4) + 8 * half;
+          v[u] = V8{};
+          if (tile < tiles && h < p.H && d < p.D)
+            v[u] = load_any<V8>(p.q + b * p.q_b + (t0 + t) * p.q_t + h * p.q_h + static_cast<int64_t>(d) * 2);
+        }
+#pragma unroll
+        for (int u = 0; u < kQueries; ++u)
+          if (base + u * kThreads < tiles * NP * 128) qs[base + u * kThreads] = v[u];
       }
       for (int i = threadIdx.x; i < tiles * 16; i += kThreads) {
-        const int t = (i >> 4) / p.head_tiles, h = i - t * p.head_tiles * 16;
+        const int t = static_cast<int>(div_by(i >> 4, p.by_head_tiles)), h = i - t * p.head_tiles * 16;
         ws[i] = h < p.H ? p.w[b * p.w_b + (t0 + t) * p.w_t + h] : 0.0f;
       }
+    }
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int at = static_cast<int>(threadIdx.x) + i * kThreads, j = min(k0 + at, n - 1);
+      const int64_t s = static_cast<int64_t>(page_id[i]) * p.by_page.d + (j - div_by(j, p.by_page) * p.by_page.d);
+      slots[at] = at < keys && s >= 0 && s < p.S ? static_cast<int32_t>(s) : -1;
     }
     new_b = false;
     __syncthreads();
@@ -165,18 +182,19 @@ __global__ __launch_bounds__(kThreads, NP <= 2 ? 3 : NP == 3 ? 2 : 1) void score
   fetch(k);
   hold(byte);  // else the loop carries 8-bit values and widens them as soon as they are loaded
   // Sums leave a step later, before the next rows are asked for: a store behind them would be waited for with them.
-  float* own = held + wave * p.tokens * kTile + lane;
-  float* out = p.out + (static_cast<int64_t>(b) * p.T + t0) * p.out_stride + k0 + lane;
+  float* own = held + wave * p.tokens * 64 + lane;
+  float* out = p.out + (static_cast<int64_t>(b) * p.T + t0) * p.out_stride + k0;
   auto leave = [&](int at) {
-    if (at >= 0 && at + lane < keys)
-      for (int t = 0; t < tokens; ++t) out[t * p.out_stride + at] = own[t * kTile];
+    const int key = at + 16 * (lane >> 5) + col;
+    if (at >= 0 && key < keys && !(g & 1))
+      for (int t = 0; t < tokens; ++t) out[t * p.out_stride + key] = own[t * 64];
   };
   for (; k < keys; k += kWaves * kTile) {
-    V8 key[4][NP][2];
-    uint32_t top[4];
+    V8 key[kSub][NP][2];
+    uint32_t top[kSub];
     hold(raw), hold(byte);
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
+    for (int s = 0; s < kSub; ++s) {
       top[s] = 0;
       if constexpr (M::kRowScale) {
 #pragma unroll
@@ -192,41 +210,36 @@ __global__ __launch_bounds__(kThreads, NP <= 2 ? 3 : NP == 3 ? 2 : 1) void score
     }
     leave(k - kWaves * kTile);
     fetch(k + kWaves * kTile);
-    const bool seen = slots[k + lane] >= 0;
+    const bool seen = slots[k + 16 * (lane >> 5) + col] >= 0;
     float size = 1.0f;
-    if (M::kRowScale) {
-      const uint32_t r = g == 0 ? top[0] : g == 1 ? top[1] : g == 2 ? top[2] : top[3];
-      size = __uint_as_float(r << 23);
-    }
+    if (M::kRowScale) size = __uint_as_float((lane < 32 ? top[0] : top[1]) << 23);
     int tile = 0;
     for (int t = 0; t < tokens; ++t) {
-      float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      float part[kSub] = {};
       for (int i = 0; i < p.head_tiles; ++i, ++tile) {
-        f32x4 acc[4] = {};
+        f32x4 acc[kSub] = {};
 #pragma unroll
         for (int j = 0; j < NP; ++j) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const V8 q = qs[((tile * NP + j) * 2 + h) * 64 + lane];
 #pragma unroll
-            for (int s = 0; s < 4; ++s) acc[s] = M::mma(q, key[s][j][h], acc[s]);
+            for (int s = 0; s < kSub; ++s) acc[s] = M::mma(q, key[s][j][h], acc[s]);
           }
         }
         const f32x4 w = *reinterpret_cast<const f32x4*>(ws + tile * 16 + 4 * g);
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
+        for (int s = 0; s < kSub; ++s)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             part[s] = fmaf(w[e], __builtin_elementwise_maximum(acc[s][e], 0.0f), part[s]);
       }
-      // over the four lanes of a key, leaving key 16 s + col in the lanes of row s
-      const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(part[0]), __float_as_uint(part[2]), false, false);
-      const auto c = __builtin_amdgcn_permlane32_swap(__float_as_uint(part[1]), __float_as_uint(part[3]), false, false);
-      const float x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
-      const float y = __uint_as_float(c[0]) + __uint_as_float(c[1]);
-      const auto e = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(y), false, false);
-      const float sum = (__uint_as_float(e[0]) + __uint_as_float(e[1])) * size;
-      own[t * kTile] = seen ? sum : kNegInf;
+      // over the four lanes of a key: key col of the first half in lanes 0 to 31, of the second in the others
+      const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(part[0]), __float_as_uint(part[1]), false, false);
+      const uint32_t x = __float_as_uint(__uint_as_float(a[0]) + __uint_as_float(a[1]));
+      const auto c = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+      const float sum = (__uint_as_float(c[0]) + __uint_as_float(c[1])) * size;
+      own[t * 64] = seen ? sum : kNegInf;
     }
   }
   leave(k - kWaves * kTile);
@@ -284,6 +297,7 @@ ets_status ets_index_scores(const void* q, int64_t q_b, int64_t q_t, int64_t q_h
   p.w = weights, p.w_b = w_b, p.w_t = w_t;
   p.B = B, p.T = T, p.H = H, p.D = D, p.L = L;
   p.head_tiles = (H + 15) / 16;
+  p.by_head_tiles = fast_div(p.head_tiles);
   const int room = kQueryBytes / (np * 2048) / p.head_tiles;
   p.tokens = T < room ? T : room;
   const int groups = (T + p.tokens - 1) / p.tokens;
@@ -293,10 +307,12 @@ ets_status ets_index_scores(const void* q, int64_t q_b, int64_t q_t, int64_t q_h
   p.by_page = fast_div(page_size);
   p.out = out, p.out_stride = out_stride;
   p.by_fills = fast_div(static_cast<uint32_t>((static_cast<int64_t>(L) + kFill - 1) / kFill));
-  // as many workgroups as the device holds at once, over the groups of tokens
-  const int64_t most = (static_cast<int64_t>(L) + kUnit - 1) / kUnit * B, fits = (3 * cu + groups - 1) / groups;
+  // as many workgroups as the device holds at once (registers, LDS), over the groups of tokens
   const int tiles = p.tokens * p.head_tiles;
   const size_t lds = static_cast<size_t>(tiles) * np * 2048 + tiles * 64 + kPiece * 4 + p.tokens * kThreads * 4;
+  const int64_t by_regs = np <= 2 ? 4 : np == 3 ? 3 : 2, by_lds = 160 * 1024 / (static_cast<int64_t>(lds) + 512);
+  const int64_t most = (static_cast<int64_t>(L) + kUnit - 1) / kUnit * B;
+  const int64_t fits = ((by_regs < by_lds ? by_regs : by_lds) * cu + groups - 1) / groups;
   const dim3 grid(static_cast<uint32_t>(most < fits ? most : fits), groups);
   auto s = static_cast<hipStream_t>(stream);
   if (dtype == ETS_BF16) {
