@@ -1,4 +1,8 @@
-"""The decode operators on the GPU against the plain 64-bit forms of tests/decode_reference.py."""
+"""The decode operators on the GPU against the plain 64-bit forms of tests/decode_reference.py.
+
+Run after test_gpu_dispatch.py (by its name): that file's check that workgroup i runs on XCD i % X holds in a process
+whose launches so far leave the dealing at XCD 0, which grids of any size do not.
+"""
 import math
 
 import pytest
