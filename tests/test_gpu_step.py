@@ -512,3 +512,40 @@ def test_refusals():
     ]:
         with pytest.raises(error):
             call()
+
+
+def test_the_example_step():
+    """examples/sparse_decode.py: graph replays follow the eager steps, and the attention is that of the chosen slots."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "sparse_decode.py")
+    spec = importlib.util.spec_from_file_location("sparse_decode", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+
+    def decoder():
+        d = example.SparseDecoder(3, 300, 32, heads=16, index_heads=8, page=16)
+        d.prefill(100)
+        d.project()
+        return d
+
+    a, b = decoder(), decoder()
+    graph, held = a.capture()
+    for step in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        out, lse = held[0].clone(), held[1].clone()
+        b.step()
+        assert torch.equal(a.lens, b.lens) and int(a.lens[0]) == 101 + step
+        assert torch.equal(a.codes.view(torch.uint8), b.codes.view(torch.uint8)) and torch.equal(a.index_scales, b.index_scales)
+        assert torch.equal(a.scores, b.scores)
+        assert torch.equal(a.chosen.sort(1).values, b.chosen.sort(1).values)
+        # the slots chosen are those of the 32 highest scores
+        top = a.scores[:, :300].topk(32, sorted=False).indices.cpu()
+        slots = torch.stack([ref.slots_of(a.table.cpu()[i], 16, top[i]) for i in range(3)])
+        assert torch.equal(a.chosen.cpu().long().sort(1).values, slots.sort(1).values)
+        q = ets.rope(a.q, a.lens - 1, a.inv_freq, offset=example.LATENT).cpu()[:, None]
+        kc, ks = a.codes.cpu(), a.scales.cpu()
+        want = ref.attend(q, kc, ks, kc[..., :512], ks[..., :16], [[a.chosen.cpu()[i]] for i in range(3)])
+        close(out[:, None], want[0], want[2], BF16)
+        close(lse[:, None], want[1], want[3], FP32)
