@@ -17,7 +17,7 @@ constexpr int kPlane = 16 * kPieces; // bytes of one half of each decoded piece 
 // apart, so that the 16 rows of an operand load fill all 64.
 constexpr int kPitch = 2 * kPlane + 16;
 constexpr int kDepth = 2;            // tiles on their way from memory
-constexpr float kSlack = 8.0f;       // how far (log2) a score may pass its reference
+constexpr float kSlack = 24.0f;      // how far (log2) a score may pass its reference
 
 // Pieces of a tile on their way through a lane, and their scale bytes.
 template <int N>
@@ -52,7 +52,7 @@ struct WideLds {
 // has one barrier; within it one wave lays out rows while the other multiplies.
 //
 // The softmax is taken relative to a whole-numbered reference that each team
-// raises only when a score passes it by more than 2^8, and that follows the
+// raises only when a score passes it by more than 2^24, and that follows the
 // other team's of the step before.  Where a reference has changed, or the two
 // differ, sums and probabilities are brought together by powers of two, which
 // is exact; that happens a few times a list.
@@ -126,8 +126,6 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendParams p
     if ((tid & 31) == 0) lds.seen[i & 7] = static_cast<uint32_t>(seen >> (tid & 32));
   };
 
-  if (tid < 4 * kTile) keep(tid >> 5, ask(tid >> 5));
-  __syncthreads();
   auto begin = [&](auto& kset, auto& vset) {  // before the first step: tiles 0 and 1 in LDS (values: 0)
     bring_k(kset[0], 0);
     bring_k(kset[1], 1);
@@ -195,12 +193,17 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendParams p
           }
         }
       if (r < p.rows && a.tree_slots) tree_bits[m] = static_cast<uint64_t>(a.tree_mask[spot.b * a.mask_b + t]);
+      lds.ref[1][team][(MQ * hg + m) * 16 + col] = kNegInf;
     }
+    __syncthreads();
     float ref[MQ], sum[MQ];
 #pragma unroll
     for (int m = 0; m < MQ; ++m) ref[m] = kNegInf, sum[m] = 0.0f;
 
     auto scores = [&](int i, const uint8_t* tile) {
+      float other[MQ];  // the other team's reference of the step before
+#pragma unroll
+      for (int m = 0; m < MQ; ++m) other[m] = lds.ref[(i & 1) ^ 1][team ^ 1][(MQ * hg + m) * 16 + col];
       f32x4 x[MQ], x1[MQ];  // two sums each: half as long a chain of products
 #pragma unroll
       for (int m = 0; m < MQ; ++m) x[m] = f32x4{}, x1[m] = f32x4{};
@@ -220,34 +223,50 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendParams p
         }
         if (n + kAhead < 2 * kPairs) k[n % kAhead] = operand(n + kAhead);
       }
+      // y: what goes into the exponential.  First as if all keys were seen and the reference stayed.
       const int at = spot.first + i, half = i & 1;
-      const uint32_t seen = lds.seen[i & 7] >> (16 * team);
+      const uint32_t seen = (__builtin_amdgcn_readfirstlane(lds.seen[i & 7]) >> (16 * team)) & 0xffffu;
+      f32x4 y[MQ];
+      bool stays = true;
+#pragma unroll
+      for (int m = 0; m < MQ; ++m) {
+        x[m] += x1[m];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[m][e] = __builtin_fmaf(x[m][e], p.scale_log2, -ref[m]);
+        const float high = fmaxf(fmaxf(y[m][0], y[m][1]), fmaxf(y[m][2], y[m][3]));
+        stays = stays && high <= kSlack && other[m] <= ref[m];
+      }
+      if (seen != 0xffffu || at >= spot.main_tiles || !__all(stays)) {
+#pragma unroll
+        for (int m = 0; m < MQ; ++m) {
+          uint32_t vis = seen;
+          if (at >= spot.main_tiles) vis &= static_cast<uint32_t>(tree_bits[m] >> (kTile * (at - spot.main_tiles) + 16 * team));
+          vis >>= 4 * g;
+          float high = kNegInf;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            x[m][e] = (vis >> e) & 1 ? x[m][e] * p.scale_log2 : kNegInf;
+            high = fmaxf(high, x[m][e]);
+          }
+          high = rows_max(high);
+          float next = fmaxf(ref[m], other[m]);
+          if (high > next + kSlack || next == kNegInf) next = ceilf(high);
+          sum[m] *= ref[m] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(ref[m] - next);
+          ref[m] = next;
+          y[m] = x[m] - (next == kNegInf ? 0.0f : next);
+        }
+      }
 #pragma unroll
       for (int m = 0; m < MQ; ++m) {
         const int rt = MQ * hg + m;
-        uint32_t vis = seen;
-        if (at >= spot.main_tiles) vis &= static_cast<uint32_t>(tree_bits[m] >> (kTile * (at - spot.main_tiles) + 16 * team));
-        vis >>= 4 * g;
-        float y[4], high = kNegInf;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          y[e] = (vis >> e) & 1 ? (x[m][e] + x1[m][e]) * p.scale_log2 : kNegInf;
-          high = fmaxf(high, y[e]);
-        }
-        high = rows_max(high);
-        float next = i ? fmaxf(ref[m], lds.ref[half ^ 1][team ^ 1][rt * 16 + col]) : ref[m];
-        if (high > next + kSlack || next == kNegInf) next = ceilf(high);
-        sum[m] *= ref[m] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(ref[m] - next);
-        ref[m] = next;
-        if (g == 0) lds.ref[half][team][rt * 16 + col] = next;
-        const float base = next == kNegInf ? 0.0f : next;
+        if (g == 0) lds.ref[half][team][rt * 16 + col] = ref[m];
         B4 prob, rest;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          y[e] = __builtin_amdgcn_exp2f(y[e] - base);
-          sum[m] += y[e];
-          prob[e] = static_cast<__bf16>(y[e]);
-          if constexpr (kTwo) rest[e] = static_cast<__bf16>(y[e] - static_cast<float>(prob[e]));
+          const float z = __builtin_amdgcn_exp2f(y[m][e]);
+          sum[m] += z;
+          prob[e] = static_cast<__bf16>(z);
+          if constexpr (kTwo) rest[e] = static_cast<__bf16>(z - static_cast<float>(prob[e]));
         }
         lds.prob[half][0][team][rt][lane] = __builtin_bit_cast(u32v2, prob);
         if constexpr (kTwo) lds.prob[half][1][team][rt][lane] = __builtin_bit_cast(u32v2, rest);
@@ -344,6 +363,8 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendParams p
     }
   };
 
+  if (tid - 256 < 4 * kTile) keep((tid - 256) >> 5, ask((tid - 256) >> 5));
+  __syncthreads();
   Pieces<4> kset[kDepth], vset[SHARED ? 1 : kDepth];
   begin(kset, vset);
   __syncthreads();
