@@ -11,6 +11,9 @@ constexpr int kAttendThreads = 256;
 constexpr int kAttendWaves = 4;
 constexpr int kAttendTile = 32;  // keys of a step
 constexpr float kNegInf = -__builtin_inff();
+// How far (log2) a score may pass the reference that its softmax is taken relative to, before the reference
+// follows: probabilities up to 2^24 are as exact as those up to 1, and a list raises its reference once or twice.
+constexpr float kSlack = 24.0f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
 struct AttendParams {

@@ -219,28 +219,39 @@ __global__ __launch_bounds__(kThreads, MT == 1 && NP <= 2 ? 3 : 1) void attend_k
     bf16x8 prob[MT], rest[MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      uint32_t vis = seen_now;
-      if (tile >= main_tiles) vis &= static_cast<uint32_t>(tree_bits[m] >> (kTile * (tile - main_tiles) & 63));
-      vis >>= 4 * g;  // bits 0..3: keys 4 g + e; bits 16..19: keys 16 + 4 g + e
+      // x: what goes into the exponential.  First as if all keys were seen and the reference stayed.
       float x[8], high = kNegInf;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        x[j] = score[m][j >> 2][j & 3] * p.scale_log2;
-        x[j] = (vis >> (16 * (j >> 2) + (j & 3))) & 1 ? x[j] : kNegInf;
+        x[j] = __builtin_fmaf(score[m][j >> 2][j & 3], p.scale_log2, -top[m]);
         high = fmaxf(high, x[j]);
       }
-      high = fmaxf(rows_max(high), top[m]);
-      const float base = high == kNegInf ? 0.0f : high;
-      if (__any(high > top[m])) {
-        const float fade = __builtin_amdgcn_exp2f(top[m] - base);
-        sum[m] *= fade;
+      if (seen_now != ~0u || tile >= main_tiles || !__all(high <= kSlack)) {
+        uint32_t vis = seen_now;
+        if (tile >= main_tiles) vis &= static_cast<uint32_t>(tree_bits[m] >> (kTile * (tile - main_tiles) & 63));
+        vis >>= 4 * g;  // bits 0..3: keys 4 g + e; bits 16..19: keys 16 + 4 g + e
+        high = kNegInf;
 #pragma unroll
-        for (int c = 0; c < 4 * NV; ++c) out[m][c] *= fade;
-        top[m] = high;
+        for (int j = 0; j < 8; ++j) {
+          x[j] = (vis >> (16 * (j >> 2) + (j & 3))) & 1 ? score[m][j >> 2][j & 3] * p.scale_log2 : kNegInf;
+          high = fmaxf(high, x[j]);
+        }
+        high = rows_max(high);
+        if (__any(high > top[m] + kSlack || top[m] == kNegInf)) {
+          const float next = high > top[m] + kSlack || top[m] == kNegInf ? high : top[m];
+          const float fade = __builtin_amdgcn_exp2f(top[m] - (next == kNegInf ? 0.0f : next));
+          sum[m] *= fade;
+#pragma unroll
+          for (int c = 0; c < 4 * NV; ++c) out[m][c] *= fade;
+          top[m] = next;
+        }
+        const float base = top[m] == kNegInf ? 0.0f : top[m];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] -= base;
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        x[j] = __builtin_amdgcn_exp2f(x[j] - base);
+        x[j] = __builtin_amdgcn_exp2f(x[j]);
         sum[m] += x[j];
         prob[m][j] = static_cast<__bf16>(x[j]);
         if constexpr (kTwo) rest[m][j] = static_cast<__bf16>(x[j] - static_cast<float>(prob[m][j]));

@@ -17,7 +17,6 @@ constexpr int kPlane = 16 * kPieces; // bytes of one half of each decoded piece 
 // apart, so that the 16 rows of an operand load fill all 64.
 constexpr int kPitch = 2 * kPlane + 16;
 constexpr int kDepth = 2;            // tiles on their way from memory
-constexpr float kSlack = 24.0f;      // how far (log2) a score may pass its reference
 
 // Pieces of a tile on their way through a lane, and their scale bytes.
 template <int N>

@@ -355,6 +355,25 @@ def test_attention(case, dtype):
     assert torch.equal(out, out2) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("order", ["rising", "falling", "mixed"])
+@pytest.mark.parametrize("shape", [(64, 1, 128, 128), (16, 2, 64, 64), (128, 1, 576, 512), (8, 1, 320, 64)])
+def test_attention_of_scores_far_apart(shape, order, dtype):
+    """Sizes of keys over 2^12, so that scores pass each other by far more than a softmax reference lets them."""
+    Hq, Hkv, D, Dv = shape
+    g, n = gen(12), 500
+    x = torch.randn(n, Hkv, D, generator=g, dtype=torch.float64) * 2.0 ** (12 * torch.arange(n).double() / n - 4).view(n, 1, 1)
+    codes, scales = ref.quantise(x)
+    vc, vs = ref.quantise(torch.randn(n, Hkv, Dv, generator=g, dtype=torch.float64))
+    slots = {"rising": torch.arange(n), "falling": torch.arange(n).flip(0), "mixed": torch.randperm(n, generator=g)}[order]
+    q = torch.randn(1, 1, Hq, D, generator=g).to(dtype)
+    out, lse, eo, el = ref.attend(q, codes, scales, vc, vs, [[slots]])
+    got, l = ets.attend_selected(q.to(dev()), codes.to(dev()), scales.to(dev()), vc.to(dev()), vs.to(dev()),
+                                 slots.to(torch.int32).view(1, 1, n).to(dev()))
+    close(got, out, eo, dtype)
+    close(l, lse, el, FP32)
+
+
 def test_attention_row_that_sees_nothing():
     """No valid slot, an empty tree line, and a slot outside the cache: out 0 and lse -inf, next to rows that see something."""
     g = gen(11)
