@@ -90,16 +90,18 @@ __global__ __launch_bounds__(kThreads, MT == 1 && NP <= 2 ? 3 : 1) void attend_k
 
   // A tile's rows on their way: lane (key col of either half, row g) brings codes 64 i + 16 g .. + 15 and their
   // scale byte.  Rows and channels that are not there come from kNothing, without a branch.
+  typedef RowScales<NP, FULL> KS;
+  typedef RowScales<NV, FULL> VS;
   const uint64_t nothing = reinterpret_cast<uint64_t>(&kNothing[0]);
   const uint64_t kc = reinterpret_cast<uint64_t>(a.k_codes + hk * a.k_h + 16 * g);
-  const uint64_t ks = reinterpret_cast<uint64_t>(a.k_scales + hk * a.ks_h + (g >> 1));
+  const uint64_t ks = KS::start(reinterpret_cast<uint64_t>(a.k_scales + hk * a.ks_h), g);
   const uint64_t vc = reinterpret_cast<uint64_t>(a.v_codes + hk * a.v_h + 16 * g);
-  const uint64_t vs = reinterpret_cast<uint64_t>(a.v_scales + hk * a.vs_h + (g >> 1));
+  const uint64_t vs = VS::start(reinterpret_cast<uint64_t>(a.v_scales + hk * a.vs_h), g);
   const uint32_t k_row = static_cast<uint32_t>(a.k_s), ks_row = static_cast<uint32_t>(a.ks_s);
   const uint32_t v_row = static_cast<uint32_t>(a.v_s), vs_row = static_cast<uint32_t>(a.vs_s);
   struct Rows {
     u32v4 k[2][NP], v[2][NV];
-    uint32_t kbyte[2][NP], vbyte[2][NV];
+    uint32_t kbyte[2][KS::n], vbyte[2][VS::n];
     uint32_t seen;  // keys that are there
   };
 
@@ -138,17 +140,17 @@ __global__ __launch_bounds__(kThreads, MT == 1 && NP <= 2 ? 3 : 1) void attend_k
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         const bool in = FULL || 64 * i + 16 * g < a.D;
-        const uint64_t c = k + 64 * i, b = kb + 2 * i;
+        const uint64_t c = k + 64 * i;
         rows.k[s][i] = load_global<u32v4>(in ? c : nothing);
-        rows.kbyte[s][i] = load_global<uint8_t>(in ? b : nothing);
       }
+      KS::load(rows.kbyte[s], kb, nothing, [&](int i) { return 64 * i + 16 * g < a.D; });
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const bool in = FULL || 64 * i + 16 * g < a.Dv;
-        const uint64_t c = v + 64 * i, b = vb + 2 * i;
+        const uint64_t c = v + 64 * i;
         rows.v[s][i] = load_global<u32v4>(in ? c : nothing);
-        rows.vbyte[s][i] = load_global<uint8_t>(in ? b : nothing);
       }
+      VS::load(rows.vbyte[s], vb, nothing, [&](int i) { return 64 * i + 16 * g < a.Dv; });
     }
   };
 
@@ -171,17 +173,13 @@ __global__ __launch_bounds__(kThreads, MT == 1 && NP <= 2 ? 3 : 1) void attend_k
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       uint32_t r = 0;
-      if constexpr (M::kRowScale) {
-#pragma unroll
-        for (int i = 0; i < NP; ++i) r = max(r, now.kbyte[s][i]);
-        r = __float_as_uint(rows_max(__uint_as_float(r << 23))) >> 23;  // bytes as powers of two keep their order
-      }
+      if constexpr (M::kRowScale) r = row_top<NP, FULL>(now.kbyte[s]);
       row_scale[s] = __uint_as_float(r << 23);
 #pragma unroll
       for (int m = 0; m < MT; ++m) score[m][s] = f32x4{};
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
-        const float f = M::scale(now.kbyte[s][i], r);
+        const float f = M::scale(KS::byte(now.kbyte[s], i, g), r);
         const u32v4 c = now.k[s][i];
         const V8 k0 = M::keys(c[0], c[1], f), k1 = M::keys(c[2], c[3], f);
 #pragma unroll
@@ -197,7 +195,7 @@ __global__ __launch_bounds__(kThreads, MT == 1 && NP <= 2 ? 3 : 1) void attend_k
       char* dst = values + (16 * s + col) * kPitch + 16 * g;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const float f = __uint_as_float(now.vbyte[s][i] << 23);
+        const float f = __uint_as_float(VS::byte(now.vbyte[s], i, g) << 23);
         const u32v4 c = now.v[s][i];
         *reinterpret_cast<bf16x8*>(dst + 64 * i) = codes_bf16(c[0], c[1], f);
         *reinterpret_cast<bf16x8*>(dst + kPlane + 64 * i) = codes_bf16(c[2], c[3], f);

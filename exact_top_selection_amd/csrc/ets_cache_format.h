@@ -57,6 +57,37 @@ __device__ __forceinline__ void hold(V (&x)[A][B]) {
     for (int j = 0; j < B; ++j) asm volatile("" : "+v"(x[i][j]));
 }
 
+// The scale bytes of a row on their way through the lanes that hold it (lane row g: codes 64 i + 16 g .. + 15).  A
+// row of 2 NP bytes (FULL; NP 1, 2 or 4) comes in one load that its four lanes share, other rows byte by byte.
+template <int NP, bool FULL>
+struct RowScales {
+  static constexpr bool kWhole = FULL && NP != 3;
+  static constexpr int n = kWhole ? (NP + 1) / 2 : NP;  // registers
+  // where a lane starts to read
+  static __device__ __forceinline__ uint64_t start(uint64_t row, int g) { return kWhole ? row : row + (g >> 1); }
+  // w <- the bytes at `from`; a byte of a step i that `in` does not have is read from `nothing`
+  template <class In>
+  static __device__ __forceinline__ void load(uint32_t (&w)[n], uint64_t from, uint64_t nothing, In in) {
+    if constexpr (kWhole && NP == 1) {
+      w[0] = load_global<uint16_t>(from);
+    } else if constexpr (kWhole && NP == 2) {
+      w[0] = load_global<uint32_t>(from);
+    } else if constexpr (kWhole) {
+      const u32v2 two = load_global<u32v2>(from);
+      w[0] = two[0], w[1] = two[1];
+    } else {
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const uint64_t b = from + 2 * i;
+        w[i] = load_global<uint8_t>(in(i) ? b : nothing);
+      }
+    }
+  }
+  static __device__ __forceinline__ uint32_t byte(const uint32_t (&w)[n], int i, int g) {
+    return kWhole ? __builtin_amdgcn_ubfe(w[kWhole ? i / 2 : i], 16 * (i & 1) + 8 * (g >> 1), 8) : w[i];
+  }
+};
+
 // n / d for 0 <= n < 2^31 and a divisor d >= 1 fixed at launch: with l =
 // ceil(log2 d) and m = ceil(2^(31 + l) / d), n * m / 2^(31 + l) exceeds n / d
 // by less than n / 2^(31 + l) <= 1 / d, so the floor is exact.  d lies in
@@ -92,6 +123,22 @@ __device__ __forceinline__ float rows_max(float x) {
   const uint32_t c = __float_as_uint(y);
   const auto t = __builtin_amdgcn_permlane16_swap(c, c, false, false);
   return fmaxf(__uint_as_float(t[0]), __uint_as_float(t[1]));
+}
+
+// The largest scale byte of a row, in all of its lanes (bytes as powers of two keep their order).
+template <int NP, bool FULL>
+__device__ __forceinline__ uint32_t row_top(const uint32_t (&w)[RowScales<NP, FULL>::n]) {
+  typedef RowScales<NP, FULL> R;
+  uint32_t top = 0;
+  if constexpr (R::kWhole) {
+#pragma unroll
+    for (int i = 0; i < 2 * NP; ++i) top = max(top, __builtin_amdgcn_ubfe(w[i / 4], 8 * (i & 3), 8));
+    return top;
+  } else {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) top = max(top, w[i]);
+    return __float_as_uint(rows_max(__uint_as_float(top << 23))) >> 23;
+  }
 }
 
 // Eight codes (two words) to eight values times `scale`, a power of two.

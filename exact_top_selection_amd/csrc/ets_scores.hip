@@ -108,10 +108,11 @@ __global__ __launch_bounds__(kThreads, NP <= 2 ? 4 : NP == 3 ? 3 : 2) void score
 
   // a step's rows on their way: lane (key col of each 16, row g) brings codes 64 i + 16 g .. + 15 and their scale
   // byte; rows and channels that are not there come from kNothing, without a branch
+  typedef RowScales<NP, FULL> KS;
   const uint64_t nothing = reinterpret_cast<uint64_t>(&kNothing[0]);
-  const uint64_t kc = reinterpret_cast<uint64_t>(p.codes) + 16 * g, ks = reinterpret_cast<uint64_t>(p.scales) + (g >> 1);
+  const uint64_t kc = reinterpret_cast<uint64_t>(p.codes) + 16 * g, ks = KS::start(reinterpret_cast<uint64_t>(p.scales), g);
   u32v4 raw[kSub][NP];
-  uint32_t byte[kSub][NP];
+  uint32_t byte[kSub][KS::n];
   auto fetch = [&](int k) {
     int32_t slot[kSub];
 #pragma unroll
@@ -124,10 +125,10 @@ __global__ __launch_bounds__(kThreads, NP <= 2 ? 4 : NP == 3 ? 3 : 2) void score
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         const bool in = FULL || 64 * i + 16 * g < p.D;
-        const uint64_t c = c1 + 64 * i, b = b1 + 2 * i;
+        const uint64_t c = c1 + 64 * i;
         raw[s][i] = load_global<u32v4>(in ? c : nothing);
-        byte[s][i] = load_global<uint8_t>(in ? b : nothing);
       }
+      KS::load(byte[s], b1, nothing, [&](int i) { return 64 * i + 16 * g < p.D; });
     }
   };
 
@@ -196,14 +197,10 @@ __global__ __launch_bounds__(kThreads, NP <= 2 ? 4 : NP == 3 ? 3 : 2) void score
 #pragma unroll
     for (int s = 0; s < kSub; ++s) {
       top[s] = 0;
-      if constexpr (M::kRowScale) {
-#pragma unroll
-        for (int i = 0; i < NP; ++i) top[s] = max(top[s], byte[s][i]);
-        top[s] = __float_as_uint(rows_max(__uint_as_float(top[s] << 23))) >> 23;  // bytes as powers of two keep their order
-      }
+      if constexpr (M::kRowScale) top[s] = row_top<NP, FULL>(byte[s]);
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
-        const float f = M::scale(byte[s][i], top[s]);
+        const float f = M::scale(KS::byte(byte[s], i, g), top[s]);
         key[s][i][0] = M::keys(raw[s][i][0], raw[s][i][1], f);
         key[s][i][1] = M::keys(raw[s][i][2], raw[s][i][3], f);
       }
