@@ -10,7 +10,7 @@ constexpr int kThreads = 256;
 constexpr int kWaves = 4;
 constexpr int kSub = 2;             // 16-key tiles of a wave's step
 constexpr int kTile = 16 * kSub;    // keys of a wave's step, held in registers
-constexpr int kUnit = 256;          // keys by which the work is dealt out
+constexpr int kUnit = 128;          // keys by which the work is dealt out: a step of all waves
 constexpr int kPiece = 2048;        // keys of a workgroup between barriers
 constexpr int kFill = 1024;         // positions past a length that are filled at a time
 constexpr int kQueryBytes = 65536;  // queries that a workgroup keeps in LDS
@@ -40,14 +40,24 @@ struct ScoreParams {
 // 16 for every 64 channels; the order of the channels inside a product is
 // free, and the queries are laid out in LDS in the same one), then takes the
 // 16-row query tiles from LDS one by one, each feeding 2 * D / 32 matrix
-// instructions (64 keys a step halve the LDS reads, but leave three waves a SIMD
-// in the place of four: 60 us against 58).  Rows of the result are heads, columns keys, so the weighted
-// sum over heads runs down a lane's registers and over four lanes at the end.
+// instructions (64 keys a step halve the LDS reads, but leave three waves a
+// SIMD in the place of four: 60 us against 58).  Rows of the result are heads,
+// columns keys, so the weighted sum over heads runs down a lane's registers
+// and over four lanes at the end.
 //
-// The lengths are known on the device only.  All keys, in units of 256, are
+// The lengths are known on the device only.  All keys, in units of 128, are
 // numbered through the batch and dealt out to the workgroups in equal runs: a
 // grid by sequence and chunk left a quarter of it idle with lengths between L
-// / 2 and L.  FULL: D is 64 NP.
+// / 2 and L (67 us against 58).  FULL: D is 64 NP.
+//
+// Measured: 56 us for 64 sequences of up to 32768 positions, 64 heads of 128
+// channels (218 MB, 3.9 TB/s, 460 TFLOP/s), 44 us for 4 tokens of each of 4
+// sequences of up to 262144, 32 heads (129 MB, 640 TFLOP/s).  Beyond the
+// last-level cache a further 2^21 keys take 72 us with 1 head as with 64: it
+// is bound by how fast half lines of rows come in (4 TB/s), and with few keys
+// by three loads in turn (length, page, row), about 8 us before the first
+// product.  Several tokens add matrix and vector instructions, which share
+// the issue of a SIMD: a weighted sum is two vector instructions a product.
 template <class T, int NP, bool FULL>
 __global__ __launch_bounds__(kThreads, NP <= 2 ? 4 : NP == 3 ? 3 : 2) void scores_kernel(ScoreParams p) {
   typedef Mat<T> M;

@@ -22,7 +22,8 @@
  *     are checked on the device: one outside [0, S) is skipped by the write,
  *     read as zeros, and not seen by scores and attention.
  *   - Strides are in elements (bytes for codes and scales); the innermost
- *     dimension is contiguous.  No alignment beyond the element's is needed;
+ *     dimension is contiguous.  Strides from slot to slot of a cache that
+ *     scores and attention read are at most 2^32 - 1.  No alignment beyond the element's is needed;
  *     rows that start at multiples of 16 bytes are the fast ones.
  *   - Results do not change from run to run.
  */

@@ -115,6 +115,19 @@ def test_attend_refusals(lib):
     assert lib.ets_attend(None, None, 0, None) == INVALID
 
 
+def test_slot_strides_out_of_range(lib):
+    """Strides from slot to slot are 32-bit numbers in the kernels: others are refused, not cut short."""
+    from exact_top_selection_amd._decode import _AttendArgs
+    need = ctypes.c_size_t(0)
+    for bad in (-1, 1 << 32):
+        for codes_s, scales_s in ((bad, 2), (64, bad)):
+            assert lib.ets_index_scores(F, 256, 256, 64, F, 4, 4, 2, 1, 4, 64, F, codes_s, F, scales_s, 8, F, 2, F, 4, 8, F, 8, 0,
+                                        None) == INVALID
+        for name in ("k_s", "ks_s", "v_s", "vs_s"):
+            args = _AttendArgs(B=2, T=2, Hq=4, Hkv=2, D=64, Dv=64, dtype=0, K=8, L=8, page_size=4, S=16, **{name: bad})
+            assert lib.ets_attend_workspace_size(ctypes.byref(args), ctypes.byref(need)) == INVALID, name
+
+
 def test_binding_refuses_host_tensors():
     import exact_top_selection_amd as ets
     x = torch.zeros(2, 1, 32)
