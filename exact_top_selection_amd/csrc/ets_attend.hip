@@ -479,13 +479,13 @@ ets_status make_plan(const ets_attend_args* a, Plan* plan) {
   const int tiles = ((paged ? a->L : a->K) + kTile - 1) / kTile + p.tree_tiles;
   const int64_t lists = static_cast<int64_t>(p.units) * p.row_groups;
   // workgroups to fill the device with: a compute unit holds one of the wide kernel's and up to three of the
-  // narrow one's, but two read faster than three (8 sequences of 32768: 134 us against 145)
+  // narrow one's, but two read faster than three (8 sequences of 32768: 118 us against 124)
   const int64_t room = static_cast<int64_t>(cu) * (plan->width == 9 ? 1 : 2);
   // Heads of one slot lie next to each other in memory: a workgroup of the narrow
   // kernel takes up to 4, a wave each, so that a slot's lines are read together (16
   // sequences of 7 tokens, 1024 slots: 69 us against 80 with one).  Where a wave has
   // few tiles, the 4 times as many splits cost more at their join (one sequence of
-  // 32771: 35 us against 31).
+  // 32771: 29.6 us against 27).
   p.heads = plan->width == 9 || tiles * lists <= 8 * room * kWaves ? 1 : a->Hkv % 4 == 0 ? 4 : a->Hkv % 2 == 0 ? 2 : 1;
   const int64_t groups = lists / p.heads;
   // each wave with a tile at least
