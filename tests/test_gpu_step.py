@@ -446,6 +446,27 @@ def test_attention_strides_streams_and_workspace():
     assert torch.equal(out, plain[0]) and torch.equal(lse, plain[1])
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("D", [64, 128, 192, 256, 576])
+def test_scale_bytes_at_odd_addresses(D, dtype):
+    """Rows of scale bytes that start anywhere, the last ending with its allocation's view: the same bits as aligned ones."""
+    g = gen(14)
+    n, blocks = 301, D // 32
+    _, _, kg, ksg = cache(n, 1, D, g)
+    odd = torch.zeros(n * (blocks + 3) + 1, dtype=torch.uint8, device=dev())[1:].view(n, 1, blocks + 3)[..., 3:]
+    odd.copy_(ksg)
+    q = torch.randn(2, 2, 6, D, generator=g).to(dtype).to(dev())
+    slots = torch.randint(0, n, (2, 2, 77), generator=g, dtype=torch.int32).to(dev())
+    slots[..., 0] = n - 1
+    one, two = ets.attend_selected(q, kg, ksg, kg, ksg, slots), ets.attend_selected(q, kg, odd, kg, odd, slots)
+    assert torch.equal(one[0], two[0]) and torch.equal(one[1], two[1])
+    if D <= 256:
+        w = torch.rand(2, 2, 6, generator=g).to(dev())
+        table = torch.arange(n - 1, -1, -1, device=dev(), dtype=torch.int32).repeat(2, 1)
+        lens = torch.tensor([n, 200], device=dev(), dtype=torch.int32)
+        assert torch.equal(ets.index_scores(q, w, kg, ksg, table, lens, 1, n), ets.index_scores(q, w, kg, odd, table, lens, 1, n))
+
+
 def test_the_operators_in_a_graph():
     """A decode step captured once; each replay, with new inputs and eager work between, equals the eager step."""
     g = gen(14)
