@@ -15,6 +15,9 @@ constexpr int kChunk = 16;  // tiles whose slots are brought at a time
 // Bytes of half a decoded row of 64 nv channels.
 constexpr int value_plane(int nv) { return 64 * nv + (nv % 4 ? 0 : 64); }
 
+// Workgroups of a compute unit, by registers (256 channels: also by LDS; two spilled, and were slower).
+constexpr int attend_per_unit(int np, int mt) { return mt == 1 && np <= 2 ? 3 : (mt == 1 && np == 3) || (mt == 2 && np <= 2) ? 2 : 1; }
+
 // One wave goes over its tiles of 32 keys alone, with the softmax's reference
 // and running sum, and the four waves of a workgroup join at the end.  The
 // reference is the largest score so far, raised only when one passes it by
@@ -52,8 +55,9 @@ constexpr int value_plane(int nv) { return 64 * nv + (nv % 4 ? 0 : 64); }
 // bits), bf16 queries as one (8 bits: each is off by at most 2^-8 of itself,
 // the errors of different keys are independent, and the result is rounded to
 // 8 bits anyway).
+
 template <class T, int NP, int NV, int MT, bool FULL>
-__global__ __launch_bounds__(kThreads, MT == 1 && NP <= 2 ? 3 : 1) void attend_kernel(AttendParams p) {
+__global__ __launch_bounds__(kThreads, attend_per_unit(NP, MT)) void attend_kernel(AttendParams p) {
   typedef Mat<T> M;
   typedef typename M::V8 V8;
   // decoded values in LDS: rows of two planes, the lower and the upper halves of
@@ -469,7 +473,9 @@ ets_status make_plan(const ets_attend_args* a, Plan* plan) {
   p.G = a->Hq / a->Hkv;
   p.rows = paged ? a->T * p.G : p.G;
   p.units = a->B * a->Hkv * (paged ? 1 : a->T);
-  const int most = plan->width <= 2 ? 4 : 2;
+  // 16-row tiles of a workgroup: four leave a wave a SIMD (8 heads of 7 sequences of 10296, 40 rows each: 101 us against
+  // 73), and so do two of 192 channels (14 us against 9.5 for 40 rows of 160 channels)
+  const int most = plan->width == 3 ? 1 : 2;
   plan->mt = 1;
   while (plan->mt < most && 16 * plan->mt < p.rows) plan->mt *= 2;
   if (plan->width == 9) plan->mt = attend_wide_rows(p.rows, plan->shared, a->dtype == ETS_BF16);
@@ -480,7 +486,8 @@ ets_status make_plan(const ets_attend_args* a, Plan* plan) {
   const int64_t lists = static_cast<int64_t>(p.units) * p.row_groups;
   // workgroups to fill the device with: a compute unit holds one of the wide kernel's and up to three of the
   // narrow one's, but two read faster than three (8 sequences of 32768: 118 us against 124)
-  const int64_t room = static_cast<int64_t>(cu) * (plan->width == 9 ? 1 : 2);
+  const int fits = plan->width == 9 ? 1 : attend_per_unit(plan->width, plan->mt);
+  const int64_t room = static_cast<int64_t>(cu) * (fits < 2 ? fits : 2);
   // Heads of one slot lie next to each other in memory: a workgroup of the narrow
   // kernel takes up to 4, a wave each, so that a slot's lines are read together (16
   // sequences of 7 tokens, 1024 slots: 69 us against 80 with one).  Where a wave has
@@ -490,6 +497,8 @@ ets_status make_plan(const ets_attend_args* a, Plan* plan) {
   const int64_t groups = lists / p.heads;
   // each wave with a tile at least
   int64_t splits = (room + groups - 1) / groups;
+  // more than the device holds at once would wait for a second turn
+  if (groups * splits > static_cast<int64_t>(cu) * fits && splits > 1) splits = static_cast<int64_t>(cu) * fits / groups;
   const int64_t cap = plan->width == 9 ? (tiles + 3) / 4 : (tiles + kWaves / p.heads - 1) / (kWaves / p.heads);
   splits = splits > cap ? cap : splits;
   p.splits = static_cast<int>(splits < 1 ? 1 : splits);
@@ -530,10 +539,8 @@ template <class T, int N>
 void launch_width(const Plan& plan, hipStream_t s) {
   if (plan.mt == 1) {
     launch_attend<T, N, 1>(plan.p, s);
-  } else if (plan.mt == 2) {
+  } else if constexpr (N != 3) {
     launch_attend<T, N, 2>(plan.p, s);
-  } else if constexpr (N <= 2) {
-    launch_attend<T, N, 4>(plan.p, s);
   }
 }
 
