@@ -8,8 +8,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kRopeTable = 2048;  // (cos, sin) pairs of a workgroup's tokens, in LDS (16 KiB)
-constexpr int kRopeStage = 32768; // bytes of rows that the staged form holds in LDS
 constexpr int kBatch = 4;         // vectors a lane has in flight
+constexpr int kRopeStage = 16 * kBatch * kThreads;  // bytes of rows that the staged form holds in LDS: all of a workgroup's
 // vectors of a lane of the read: one more load under way hides the slot's; 4 and more took longer (131072 x 576: 46 us with
 // 2, 47 with 1, 50 with 4, 56 with 8, whose few workgroups end unevenly)
 constexpr int kReadBatch = 2;
@@ -56,17 +56,21 @@ __device__ __forceinline__ void put(char* to, const V& v, bool stream) {
 //
 // kInterleaved / kHalf: a lane turns one or two 16-byte vectors whose pairs it
 // holds whole.  kStaged: pairs that cross vectors (odd offsets, odd R / 2, D
-// not a multiple of a vector) are read from the rows staged in LDS.
+// not a multiple of a vector).  A lane holds its vectors as in the other forms,
+// all rows of the workgroup go to LDS as well (out may be x), and the partners
+// of a vector's channels come from there as one or two vectors at any address.
 //
 // Measured: 42 us for 16384 x 32 heads of 128 channels in bf16 (268 MB, 6.4
 // TB/s; a copy of 1 GiB reaches 5.2), 6.7 us for the transposed map of 4099 x 9
-// x 96 in fp32 (28 MB), 3 us for a single token (the launch).
+// x 96 in fp32 (28 MB), 3 us for a single token (the launch); staged: 43 us for
+// 8344 x 10 x 480 in bf16 from channel 259 on (160 MB; 74 us with partners read
+// one by one).
 template <class T, int MODE>
 __global__ __launch_bounds__(kThreads) void rope_kernel(RopeParams p) {
   constexpr int V = Vec<T>::n;
   typedef typename Vec<T>::type VT;
   __shared__ f32x2 table[kRopeTable];
-  __shared__ __align__(16) char stage[MODE == kStaged ? kRopeStage : 16];
+  __shared__ __align__(16) char stage[MODE == kStaged ? kRopeStage + 32 : 16];
 
   const uint32_t tile = div_by(blockIdx.x, p.by_groups);
   const int64_t n0 = static_cast<int64_t>(tile) * p.tokens;
@@ -113,12 +117,20 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeParams p) {
       it[u] = item_of(base + u * kThreads + static_cast<int>(threadIdx.x));
       if (it[u].live) {
         const char* src = p.x + it[u].in + static_cast<int64_t>(channel(it[u].v)) * sizeof(T);
+        const int left = p.D - it[u].v * V;
+        if (MODE == kStaged && left < V) {  // a short last vector
+          a[u] = VT{};
+#pragma unroll
+          for (int j = 0; j < V; ++j)
+            if (j < left) a[u][j] = reinterpret_cast<const T*>(src)[j];
+          continue;
+        }
         a[u] = load_any<VT>(src);
         if (MODE == kHalf && it[u].v < half_vecs) b[u] = load_any<VT>(src + static_cast<int64_t>(pairs) * sizeof(T));
       }
     }
   };
-  if (MODE != kStaged) fetch(0);
+  fetch(0);  // all of them in the staged form
 
   const float sign = p.inverse ? -1.0f : 1.0f;
   for (int i = threadIdx.x; i < tokens * pairs; i += kThreads) {
@@ -131,53 +143,46 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeParams p) {
     table[i] = f32x2{c * size, sign * s * size};
   }
 
+  // staged rows lie 16 * items bytes apart, with a vector of room before and behind them
+  T* const rows = reinterpret_cast<T*>(stage) + V;
   if (MODE == kStaged) {
-    const int row_bytes = p.D * static_cast<int>(sizeof(T));
-    for (int i = threadIdx.x; i < total; i += kThreads) {
-      const Item s = item_of(i);
-      if (!s.live) continue;
-      const uint32_t row = div_by(i, p.by_items);
-      const int at = s.v * V, left = p.D - at;
-      const char* src = p.x + s.in + static_cast<int64_t>(at) * sizeof(T);
-      char* dst = stage + static_cast<int>(row) * row_bytes + at * static_cast<int>(sizeof(T));
-      if (left >= V) {
-        store_any(dst, load_any<VT>(src));
-      } else {
-        for (int j = 0; j < left; ++j)
-          reinterpret_cast<T*>(dst)[j] = reinterpret_cast<const T*>(src)[j];
-      }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int i = u * kThreads + static_cast<int>(threadIdx.x);
+      if (it[u].live) *reinterpret_cast<VT*>(rows + i * V) = a[u];
     }
   }
   __syncthreads();
 
   if (MODE == kStaged) {
-    const T* rows = reinterpret_cast<const T*>(stage);
     const bool half = p.layout == ETS_ROPE_HALF;
-    for (int i = threadIdx.x; i < total; i += kThreads) {
-      const Item s = item_of(i);
-      if (!s.live) continue;
-      const T* row = rows + static_cast<int>(div_by(i, p.by_items)) * p.D;
-      const f32x2* cs = table + s.token * pairs;
-      const int at = s.v * V, count = min(V, p.D - at);
-      VT y;
+    const int apart = half ? pairs : 1;  // channels between the members of a pair
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const int d = min(at + j, p.D - 1), r = d - p.offset;
-        float v = static_cast<float>(row[d]);
-        if (static_cast<uint32_t>(r) < static_cast<uint32_t>(p.R)) {
-          const bool second = half ? r >= pairs : r & 1;
-          const int f = half ? (second ? r - pairs : r) : r >> 1;
-          const int other = half ? (second ? d - pairs : d + pairs) : (second ? d - 1 : d + 1);
-          const float w = static_cast<float>(row[other]);
-          const f32x2 c = cs[f];
-          v = second ? v * c[0] + w * c[1] : v * c[0] - w * c[1];
+    for (int u = 0; u < kBatch; ++u) {
+      if (!it[u].live) continue;
+      const int at = it[u].v * V, r0 = at - p.offset, count = min(V, p.D - at);
+      const f32x2* cs = table + it[u].token * pairs;
+      const T* own = rows + (u * kThreads + static_cast<int>(threadIdx.x)) * V;
+      VT y = a[u];
+      if (r0 + V > 0 && r0 < p.R) {
+        // the partners of first and of second members; a vector that has none reads its own place
+        const VT next = load_any<VT>(half && r0 >= pairs ? own : own + apart);
+        const VT before = load_any<VT>(half && r0 + V <= pairs ? own : own - apart);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const int r = r0 + j;
+          const bool turns = static_cast<uint32_t>(r) < static_cast<uint32_t>(p.R), second = half ? r >= pairs : r & 1;
+          const f32x2 c = cs[turns ? half ? (second ? r - pairs : r) : r >> 1 : 0];
+          const float v = static_cast<float>(a[u][j]), w = static_cast<float>(second ? before[j] : next[j]);
+          const T to = static_cast<T>(second ? v * c[0] + w * c[1] : v * c[0] - w * c[1]);
+          y[j] = turns ? to : y[j];
         }
-        y[j] = static_cast<T>(v);
       }
-      char* dst = p.out + s.out + static_cast<int64_t>(at) * sizeof(T);
+      char* dst = p.out + it[u].out + static_cast<int64_t>(at) * sizeof(T);
       if (count == V) {
-        store_any(dst, y);
+        put(dst, y, p.stream);
       } else {
+#pragma unroll
         for (int j = 0; j < V; ++j)
           if (j < count) reinterpret_cast<T*>(dst)[j] = y[j];
       }
@@ -395,7 +400,6 @@ ets_status ets_rope(const void* x, int64_t x_n, int64_t x_h, void* out, int64_t 
   int64_t want = all / (static_cast<int64_t>(cu) * 8);
   want = want < kThreads ? kThreads : want > kBatch * kThreads ? kBatch * kThreads : want;
   int64_t rows = want / items;
-  if (mode == kStaged && rows * D * size > kRopeStage) rows = kRopeStage / (static_cast<int64_t>(D) * size);
   if (rows < 1) rows = 1;
   p.heads = static_cast<int>(rows < H ? rows : H);
   int64_t tokens = rows / p.heads;
