@@ -51,11 +51,9 @@ constexpr int attend_per_unit(int np, int mt) { return mt == 1 && np <= 2 ? 3 : 
 // waves a compute unit; two tiles under way in registers spilled and were
 // slower.
 //
-// fp16 queries keep their probabilities as the sum of two bf16 numbers (16
-// bits), bf16 queries as one (8 bits: each is off by at most 2^-8 of itself,
-// the errors of different keys are independent, and the result is rounded to
-// 8 bits anyway).
-
+// Probabilities are the sum of two bf16 numbers (16 bits): with one, results of
+// few keys were off by up to three times their own rounding to bf16, and the
+// second costs nothing where the memory is what is waited for.
 template <class T, int NP, int NV, int MT, bool FULL>
 __global__ __launch_bounds__(kThreads, attend_per_unit(NP, MT)) void attend_kernel(AttendParams p) {
   typedef Mat<T> M;
@@ -63,7 +61,6 @@ __global__ __launch_bounds__(kThreads, attend_per_unit(NP, MT)) void attend_kern
   // decoded values in LDS: rows of two planes, the lower and the upper halves of
   // their 16-channel pieces; rows lie 4 banks apart, planes not a multiple of 64
   constexpr int kPlane = value_plane(NV), kPitch = 2 * kPlane + 16;
-  constexpr bool kTwo = M::kRowScale;  // fp16: two-part probabilities
   extern __shared__ __align__(16) char lds[];
   const ets_attend_args& a = p.a;
 
@@ -269,7 +266,7 @@ __global__ __launch_bounds__(kThreads, attend_per_unit(NP, MT)) void attend_kern
         x[j] = __builtin_amdgcn_exp2f(x[j]);
         sum[m] += x[j];
         prob[m][j] = static_cast<__bf16>(x[j]);
-        if constexpr (kTwo) rest[m][j] = static_cast<__bf16>(x[j] - static_cast<float>(prob[m][j]));
+        rest[m][j] = static_cast<__bf16>(x[j] - static_cast<float>(prob[m][j]));
       }
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -284,7 +281,7 @@ __global__ __launch_bounds__(kThreads, attend_per_unit(NP, MT)) void attend_kern
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         out[m][c] = Mat<__bf16>::mma(v, prob[m], out[m][c]);
-        if constexpr (kTwo) out[m][c] = Mat<__bf16>::mma(v, rest[m], out[m][c]);
+        out[m][c] = Mat<__bf16>::mma(v, rest[m], out[m][c]);
       }
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");

@@ -22,19 +22,19 @@ constexpr int kDepth = 2;            // tiles on their way from memory
 template <int N>
 struct Pieces {
   static constexpr int n = N;
-  u32v4 w[N];
-  uint32_t byte[N];
+  u32v4 w[N ? N : 1];
+  uint32_t byte[N ? N : 1];
 };
 
-template <int RT, bool SHARED, bool TWO>
+template <int RT, bool SHARED, bool REST>
 struct WideLds {
   uint8_t k[SHARED ? 3 : 2][kTile * kPitch];
   uint8_t v[SHARED ? 1 : 2][SHARED ? 16 : kTile * kPitch];
-  u32v2 prob[2][TWO ? 2 : 1][2][RT][64];  // [parity][part][team]
+  u32v2 prob[2][REST ? 2 : 1][2][RT][64];  // [parity][part][team]
   float ref[2][2][RT * 16];               // [parity][team]
   int32_t slot[4][kTile];  // -1: not there
   uint32_t seen[8];                          // which keys of a tile are there
-  f32x2 stat[2][RT * 16];
+  f32x4 stat[2][RT * 16];
 };
 
 // A workgroup takes 16 RT query rows through its share of the keys, 32 a step.
@@ -58,10 +58,13 @@ struct WideLds {
 // powers of two, which is exact.  (With 2^8 every second step of 64 rows had
 // such a change; both together took 74 us to 62.)
 //
-// fp16 queries and probabilities (TWO) are sums of two bf16 numbers each: the
-// query exactly, the probability to 16 bits.  bf16 queries take probabilities
-// of 8 bits (off by at most 2^-8 of themselves, independently over the keys)
-// with sums of the unrounded ones; the result is rounded to 8 bits anyway.
+// fp16 queries are sums of two bf16 numbers each, exactly (kTwo).
+// Probabilities are too, to 16 bits (kRest), but for 64 rows of bf16 queries,
+// whose sums leave no room for a second part (94 us with it against 62): there
+// they are rounded to 8 bits (off by at most 2^-8 of themselves, independently
+// over the keys), and the result is divided by the sum of the rounded ones, so
+// that what all of a row's keys have in common, a single key above all, is free
+// of it.  The log-sum-exp takes the unrounded sum.
 //
 // Measured: 61 us for 64 sequences, 128 heads on one latent head of 576
 // channels, 2048 slots each (36.5 GFLOP: 600 TFLOP/s), and 11 us for the join
@@ -74,9 +77,10 @@ struct WideLds {
 // a wave's own conversions changed nothing (2500 to 2600 for both).
 template <class T, int RT, int NC, bool SHARED>
 __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendParams p) {
-  constexpr bool kTwo = Mat<T>::kRowScale;
+  constexpr bool kTwo = Mat<T>::kRowScale;    // fp16: queries of two parts
+  constexpr bool kRest = kTwo || RT == 2;     // probabilities of two parts
   constexpr int MQ = RT / 2;  // 16-row tiles of a score wave
-  typedef WideLds<RT, SHARED, kTwo> Lds;
+  typedef WideLds<RT, SHARED, kRest> Lds;
   typedef T T8 __attribute__((ext_vector_type(8)));
   typedef __bf16 B4 __attribute__((ext_vector_type(4)));
   extern __shared__ __align__(16) char lds_raw[];
@@ -89,10 +93,14 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendParams p
   const int tiles = max(spot.last - spot.first, 0);
   const int steps = (tiles + 1) & ~1;  // pairs: the staging registers of either parity keep their places
 
-  // The 1152 pieces of a tile: waves 4 to 7 bring four a lane, waves 0 and 1 the
-  // last 128 (waves 0 to 3 need their registers for operands on their way).
+  // The 1152 pieces of a tile.  RT 4: waves 4 to 7 bring four a lane, waves 0
+  // and 1 the last 128.  RT 2: waves 4 to 7 three, waves 0 and 1 two, waves 2 and
+  // 3, which also find the rows, one: no spills in any form, where the other
+  // split spilled 20 registers with values of their own (at RT 4 it costs 3 us of 67).
+  constexpr bool kEven = RT == 2;
   const bool sums = wave >= 4;
-  const int piece0 = sums ? tid - 256 : 1024 + tid;
+  const int piece0 = sums ? tid - 256 : !kEven ? 1024 + tid : wave < 2 ? 768 + tid : 1024 + tid - 128;
+  const int apart = sums || !kEven ? 256 : 128;
   // addresses as numbers: a row that is not there is read from kNothing, without a branch
   const uint64_t nothing = reinterpret_cast<uint64_t>(&kNothing[0]);
   auto bring = [&](auto& set, int i, uint64_t codes, uint32_t row, uint64_t scales, uint32_t scale_row, int pieces) {
@@ -100,10 +108,10 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendParams p
     constexpr int N = std::remove_reference_t<decltype(set)>::n;
     int32_t slot[N];
 #pragma unroll
-    for (int j = 0; j < N; ++j) slot[j] = slots[(piece0 + 256 * j) / kPieces];
+    for (int j = 0; j < N; ++j) slot[j] = slots[(piece0 + apart * j) / kPieces];
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      const int at = (piece0 + 256 * j) % kPieces;
+      const int at = (piece0 + apart * j) % kPieces;
       const bool there = slot[j] >= 0 && at < pieces;
       const uint64_t w = codes + static_cast<uint64_t>(static_cast<uint32_t>(slot[j])) * row + 16 * at;
       const uint64_t b = scales + static_cast<uint64_t>(static_cast<uint32_t>(slot[j])) * scale_row + (at >> 1);
@@ -114,7 +122,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendParams p
   auto lay = [&](const auto& set, uint8_t* tile) {
 #pragma unroll
     for (int j = 0; j < set.n; ++j) {
-      const int c = piece0 + 256 * j;
+      const int c = piece0 + apart * j;
       const float f = __uint_as_float(set.byte[j] << 23);
       uint8_t* dst = tile + c / kPieces * kPitch + 16 * (c % kPieces);
       *reinterpret_cast<bf16x8*>(dst) = codes_bf16(set.w[j][0], set.w[j][1], f);
@@ -209,9 +217,9 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendParams p
       lds.ref[1][team][(MQ * hg + m) * 16 + col] = kNegInf;
     }
     __syncthreads();
-    float ref[MQ], sum[MQ];
+    float ref[MQ], sum[MQ], rounded[MQ];  // rounded: the sum of the probabilities as they are multiplied
 #pragma unroll
-    for (int m = 0; m < MQ; ++m) ref[m] = kNegInf, sum[m] = 0.0f;
+    for (int m = 0; m < MQ; ++m) ref[m] = kNegInf, sum[m] = 0.0f, rounded[m] = 0.0f;
 
     auto scores = [&](int i, const uint8_t* tile) {
       float other[MQ];  // the other team's reference of the step before
@@ -264,7 +272,8 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendParams p
           high = rows_max(high);
           float next = fmaxf(ref[m], other[m]);
           if (high > next + kSlack || next == kNegInf) next = ceilf(high);
-          sum[m] *= ref[m] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(ref[m] - next);
+          const float fade = ref[m] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(ref[m] - next);
+          sum[m] *= fade, rounded[m] *= fade;
           ref[m] = next;
           y[m] = x[m] - (next == kNegInf ? 0.0f : next);
         }
@@ -279,15 +288,19 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendParams p
           const float z = __builtin_amdgcn_exp2f(y[m][e]);
           sum[m] += z;
           prob[e] = static_cast<__bf16>(z);
-          if constexpr (kTwo) rest[e] = static_cast<__bf16>(z - static_cast<float>(prob[e]));
+          if constexpr (kRest) {
+            rest[e] = static_cast<__bf16>(z - static_cast<float>(prob[e]));
+          } else {
+            rounded[m] += static_cast<float>(prob[e]);
+          }
         }
         lds.prob[half][0][team][rt][lane] = __builtin_bit_cast(u32v2, prob);
-        if constexpr (kTwo) lds.prob[half][1][team][rt][lane] = __builtin_bit_cast(u32v2, rest);
+        if constexpr (kRest) lds.prob[half][1][team][rt][lane] = __builtin_bit_cast(u32v2, rest);
       }
     };
 
     if (wave < 2) {
-      Pieces<1> kset[kDepth], vset[SHARED ? 1 : kDepth];
+      Pieces<kEven ? 2 : 1> kset[kDepth], vset[SHARED ? 1 : kDepth];
       begin(kset, vset);
       __syncthreads();
       scores(0, lds.k[0]);
@@ -297,22 +310,26 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendParams p
         stage(kset, vset, odd, i, after);
       });
     } else {  // these two find the rows (both the same ones)
+      Pieces<kEven ? 1 : 0> kset[kDepth], vset[SHARED ? 1 : kDepth];
       int32_t asked = ask(4);
+      if constexpr (kEven) begin(kset, vset);
       __syncthreads();
       keep(4, asked);
       asked = ask(5);
       scores(0, lds.k[0]);
       __syncthreads();
-      run([&](auto, int i, int, int next, int) {
+      run([&](auto odd, int i, int, int next, int after) {
         keep(i + 5, asked);
         asked = ask(i + 6);
         scores(i + 1, lds.k[next]);
+        if constexpr (kEven) stage(kset, vset, odd, i, after);
       });
     }
 #pragma unroll
     for (int m = 0; m < MQ; ++m) {
       sum[m] = rows_sum(sum[m]);
-      if (g == 0) lds.stat[team][(MQ * hg + m) * 16 + col] = f32x2{ref[m], sum[m]};
+      if constexpr (!kRest) rounded[m] = rows_sum(rounded[m]);
+      if (g == 0) lds.stat[team][(MQ * hg + m) * 16 + col] = f32x4{ref[m], sum[m], rounded[m], 0.0f};
     }
     __syncthreads();
     return;
@@ -330,7 +347,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendParams p
   }
   auto products = [&](int i, const uint8_t* tile) {
     const int half = i & 1;
-    constexpr int kParts = kTwo ? 2 : 1;
+    constexpr int kParts = kRest ? 2 : 1;
     bf16x8 prob[kParts][RT];
     auto join = [](u32v2 lo, u32v2 hi) { return __builtin_bit_cast(bf16x8, u32v4{lo[0], lo[1], hi[0], hi[1]}); };
     bool moved = false;
@@ -378,7 +395,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendParams p
 
   if (tid - 256 < 4 * kTile) keep((tid - 256) >> 5, ask((tid - 256) >> 5));
   __syncthreads();
-  Pieces<4> kset[kDepth], vset[SHARED ? 1 : kDepth];
+  Pieces<kEven ? 3 : 4> kset[kDepth], vset[SHARED ? 1 : kDepth];
   begin(kset, vset);
   __syncthreads();
   __syncthreads();
@@ -393,9 +410,15 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendParams p
   for (int m = 0; m < RT; ++m) {
     const int r = spot.row0 + 16 * m + col;
     if (r >= p.rows) continue;
-    const f32x2 s0 = lds.stat[0][16 * m + col], s1 = lds.stat[1][16 * m + col];
+    const f32x4 s0 = lds.stat[0][16 * m + col], s1 = lds.stat[1][16 * m + col];
     const float zero = base[m] == kNegInf ? 0.0f : base[m];
-    const f32x2 s = {base[m], s0[1] * __builtin_amdgcn_exp2f(s0[0] - zero) + s1[1] * __builtin_amdgcn_exp2f(s1[0] - zero)};
+    const float f0 = __builtin_amdgcn_exp2f(s0[0] - zero), f1 = __builtin_amdgcn_exp2f(s1[0] - zero);
+    const f32x2 s = {base[m], s0[1] * f0 + s1[1] * f1};
+    if constexpr (!kRest) {
+      const float of = s0[2] * f0 + s1[2] * f1, exact = of > 0.0f ? s[1] / of : 1.0f;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) out[m][c] *= exact;
+    }
     const bool first = quarter == 0 && g == 0;
     if (p.splits > 1) {
       const int64_t at = block * (16 * RT) + 16 * m + col;
@@ -427,7 +450,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendParams p
 template <class T, int RT, int NC, bool SHARED>
 void launch(const AttendParams& p, hipStream_t s) {
   hipLaunchKernelGGL((attend_wide_kernel<T, RT, NC, SHARED>), dim3(attend_grid(p)), dim3(kThreads),
-                     sizeof(WideLds<RT, SHARED, Mat<T>::kRowScale>), s, p);
+                     sizeof(WideLds<RT, SHARED, Mat<T>::kRowScale || RT == 2>), s, p);
 }
 
 }  // namespace
