@@ -66,9 +66,9 @@ struct WideLds {
 // that what all of a row's keys have in common, a single key above all, is free
 // of it.  The log-sum-exp takes the unrounded sum.
 //
-// Measured: 61 us for 64 sequences, 128 heads on one latent head of 576
+// Measured: 62 us for 64 sequences, 128 heads on one latent head of 576
 // channels, 2048 slots each (36.5 GFLOP: 600 TFLOP/s), and 11 us for the join
-// of its two shares.  Of the 61, 8 go by until the first product (queries and
+// of its two shares.  Of the 62, 8 go by until the first product (queries and
 // first rows come at once, 28 MB) and 4 after the last (33 MB of sums).  A
 // step of 32 keys takes 2800 cycles: the sums' waves lay out rows for 1300 and
 // multiply for 1300.  Matrix instructions of one wave leave another wave of
