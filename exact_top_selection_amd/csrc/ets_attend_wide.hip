@@ -22,19 +22,21 @@ constexpr int kDepth = 2;            // tiles on their way from memory
 template <int N>
 struct Pieces {
   static constexpr int n = N;
-  u32v4 w[N ? N : 1];
-  uint32_t byte[N ? N : 1];
+  u32v4 w[N];
+  uint32_t byte[N];
 };
 
-template <int RT, bool SHARED, bool REST>
+// What lanes address by themselves comes first: an LDS instruction's own offset
+// reaches 64 KiB, and each address behind that took a register through the loop.
+template <int RT, bool SHARED>
 struct WideLds {
-  uint8_t k[SHARED ? 3 : 2][kTile * kPitch];
+  u32v2 prob[2][2][2][RT][64];  // [parity][part][team]
+  f32x2 stat[2][RT * 16];
+  float ref[2][2][RT * 16];     // [parity][team]
+  int32_t slot[4][kTile];       // -1: not there
+  uint32_t seen[8];             // which keys of a tile are there
+  alignas(16) uint8_t k[SHARED ? 3 : 2][kTile * kPitch];
   uint8_t v[SHARED ? 1 : 2][SHARED ? 16 : kTile * kPitch];
-  u32v2 prob[2][REST ? 2 : 1][2][RT][64];  // [parity][part][team]
-  float ref[2][2][RT * 16];               // [parity][team]
-  int32_t slot[4][kTile];  // -1: not there
-  uint32_t seen[8];                          // which keys of a tile are there
-  f32x4 stat[2][RT * 16];
 };
 
 // A workgroup takes 16 RT query rows through its share of the keys, 32 a step.
@@ -58,29 +60,23 @@ struct WideLds {
 // powers of two, which is exact.  (With 2^8 every second step of 64 rows had
 // such a change; both together took 74 us to 62.)
 //
-// fp16 queries are sums of two bf16 numbers each, exactly (kTwo).
-// Probabilities are too, to 16 bits (kRest), but for 64 rows of bf16 queries,
-// whose sums leave no room for a second part (94 us with it against 62): there
-// they are rounded to 8 bits (off by at most 2^-8 of themselves, independently
-// over the keys), and the result is divided by the sum of the rounded ones, so
-// that what all of a row's keys have in common, a single key above all, is free
-// of it.  The log-sum-exp takes the unrounded sum.
+// Probabilities are the sum of two bf16 numbers (16 bits), and fp16 queries are
+// so too, exactly (kTwo).  One part of 8 bits took 62 us on the case below in
+// the place of 71, but its results were off by up to 3.4 times their own
+// rounding to bf16 with few keys, and 1.1 times when divided by the sum of the
+// rounded probabilities.
 //
-// Measured: 62 us for 64 sequences, 128 heads on one latent head of 576
-// channels, 2048 slots each (36.5 GFLOP: 600 TFLOP/s), and 11 us for the join
-// of its two shares.  Of the 62, 8 go by until the first product (queries and
-// first rows come at once, 28 MB) and 4 after the last (33 MB of sums).  A
-// step of 32 keys takes 2800 cycles: the sums' waves lay out rows for 1300 and
-// multiply for 1300.  Matrix instructions of one wave leave another wave of
-// their SIMD every second vector slot, so 68 of them, 40 conversions and 300
-// other vector instructions need 2000 of those cycles; products put in between
-// a wave's own conversions changed nothing (2500 to 2600 for both).
+// Measured: 71 us for 64 sequences, 128 heads on one latent head of 576
+// channels, 2048 slots each (36.5 GFLOP: 515 TFLOP/s), and 11 us for the join
+// of its two shares.  Of the 71, 8 go by until the first product (queries and
+// first rows come at once, 28 MB) and 4 after the last (33 MB of sums).  A step
+// of 32 keys is 100 matrix instructions a SIMD (1600 cycles), and those of one
+// wave leave another wave of their SIMD every second vector slot.
 template <class T, int RT, int NC, bool SHARED>
 __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendParams p) {
-  constexpr bool kTwo = Mat<T>::kRowScale;    // fp16: queries of two parts
-  constexpr bool kRest = kTwo || RT == 2;     // probabilities of two parts
+  constexpr bool kTwo = Mat<T>::kRowScale;  // fp16: queries of two parts
   constexpr int MQ = RT / 2;  // 16-row tiles of a score wave
-  typedef WideLds<RT, SHARED, kRest> Lds;
+  typedef WideLds<RT, SHARED> Lds;
   typedef T T8 __attribute__((ext_vector_type(8)));
   typedef __bf16 B4 __attribute__((ext_vector_type(4)));
   extern __shared__ __align__(16) char lds_raw[];
@@ -93,14 +89,13 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendParams p
   const int tiles = max(spot.last - spot.first, 0);
   const int steps = (tiles + 1) & ~1;  // pairs: the staging registers of either parity keep their places
 
-  // The 1152 pieces of a tile.  RT 4: waves 4 to 7 bring four a lane, waves 0
-  // and 1 the last 128.  RT 2: waves 4 to 7 three, waves 0 and 1 two, waves 2 and
-  // 3, which also find the rows, one: no spills in any form, where the other
-  // split spilled 20 registers with values of their own (at RT 4 it costs 3 us of 67).
-  constexpr bool kEven = RT == 2;
+  // The 1152 pieces of a tile: waves 4 to 7 bring three a lane, waves 0 and 1
+  // two, waves 2 and 3, which also find the rows, one.  (64 rows: 71 us; with
+  // four a lane of waves 4 to 7 and one of waves 0 and 1 72, with two, three and
+  // two 75.)
   const bool sums = wave >= 4;
-  const int piece0 = sums ? tid - 256 : !kEven ? 1024 + tid : wave < 2 ? 768 + tid : 1024 + tid - 128;
-  const int apart = sums || !kEven ? 256 : 128;
+  const int piece0 = sums ? tid - 256 : wave < 2 ? 768 + tid : 1024 + tid - 128;
+  const int apart = sums ? 256 : 128;
   // addresses as numbers: a row that is not there is read from kNothing, without a branch
   const uint64_t nothing = reinterpret_cast<uint64_t>(&kNothing[0]);
   auto bring = [&](auto& set, int i, uint64_t codes, uint32_t row, uint64_t scales, uint32_t scale_row, int pieces) {
@@ -217,9 +212,9 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendParams p
       lds.ref[1][team][(MQ * hg + m) * 16 + col] = kNegInf;
     }
     __syncthreads();
-    float ref[MQ], sum[MQ], rounded[MQ];  // rounded: the sum of the probabilities as they are multiplied
+    float ref[MQ], sum[MQ];
 #pragma unroll
-    for (int m = 0; m < MQ; ++m) ref[m] = kNegInf, sum[m] = 0.0f, rounded[m] = 0.0f;
+    for (int m = 0; m < MQ; ++m) ref[m] = kNegInf, sum[m] = 0.0f;
 
     auto scores = [&](int i, const uint8_t* tile) {
       float other[MQ];  // the other team's reference of the step before
@@ -273,7 +268,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendParams p
           float next = fmaxf(ref[m], other[m]);
           if (high > next + kSlack || next == kNegInf) next = ceilf(high);
           const float fade = ref[m] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(ref[m] - next);
-          sum[m] *= fade, rounded[m] *= fade;
+          sum[m] *= fade;
           ref[m] = next;
           y[m] = x[m] - (next == kNegInf ? 0.0f : next);
         }
@@ -288,19 +283,15 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendParams p
           const float z = __builtin_amdgcn_exp2f(y[m][e]);
           sum[m] += z;
           prob[e] = static_cast<__bf16>(z);
-          if constexpr (kRest) {
-            rest[e] = static_cast<__bf16>(z - static_cast<float>(prob[e]));
-          } else {
-            rounded[m] += static_cast<float>(prob[e]);
-          }
+          rest[e] = static_cast<__bf16>(z - static_cast<float>(prob[e]));
         }
         lds.prob[half][0][team][rt][lane] = __builtin_bit_cast(u32v2, prob);
-        if constexpr (kRest) lds.prob[half][1][team][rt][lane] = __builtin_bit_cast(u32v2, rest);
+        lds.prob[half][1][team][rt][lane] = __builtin_bit_cast(u32v2, rest);
       }
     };
 
     if (wave < 2) {
-      Pieces<kEven ? 2 : 1> kset[kDepth], vset[SHARED ? 1 : kDepth];
+      Pieces<2> kset[kDepth], vset[SHARED ? 1 : kDepth];
       begin(kset, vset);
       __syncthreads();
       scores(0, lds.k[0]);
@@ -310,9 +301,9 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendParams p
         stage(kset, vset, odd, i, after);
       });
     } else {  // these two find the rows (both the same ones)
-      Pieces<kEven ? 1 : 0> kset[kDepth], vset[SHARED ? 1 : kDepth];
+      Pieces<1> kset[kDepth], vset[SHARED ? 1 : kDepth];
       int32_t asked = ask(4);
-      if constexpr (kEven) begin(kset, vset);
+      begin(kset, vset);
       __syncthreads();
       keep(4, asked);
       asked = ask(5);
@@ -322,14 +313,13 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendParams p
         keep(i + 5, asked);
         asked = ask(i + 6);
         scores(i + 1, lds.k[next]);
-        if constexpr (kEven) stage(kset, vset, odd, i, after);
+        stage(kset, vset, odd, i, after);
       });
     }
 #pragma unroll
     for (int m = 0; m < MQ; ++m) {
       sum[m] = rows_sum(sum[m]);
-      if constexpr (!kRest) rounded[m] = rows_sum(rounded[m]);
-      if (g == 0) lds.stat[team][(MQ * hg + m) * 16 + col] = f32x4{ref[m], sum[m], rounded[m], 0.0f};
+      if (g == 0) lds.stat[team][(MQ * hg + m) * 16 + col] = f32x2{ref[m], sum[m]};
     }
     __syncthreads();
     return;
@@ -345,57 +335,63 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendParams p
 #pragma unroll
     for (int c = 0; c < NC; ++c) out[m][c] = f32x4{};
   }
+  // Two row tiles at a time: the probabilities of four spill (74 us), and the loads of one pair are not kept for the
+  // next by the compiler, for which rows is a new value.
   auto products = [&](int i, const uint8_t* tile) {
+    typedef __attribute__((address_space(3))) s16x4* Lds4;
+    typedef short s16x8 __attribute__((ext_vector_type(8)));
     const int half = i & 1;
-    constexpr int kParts = kRest ? 2 : 1;
-    bf16x8 prob[kParts][RT];
-    auto join = [](u32v2 lo, u32v2 hi) { return __builtin_bit_cast(bf16x8, u32v4{lo[0], lo[1], hi[0], hi[1]}); };
-    bool moved = false;
-    float r0[RT], r1[RT];
-#pragma unroll
-    for (int m = 0; m < RT; ++m) {
-      r0[m] = lds.ref[half][0][16 * m + col];
-      r1[m] = lds.ref[half][1][16 * m + col];
-      moved = moved || r0[m] != base[m] || r1[m] != base[m];
-#pragma unroll
-      for (int k = 0; k < kParts; ++k)
-        prob[k][m] = join(lds.prob[half][k][0][m][lane], lds.prob[half][k][1][m][lane]);
-    }
-    if (__any(moved)) {
-#pragma unroll
-      for (int m = 0; m < RT; ++m) {
-        const float next = fmaxf(base[m], fmaxf(r0[m], r1[m])), zero = next == kNegInf ? 0.0f : next;
-        const float fade = __builtin_amdgcn_exp2f(base[m] - zero);
-        const float f0 = __builtin_amdgcn_exp2f(r0[m] - zero), f1 = __builtin_amdgcn_exp2f(r1[m] - zero);
-        base[m] = next;
-#pragma unroll
-        for (int c = 0; c < NC; ++c) out[m][c] *= fade;
-#pragma unroll
-        for (int k = 0; k < kParts; ++k)
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            prob[k][m][e] = static_cast<__bf16>(static_cast<float>(prob[k][m][e]) * (e < 4 ? f0 : f1));
-      }
-    }
     // 16 channels by 4 keys a load: lane (key col / 4, four channels col % 4) of the upper or lower halves
-    const uint8_t* rows = tile + (4 * g + (col >> 2)) * kPitch + kPlane * ((col >> 1) & 1) + 8 * (col & 1) + 16 * (quarter * NC);
+    uint32_t rows = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
+        (Lds4)(tile + (4 * g + (col >> 2)) * kPitch + kPlane * ((col >> 1) & 1) + 8 * (col & 1) + 16 * (quarter * NC))));
+    auto join = [](u32v2 lo, u32v2 hi) { return __builtin_bit_cast(bf16x8, u32v4{lo[0], lo[1], hi[0], hi[1]}); };
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      typedef __attribute__((address_space(3))) s16x4* Lds4;
-      typedef short s16x8 __attribute__((ext_vector_type(8)));
-      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds4)(rows + 16 * c));
-      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds4)(rows + 16 * kPitch + 16 * c));
-      const bf16x8 v = __builtin_bit_cast(bf16x8, s16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
+    for (int m0 = 0; m0 < RT; m0 += 2) {
+      bf16x8 prob[2][2];
+      bool moved = false;
+      float r0[2], r1[2];
 #pragma unroll
-      for (int m = 0; m < RT; ++m)
+      for (int m = 0; m < 2; ++m) {
+        r0[m] = lds.ref[half][0][16 * (m0 + m) + col];
+        r1[m] = lds.ref[half][1][16 * (m0 + m) + col];
+        moved = moved || r0[m] != base[m0 + m] || r1[m] != base[m0 + m];
 #pragma unroll
-        for (int k = 0; k < kParts; ++k) out[m][c] = Mat<__bf16>::mma(v, prob[k][m], out[m][c]);
+        for (int k = 0; k < 2; ++k)
+          prob[k][m] = join(lds.prob[half][k][0][m0 + m][lane], lds.prob[half][k][1][m0 + m][lane]);
+      }
+      if (__any(moved)) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const float next = fmaxf(base[m0 + m], fmaxf(r0[m], r1[m])), zero = next == kNegInf ? 0.0f : next;
+          const float fade = __builtin_amdgcn_exp2f(base[m0 + m] - zero);
+          const float f0 = __builtin_amdgcn_exp2f(r0[m] - zero), f1 = __builtin_amdgcn_exp2f(r1[m] - zero);
+          base[m0 + m] = next;
+#pragma unroll
+          for (int c = 0; c < NC; ++c) out[m0 + m][c] *= fade;
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              prob[k][m][e] = static_cast<__bf16>(static_cast<float>(prob[k][m][e]) * (e < 4 ? f0 : f1));
+        }
+      }
+      asm volatile("" : "+v"(rows));
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds4)(uintptr_t)(rows + 16 * c));
+        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds4)(uintptr_t)(rows + 16 * kPitch + 16 * c));
+        const bf16x8 v = __builtin_bit_cast(bf16x8, s16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int m = 0; m < 2; ++m) out[m0 + m][c] = Mat<__bf16>::mma(v, prob[k][m], out[m0 + m][c]);
+      }
     }
   };
 
   if (tid - 256 < 4 * kTile) keep((tid - 256) >> 5, ask((tid - 256) >> 5));
   __syncthreads();
-  Pieces<kEven ? 3 : 4> kset[kDepth], vset[SHARED ? 1 : kDepth];
+  Pieces<3> kset[kDepth], vset[SHARED ? 1 : kDepth];
   begin(kset, vset);
   __syncthreads();
   __syncthreads();
@@ -410,15 +406,10 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendParams p
   for (int m = 0; m < RT; ++m) {
     const int r = spot.row0 + 16 * m + col;
     if (r >= p.rows) continue;
-    const f32x4 s0 = lds.stat[0][16 * m + col], s1 = lds.stat[1][16 * m + col];
+    const f32x2 s0 = lds.stat[0][16 * m + col], s1 = lds.stat[1][16 * m + col];
     const float zero = base[m] == kNegInf ? 0.0f : base[m];
     const float f0 = __builtin_amdgcn_exp2f(s0[0] - zero), f1 = __builtin_amdgcn_exp2f(s1[0] - zero);
     const f32x2 s = {base[m], s0[1] * f0 + s1[1] * f1};
-    if constexpr (!kRest) {
-      const float of = s0[2] * f0 + s1[2] * f1, exact = of > 0.0f ? s[1] / of : 1.0f;
-#pragma unroll
-      for (int c = 0; c < NC; ++c) out[m][c] *= exact;
-    }
     const bool first = quarter == 0 && g == 0;
     if (p.splits > 1) {
       const int64_t at = block * (16 * RT) + 16 * m + col;
@@ -450,7 +441,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendParams p
 template <class T, int RT, int NC, bool SHARED>
 void launch(const AttendParams& p, hipStream_t s) {
   hipLaunchKernelGGL((attend_wide_kernel<T, RT, NC, SHARED>), dim3(attend_grid(p)), dim3(kThreads),
-                     sizeof(WideLds<RT, SHARED, Mat<T>::kRowScale || RT == 2>), s, p);
+                     sizeof(WideLds<RT, SHARED>), s, p);
 }
 
 }  // namespace
