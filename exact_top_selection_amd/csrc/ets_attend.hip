@@ -407,7 +407,8 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttendParams p) {
     sums[threadIdx.x] = v;
     joined[threadIdx.x] = f32x2{high, total};
     __syncthreads();
-    if (mine != 0) return;
+    // lanes of no part stand past the last share: theirs would be read behind the arrays
+    if (mine != 0 || !live) return;
     for (int i = 1; i < p.join_groups; ++i) high = fmaxf(high, joined[threadIdx.x + i * lanes][0]);
     const float base = high == kNegInf ? 0.0f : high;
     v = f32x4{};

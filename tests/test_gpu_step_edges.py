@@ -38,3 +38,17 @@ def test_probabilities_of_two_parts(n, shape, dtype):
     out, lse = ets.attend_selected(q.to(dev()), kg, ksg, vg, vsg, slots.to(dev()))
     close(out, want[0], want[2], dtype)
     close(lse, want[1], want[3], FP32)
+
+
+@pytest.mark.parametrize("n", [1500, 1900])  # 12 and 15 splits: the join's shares leave lanes over
+@pytest.mark.parametrize("Dv", [32, 96, 128, 160, 192])
+def test_joins_with_lanes_left_over(Dv, n):
+    g = gen(22)
+    kc, ks, kg, ksg = cache(n, 1, 64, g)
+    vc, vs, vg, vsg = cache(n, 1, Dv, g)
+    q = torch.randn(1, 1, 8, 64, generator=g).to(FP16)
+    slots = torch.randperm(n, generator=g).to(torch.int32).view(1, 1, n)
+    want = ref.attend(q, kc, ks, vc, vs, [[slots[0, 0]]])
+    out, lse = ets.attend_selected(q.to(dev()), kg, ksg, vg, vsg, slots.to(dev()))
+    close(out, want[0], want[2], FP16)
+    close(lse, want[1], want[3], FP32)
