@@ -116,6 +116,39 @@ __device__ __forceinline__ int64_t attend_place(const AttendParams& p, const Att
   return ((static_cast<int64_t>(s.bt) * p.a.Hkv + hk) * p.row_groups + s.group) * p.splits + s.split;
 }
 
+// Drafted tokens that some rows of a workgroup see and others do not: their
+// probability is zero there, and zero times a value that is no number is not
+// zero.  Such values are taken out of a tile before the second product, and
+// two products of their places with what each row sees bring them back where
+// they belong: large times large is infinity, and that less infinity no number.
+typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
+constexpr uint16_t kLarge = 0x7f7f;  // the largest bf16
+__device__ __forceinline__ bool no_number(uint16_t bf16) { return (bf16 & 0x7f80) == 0x7f80; }
+__device__ __forceinline__ bf16x8 odd_places(bf16x8 v) {
+  const u16x8 bits = __builtin_bit_cast(u16x8, v);
+  u16x8 x;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = no_number(bits[e]) ? kLarge : 0;
+  return __builtin_bit_cast(bf16x8, x);
+}
+// Bits 0..3 and 16..19 of vis: a lane's keys in the second product.
+__device__ __forceinline__ bf16x8 seen_places(uint32_t vis) {
+  u16x8 x;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) x[j] = vis >> (16 * (j >> 2) + (j & 3)) & 1 ? kLarge : 0;
+  return __builtin_bit_cast(bf16x8, x);
+}
+__device__ __forceinline__ f32x4 spoilt(f32x4 x, bf16x8 odd, bf16x8 seen) {
+  x = Mat<__bf16>::mma(odd, seen, x);
+  return Mat<__bf16>::mma(odd, -seen, x);
+}
+__device__ __forceinline__ void clear_odd(void* eight) {  // in LDS
+  u16x8 bits = *static_cast<u16x8*>(eight);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) bits[e] = no_number(bits[e]) ? 0 : bits[e];
+  *static_cast<u16x8*>(eight) = bits;
+}
+
 __device__ __forceinline__ float attend_lse(float reference, float sum) {
   return sum == 0.0f ? kNegInf : (reference + __builtin_amdgcn_logf(sum)) * kLn2;
 }

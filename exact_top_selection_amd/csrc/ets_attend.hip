@@ -72,6 +72,7 @@ __global__ __launch_bounds__(kThreads, attend_per_unit(NP, MT)) void attend_kern
   const AttendSpot spot = attend_spot(p);
   if (!spot.live) return;
   const int b = spot.b, row0 = spot.row0, main_tiles = spot.main_tiles, last = spot.last;
+  const bool forked = spot.paged && p.tree_tiles > 0;  // rows of the workgroup see different drafted tokens
   // a wave's head, and the team of waves that share the head's keys
   const int hk = spot.hk + wave % p.heads, team = wave / p.heads, teams = kWaves / p.heads;
 
@@ -271,13 +272,34 @@ __global__ __launch_bounds__(kThreads, attend_per_unit(NP, MT)) void attend_kern
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     const char* src = values + (4 * g + (col >> 2)) * kPitch + kPlane * ((col >> 1) & 1) + 8 * (col & 1);
-#pragma unroll
-    for (int c = 0; c < 4 * NV; ++c) {
+    auto value = [&](int c) {
       typedef __attribute__((address_space(3))) s16x4* Lds4;
+      typedef short s16x8 __attribute__((ext_vector_type(8)));
       const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds4)(src + 16 * c));
       const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds4)(src + 16 * kPitch + 16 * c));
-      typedef short s16x8 __attribute__((ext_vector_type(8)));
-      const bf16x8 v = __builtin_bit_cast(bf16x8, s16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
+      return __builtin_bit_cast(bf16x8, s16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
+    };
+    if (forked && tile >= main_tiles) {
+      bf16x8 sees[MT];
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+        sees[m] = seen_places((seen_now & static_cast<uint32_t>(tree_bits[m] >> (kTile * (tile - main_tiles) & 63))) >> (4 * g));
+#pragma unroll
+      for (int c = 0; c < 4 * NV; ++c) {
+        const bf16x8 odd = odd_places(value(c));
+#pragma unroll
+        for (int m = 0; m < MT; ++m) out[m][c] = spoilt(out[m][c], odd, sees[m]);
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      for (int i = lane; i < kTile * 8 * NV; i += 64) {
+        const int row = i / (8 * NV), piece = i % (8 * NV);
+        clear_odd(values + row * kPitch + (piece & 1) * kPlane + 16 * (piece >> 1));
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+#pragma unroll
+    for (int c = 0; c < 4 * NV; ++c) {
+      const bf16x8 v = value(c);
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         out[m][c] = Mat<__bf16>::mma(v, prob[m], out[m][c]);

@@ -35,6 +35,7 @@ struct WideLds {
   float ref[2][2][RT * 16];     // [parity][team]
   int32_t slot[4][kTile];       // -1: not there
   uint32_t seen[8];             // which keys of a tile are there
+  uint32_t sees[2][2][RT * 16]; // [parity][team] which drafted tokens a row sees
   alignas(16) uint8_t k[SHARED ? 3 : 2][kTile * kPitch];
   uint8_t v[SHARED ? 1 : 2][SHARED ? 16 : kTile * kPitch];
 };
@@ -87,6 +88,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendParams p
   const int tid = threadIdx.x, lane = tid & 63, col = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int tiles = max(spot.last - spot.first, 0);
+  const bool forked = spot.paged && p.tree_tiles > 0;  // rows of the workgroup see different drafted tokens
   const int steps = (tiles + 1) & ~1;  // pairs: the staging registers of either parity keep their places
 
   // The 1152 pieces of a tile: waves 4 to 7 bring three a lane, waves 0 and 1
@@ -257,6 +259,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendParams p
         for (int m = 0; m < MQ; ++m) {
           uint32_t vis = seen;
           if (at >= spot.main_tiles) vis &= static_cast<uint32_t>(tree_bits[m] >> (kTile * (at - spot.main_tiles) + 16 * team));
+          if (!SHARED && forked && g == 0) lds.sees[half][team][(MQ * hg + m) * 16 + col] = vis;
           vis >>= 4 * g;
           float high = kNegInf;
 #pragma unroll
@@ -337,7 +340,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendParams p
   }
   // Two row tiles at a time: the probabilities of four spill (74 us), and the loads of one pair are not kept for the
   // next by the compiler, for which rows is a new value.
-  auto products = [&](int i, const uint8_t* tile) {
+  auto products = [&](int i, uint8_t* tile) {
     typedef __attribute__((address_space(3))) s16x4* Lds4;
     typedef short s16x8 __attribute__((ext_vector_type(8)));
     const int half = i & 1;
@@ -345,6 +348,32 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendParams p
     uint32_t rows = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
         (Lds4)(tile + (4 * g + (col >> 2)) * kPitch + kPlane * ((col >> 1) & 1) + 8 * (col & 1) + 16 * (quarter * NC))));
     auto join = [](u32v2 lo, u32v2 hi) { return __builtin_bit_cast(bf16x8, u32v4{lo[0], lo[1], hi[0], hi[1]}); };
+    auto value = [&](int c) {
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds4)(uintptr_t)(rows + 16 * c));
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds4)(uintptr_t)(rows + 16 * kPitch + 16 * c));
+      return __builtin_bit_cast(bf16x8, s16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
+    };
+    // The wave's channels of a tile are its own.  Where they are the keys' too, the row's score has told (it is no number either).
+    if (forked && spot.first + i >= spot.main_tiles) {
+      if constexpr (!SHARED) {
+        bf16x8 sees[RT];
+#pragma unroll
+        for (int m = 0; m < RT; ++m)
+          sees[m] = seen_places((lds.sees[half][0][16 * m + col] | lds.sees[half][1][16 * m + col] << 16) >> (4 * g));
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          const bf16x8 odd = odd_places(value(c));
+#pragma unroll
+          for (int m = 0; m < RT; ++m) out[m][c] = spoilt(out[m][c], odd, sees[m]);
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      }
+      for (int n = lane; n < kTile * 2 * NC; n += 64) {
+        const int row = n / (2 * NC), piece = n % (2 * NC);
+        clear_odd(tile + row * kPitch + (piece & 1) * kPlane + 16 * (quarter * NC + (piece >> 1)));
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
 #pragma unroll
     for (int m0 = 0; m0 < RT; m0 += 2) {
       bf16x8 prob[2][2];
@@ -378,9 +407,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendParams p
       asm volatile("" : "+v"(rows));
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds4)(uintptr_t)(rows + 16 * c));
-        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds4)(uintptr_t)(rows + 16 * kPitch + 16 * c));
-        const bf16x8 v = __builtin_bit_cast(bf16x8, s16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
+        const bf16x8 v = value(c);
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll

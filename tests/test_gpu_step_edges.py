@@ -52,3 +52,46 @@ def test_joins_with_lanes_left_over(Dv, n):
     out, lse = ets.attend_selected(q.to(dev()), kg, ksg, vg, vsg, slots.to(dev()))
     close(out, want[0], want[2], FP16)
     close(lse, want[1], want[3], FP32)
+
+
+def close_where_numbers(got, want, bound, dtype):
+    """close(), with numbers in the same places."""
+    none = torch.isnan(want)
+    assert torch.equal(torch.isnan(got.cpu()), none)
+    close(got.cpu().masked_fill(none, 0), want.masked_fill(none, 0), bound.masked_fill(none, 0), dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("T", [5, 40])  # drafted tokens of one tile, and of two
+@pytest.mark.parametrize("shape", [(2, 2, 64, 64), (12, 2, 128, 96), (4, 1, 192, 192), (3, 1, 256, 256), (6, 1, 256, 128),
+                                   (3, 1, 320, 320), (2, 1, 576, 512)])
+def test_drafted_tokens_that_are_no_numbers(shape, T, dtype):
+    """A draft with a value that is no number spoils the channels and heads of the tokens that see it, and nothing else."""
+    Hq, Hkv, D, Dv = shape
+    g = gen(23)
+    B, page, n = 2, 16, 70
+    lens = torch.tensor([37, 70], dtype=torch.int32)
+    per = -(-(n + T) // page)
+    table = torch.randperm(B * per, generator=g).to(torch.int32).view(B, per)
+    kc, ks, _, _ = cache(B * per * page, Hkv, D, g)
+    latent = Dv == 512
+    vc, vs = (kc[..., :Dv], ks[..., :Dv // 32]) if latent else cache(B * per * page, Hkv, Dv, g)[:2]
+    drafts = torch.stack([ref.slots_of(table[b], page, int(lens[b]) + torch.arange(T)) for b in range(B)])
+    # draft 0 is the root of all; 1 hangs on it, 2 on 1, the others on 0; nobody sees the last
+    mask = torch.tensor([1, 3, 7] + [1 | 1 << t for t in range(3, T - 1)] + [1]).repeat(B, 1)
+    codes = vc.view(torch.uint8)
+    codes[drafts[0, 1], -1, 5], codes[drafts[1, 3], 0, Dv - 1] = 0x7F, 0xFF
+    if not latent:
+        kc.view(torch.uint8)[drafts[1, 2], 0, 0] = 0x7F
+    codes[drafts[:, T - 1]], vs[drafts[:, T - 1]] = 0x7F, 255  # a place that was never written
+    kc.view(torch.uint8)[drafts[:, T - 1]] = 0xFF
+    q = torch.randn(B, T, Hq, D, generator=g).to(dtype)
+    lists = [[ref.slots_of(table[b], page, torch.arange(int(lens[b])))] * T for b in range(B)]
+    want = two_parts(q, kc, ks, vc, vs, lists, drafts, mask)
+    assert torch.isnan(want[0][0, 1]).any() and torch.isfinite(want[0][:, 0]).all() and torch.isfinite(want[0][:, T - 1]).all()
+    kg, ksg = kc.to(dev()), ks.to(dev())
+    vg, vsg = (kg[..., :Dv], ksg[..., :Dv // 32]) if latent else (vc.to(dev()), vs.to(dev()))
+    out, lse = ets.attend_paged(q.to(dev()), kg, ksg, vg, vsg, table.to(dev()), lens.to(dev()), page, n,
+                                tree_slots=drafts.to(torch.int32).to(dev()), tree_mask=mask.to(dev()))
+    close_where_numbers(out, want[0], want[2], dtype)
+    close_where_numbers(lse, want[1], want[3], FP32)
