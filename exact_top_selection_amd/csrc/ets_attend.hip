@@ -188,7 +188,7 @@ __global__ __launch_bounds__(kThreads, attend_per_unit(NP, MT)) void attend_kern
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       uint32_t r = 0;
-      if constexpr (M::kRowScale) r = row_top<NP, FULL>(now.kbyte[s]);
+      if constexpr (M::kRowScale) r = row_top<NP, FULL>(now.kbyte[s], now.k[s], g);
       row_scale[s] = __uint_as_float(r << 23);
 #pragma unroll
       for (int m = 0; m < MT; ++m) score[m][s] = f32x4{};

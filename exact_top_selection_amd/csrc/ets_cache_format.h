@@ -125,11 +125,39 @@ __device__ __forceinline__ float rows_max(float x) {
   return fmaxf(__uint_as_float(t[0]), __uint_as_float(t[1]));
 }
 
-// The largest scale byte of a row, in all of its lanes (bytes as powers of two keep their order).
+// The exponent that a row is taken over, in all of its lanes, as a scale byte:
+// the row's largest one where every 16 codes have one of at least 2, as those
+// of cache_write nearly always do (so that the largest block's values reach
+// high).  A block of zeros, or of codes that are small for their scale, says
+// nothing of the row's size: with one in sight the byte follows the largest
+// value, so that it comes to lie in [2^8, 2^9).  (Byte 0: a row or channels that are
+// not there.)
 template <int NP, bool FULL>
-__device__ __forceinline__ uint32_t row_top(const uint32_t (&w)[RowScales<NP, FULL>::n]) {
+__device__ __forceinline__ uint32_t row_top(const uint32_t (&w)[RowScales<NP, FULL>::n], const u32v4 (&codes)[NP], int g) {
   typedef RowScales<NP, FULL> R;
+  bool small = false;
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    const u32v4 c = codes[i];
+    small = small || (((c[0] | c[1] | c[2] | c[3]) & 0x40404040u) == 0 && R::byte(w, i, g) != 0);
+  }
   uint32_t top = 0;
+  if (__any(small)) {
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      u16x2 high = {0, 0};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        high = __builtin_elementwise_max(high, __builtin_bit_cast(u16x2, codes[i][j] & 0x007f007fu));
+        high = __builtin_elementwise_max(high, __builtin_bit_cast(u16x2, codes[i][j] >> 8 & 0x007f007fu));
+      }
+      const uint32_t code = max(high[0], high[1]);
+      const int byte = static_cast<int>(R::byte(w, i, g)) - 15 + static_cast<int>(code >> 3);
+      top = code ? max(top, static_cast<uint32_t>(max(byte, 1))) : top;
+    }
+    return __float_as_uint(rows_max(__uint_as_float(top << 23))) >> 23;
+  }
   if constexpr (R::kWhole) {
 #pragma unroll
     for (int i = 0; i < 2 * NP; ++i) top = max(top, __builtin_amdgcn_ubfe(w[i / 4], 8 * (i & 3), 8));
@@ -162,10 +190,11 @@ __device__ __forceinline__ f16x8 codes_f16(uint32_t lo, uint32_t hi, float scale
 // The matrix operand types of a query type.  A key is brought to the query's
 // own type, so that products are exact in 32 bits:
 //   bf16  the key's values;
-//   fp16  the key's values over 2^(r - 127), r the row's largest scale byte:
-//         at most 448, and a block 2^15 and more below the row's largest
-//         loses bits only beneath 2^-33 of it.  The product is multiplied by
-//         2^(r - 127) afterwards.
+//   fp16  the key's values over 2^(r - 127), r from row_top: less than 2^9, and
+//         a block far below the row's largest loses bits only beneath 2^-25,
+//         which is 2^-33 of the row's largest value (2^-26 where no code of the
+//         largest block is over 2).  The product is multiplied by 2^(r - 127)
+//         afterwards.
 template <class T>
 struct Mat;
 template <>
@@ -184,7 +213,7 @@ struct Mat<_Float16> {
   static constexpr bool kRowScale = true;
   static __device__ __forceinline__ float scale(uint32_t byte, uint32_t top) {
     const int e = static_cast<int>(byte) - static_cast<int>(top) + kScaleBias;
-    return __uint_as_float(static_cast<uint32_t>(e < 0 ? 0 : e) << 23);
+    return __uint_as_float(static_cast<uint32_t>(min(max(e, 0), 254)) << 23);  // over 142 for blocks of zeros only
   }
   static __device__ __forceinline__ V8 keys(uint32_t lo, uint32_t hi, float s) { return codes_f16(lo, hi, s); }
   static __device__ __forceinline__ f32x4 mma(V8 a, V8 b, f32x4 c) {

@@ -207,7 +207,7 @@ __global__ __launch_bounds__(kThreads, NP <= 2 ? 4 : NP == 3 ? 3 : 2) void score
 #pragma unroll
     for (int s = 0; s < kSub; ++s) {
       top[s] = 0;
-      if constexpr (M::kRowScale) top[s] = row_top<NP, FULL>(byte[s]);
+      if constexpr (M::kRowScale) top[s] = row_top<NP, FULL>(byte[s], raw[s], g);
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         const float f = M::scale(KS::byte(byte[s], i, g), top[s]);

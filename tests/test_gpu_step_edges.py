@@ -95,3 +95,40 @@ def test_drafted_tokens_that_are_no_numbers(shape, T, dtype):
                                 tree_slots=drafts.to(torch.int32).to(dev()), tree_mask=mask.to(dev()))
     close_where_numbers(out, want[0], want[2], dtype)
     close_where_numbers(lse, want[1], want[3], FP32)
+
+
+def uneven_blocks(n, D, size, g):
+    """A cache whose rows hold values of about `size`, blocks of zeros under scales of all sizes, and blocks whose codes are
+    far smaller than their scale lets them be."""
+    codes, scales = ref.quantise(torch.randn(n, 1, D, generator=g) * size)
+    for block in range(D // 32):
+        kind = torch.randint(0, 4, (n,), generator=g)
+        at = slice(32 * block, 32 * block + 32)
+        empty = kind == 1
+        codes[empty, :, at] = 0
+        scales[empty, :, block] = torch.tensor([1, 118, 246], dtype=torch.uint8)[torch.randint(0, 3, (int(empty.sum()), 1), generator=g)]
+        small = kind == 2  # codes up to 2^-6, the same values as the others'
+        codes[small, :, at] = torch.randint(0, 8, (int(small.sum()), 1, 32), generator=g, dtype=torch.uint8)
+        scales[small, :, block] = (scales[small, :, block].int() + 14).clamp(max=246).to(torch.uint8)
+    return codes, scales
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("D", [32, 64, 96, 128, 192, 256])
+@pytest.mark.parametrize("size", [1.0, 1e-4, 1e-8, 1e-10, 1e-30])
+def test_keys_with_blocks_of_zeros_and_small_codes(size, D, dtype):
+    g = gen(24)
+    n = 150
+    kc, ks = uneven_blocks(n, D, size, g)
+    kg, ksg = kc.to(dev()), ks.to(dev())
+    q, w = torch.randn(1, 2, 8, D, generator=g).to(dtype), torch.randn(1, 2, 8, generator=g)
+    table, lens = torch.arange(n, dtype=torch.int32).view(1, n), torch.tensor([n], dtype=torch.int32)
+    want, bound = ref.index_scores(q, w, kc, ks, table, lens, 1, n)
+    got = ets.index_scores(q.to(dev()), w.to(dev()), kg, ksg, table.to(dev()), lens.to(dev()), 1, n)
+    close(got, want, bound, FP32)
+    vc, vs, vg, vsg = cache(n, 1, D, g)
+    q = (q.double() / size).clamp(-60000, 60000).to(dtype)  # scores of about 1, as far as the type goes
+    want = two_parts(q, kc, ks, vc, vs, [[table[0], table[0]]])
+    out, lse = ets.attend_paged(q.to(dev()), kg, ksg, vg, vsg, table.to(dev()), lens.to(dev()), 1, n)
+    close(out, want[0], want[2], dtype)
+    close(lse, want[1], want[3], FP32)
