@@ -24,6 +24,8 @@ from . import _check, _load, _on, _require, _rows, _same_device, _stream, _vec
 
 CACHE_BLOCK = 32
 MAX_ROPE_DIM, MAX_HEAD_DIM, MAX_INDEX_DIM, MAX_INDEX_HEADS, MAX_TREE = 4096, 576, 256, 128, 64
+MAX_LENGTH = 0x7FFFF000  # positions of a sequence, slots of a list
+_INT32 = 0x7FFFFFFF      # sizes are 32-bit numbers in the C ABI, which ctypes would cut silently
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _LAYOUTS = {"interleaved": 0, "half": 1}
 
@@ -118,8 +120,8 @@ def _cache(codes: torch.Tensor, scales: torch.Tensor, name: str) -> Tuple[int, i
     S, H, D = codes.shape
     if D < CACHE_BLOCK or D % CACHE_BLOCK:
         raise ValueError("%scodes must have a multiple of %d channels, got %d" % (name, CACHE_BLOCK, D))
-    if H < 1 or S > 0x7FFFFFFF:
-        raise ValueError("%scodes must have at least one head and fewer than 2^31 slots" % name)
+    if H < 1 or S > _INT32 or H * D > 1 << 28:
+        raise ValueError("%scodes must have at least one head, at most 2^28 values a slot and fewer than 2^31 slots" % name)
     if scales.shape != (S, H, D // CACHE_BLOCK):
         raise ValueError("%sscales must have shape %s, got %s" % (name, (S, H, D // CACHE_BLOCK), tuple(scales.shape)))
     if codes.stride(2) != 1 or (D > CACHE_BLOCK and scales.stride(2) != 1):
@@ -163,8 +165,8 @@ def rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, layou
     pairs = _LAYOUTS.get(layout)
     if pairs is None:
         raise ValueError("layout must be 'interleaved' or 'half', got %r" % (layout,))
-    if D < 1 or D > MAX_ROPE_DIM:
-        raise ValueError("x must have 1 to %d channels, got %d" % (MAX_ROPE_DIM, D))
+    if D < 1 or D > MAX_ROPE_DIM or H > _INT32:
+        raise ValueError("x must have 1 to %d channels and at most %d heads, got %d and %d" % (MAX_ROPE_DIM, _INT32, D, H))
     if offset < 0 or offset + R > D:
         raise ValueError("channels [%d, %d) do not lie inside the %d of x" % (offset, offset + R, D))
     if out is None:
@@ -237,8 +239,8 @@ def _pages(page_table: torch.Tensor, seq_lens: torch.Tensor, page_size: int, L: 
     _vec(seq_lens, "seq_lens", B)
     if page_table.shape[0] != B:
         raise ValueError("page_table must have %d rows, got %d" % (B, page_table.shape[0]))
-    if page_size < 1 or L < 0:
-        raise ValueError("page_size must be >= 1 and L >= 0")
+    if not 1 <= page_size <= _INT32 or not 0 <= L <= MAX_LENGTH:
+        raise ValueError("page_size must be 1 to %d and L 0 to %d, got %s and %s" % (_INT32, MAX_LENGTH, page_size, L))
     if page_table.shape[1] * page_size < L:
         raise ValueError("page_table has %d pages of %d, fewer than L = %d positions"
                          % (page_table.shape[1], page_size, L))
@@ -268,6 +270,8 @@ def index_scores(q: torch.Tensor, weights: torch.Tensor, codes: torch.Tensor, sc
         raise ValueError("codes must have shape [S, 1, %d], got %s" % (D, tuple(codes.shape)))
     if D > MAX_INDEX_DIM or not 1 <= H <= MAX_INDEX_HEADS:
         raise ValueError("q must have 1 to %d heads of at most %d channels" % (MAX_INDEX_HEADS, MAX_INDEX_DIM))
+    if B > 65535 or T > _INT32:
+        raise ValueError("q must have at most 65535 sequences and %d tokens, got %d and %d" % (_INT32, B, T))
     _pages(page_table, seq_lens, page_size, L, B)
     _same_device(index, (weights, "weights"), (codes, "codes"), (scales, "scales"), (page_table, "page_table"),
                  (seq_lens, "seq_lens"))
@@ -301,6 +305,8 @@ def _attend(what, q, k_codes, k_scales, v_codes, v_scales, tree_slots, tree_mask
         raise ValueError("v_codes must have the slots and heads of k_codes %s, got %s" % ((S, Hkv), (Sv, Hv)))
     if D > MAX_HEAD_DIM or Dv > MAX_HEAD_DIM:
         raise ValueError("heads may have at most %d channels" % MAX_HEAD_DIM)
+    if B * T * Hq > _INT32:
+        raise ValueError("q must have at most %d rows, got %d" % (_INT32, B * T * Hq))
     if Hq < 1 or Hq % Hkv:
         raise ValueError("q must have a multiple of the cache's %d heads, got %d" % (Hkv, Hq))
     _same_device(index, (k_codes, "k_codes"), (k_scales, "k_scales"), (v_codes, "v_codes"), (v_scales, "v_scales"),
@@ -369,6 +375,8 @@ def attend_selected(q: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.Tens
     _require(slots, "slots", torch.int32, 3)
     if not isinstance(q, torch.Tensor) or q.ndim != 4 or slots.shape[:2] != q.shape[:2]:
         raise ValueError("slots must have shape [B, T, K] like q [B, T, Hq, D], got %s" % (tuple(slots.shape),))
+    if slots.shape[2] > MAX_LENGTH:
+        raise ValueError("slots must have at most %d entries a token, got %d" % (MAX_LENGTH, slots.shape[2]))
     if slots.shape[2] > 1 and slots.stride(2) != 1:
         raise ValueError("slots must be contiguous in its last dimension")
     return _attend("ets_attend (selected)", q, k_codes, k_scales, v_codes, v_scales, tree_slots, tree_mask, workspace,

@@ -474,7 +474,8 @@ ets_status make_plan(const ets_attend_args* a, Plan* plan) {
     return ETS_ERR_INVALID_ARG;
   if ((a->dtype != ETS_BF16 && a->dtype != ETS_FP16) || a->S < 0 || a->S > INT32_MAX) return ETS_ERR_INVALID_ARG;
   const bool paged = a->slots == nullptr;
-  if (paged ? (a->L < 0 || a->page_size < 1) : a->K < 0) return ETS_ERR_INVALID_ARG;
+  // positions are 32-bit numbers in the kernels, and stand up to 3 chunks of slots behind a list's end
+  if (paged ? (a->L < 0 || a->L > ETS_MAX_LENGTH || a->page_size < 1) : (a->K < 0 || a->K > ETS_MAX_LENGTH)) return ETS_ERR_INVALID_ARG;
   if (a->tree_slots && a->T > ETS_MAX_TREE) return ETS_ERR_INVALID_ARG;
   // row strides are 32-bit numbers in the kernels; 4 GiB from slot to slot is no cache
   if (a->k_s < 0 || a->ks_s < 0 || a->v_s < 0 || a->vs_s < 0 || (a->k_s | a->ks_s | a->v_s | a->vs_s) > UINT32_MAX)

@@ -13,6 +13,7 @@ constexpr int kTile = 16 * kSub;    // keys of a wave's step, held in registers
 constexpr int kUnit = 128;          // keys by which the work is dealt out: a step of all waves
 constexpr int kPiece = 2048;        // keys of a workgroup between barriers
 constexpr int kFill = 1024;         // positions past a length that are filled at a time
+static_assert(ETS_MAX_LENGTH <= INT32_MAX - kPiece, "positions are 32-bit numbers, and stand up to a piece behind a length");
 constexpr int kQueryBytes = 65536;  // queries that a workgroup keeps in LDS
 constexpr float kNegInf = -__builtin_inff();
 
@@ -290,7 +291,7 @@ ets_status ets_index_scores(const void* q, int64_t q_b, int64_t q_t, int64_t q_h
                             int64_t out_stride, int32_t dtype, void* stream) {
   using namespace ets;
   if (B < 0 || B > 65535 || T < 0 || H < 1 || H > ETS_MAX_INDEX_HEADS || D < kCacheBlock || D % kCacheBlock ||
-      D > ETS_MAX_INDEX_DIM || S < 0 || S > INT32_MAX || page_size < 1 || L < 0 || out_stride < L ||
+      D > ETS_MAX_INDEX_DIM || S < 0 || S > INT32_MAX || page_size < 1 || L < 0 || L > ETS_MAX_LENGTH || out_stride < L ||
       (dtype != ETS_BF16 && dtype != ETS_FP16) ||
       codes_s < 0 || codes_s > UINT32_MAX || scales_s < 0 || scales_s > UINT32_MAX || static_cast<int64_t>(B) * ((static_cast<int64_t>(L) + kFill - 1) / kFill) > INT32_MAX)
     return ETS_ERR_INVALID_ARG;

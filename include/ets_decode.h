@@ -50,6 +50,7 @@ extern "C" {
 #define ETS_MAX_INDEX_DIM 256   /* largest D of index scores */
 #define ETS_MAX_INDEX_HEADS 128 /* largest H of index scores */
 #define ETS_MAX_TREE 64         /* most drafted tokens of a sequence */
+#define ETS_MAX_LENGTH 0x7ffff000 /* most positions of a sequence, slots of a list */
 
 /*
  * Rotates channels [offset, offset + R) of x[N][H][D] and copies the others.
@@ -97,7 +98,7 @@ ets_status ets_cache_read(const uint8_t* codes, int64_t codes_s, int64_t codes_h
  * infinity.  Sums are held in 32 bits.
  *   q        [B][T][H][D], bf16 or fp16.   weights  float [B][T][H].
  *   codes    row of slot s at s * codes_s.  D <= ETS_MAX_INDEX_DIM,
- *            H <= ETS_MAX_INDEX_HEADS, B <= 65535.
+ *            H <= ETS_MAX_INDEX_HEADS, B <= 65535, L <= ETS_MAX_LENGTH.
  *   page_table int32 [B][>= ceil(L / page_size)], rows pt_b apart.
  *   out      float [B * T][out_stride >= L].
  */
@@ -126,8 +127,8 @@ ets_status ets_index_scores(const void* q, int64_t q_b, int64_t q_t, int64_t q_h
 typedef struct ets_attend_args {
   int32_t B, T, Hq, Hkv, D, Dv;
   int32_t dtype;          /* of q and out: ETS_BF16 or ETS_FP16 */
-  int32_t K;              /* selected: slots of a token */
-  int32_t L;              /* paged: capacity of a sequence */
+  int32_t K;              /* selected: slots of a token, at most ETS_MAX_LENGTH */
+  int32_t L;              /* paged: capacity of a sequence, at most ETS_MAX_LENGTH */
   int32_t page_size;      /* paged */
   int64_t S;              /* slots of the cache */
   const void* q;          /* [B][T][Hq][D] */

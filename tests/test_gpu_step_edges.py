@@ -132,3 +132,24 @@ def test_keys_with_blocks_of_zeros_and_small_codes(size, D, dtype):
     out, lse = ets.attend_paged(q.to(dev()), kg, ksg, vg, vsg, table.to(dev()), lens.to(dev()), 1, n)
     close(out, want[0], want[2], dtype)
     close(lse, want[1], want[3], FP32)
+
+
+def test_sizes_are_not_cut_to_32_bits():
+    new = dict(device="cuda:0")
+    codes, scales = torch.zeros(8, 1, 64, dtype=torch.uint8, **new), torch.full((8, 1, 2), 127, dtype=torch.uint8, **new)
+    q, w = torch.zeros(1, 1, 4, 64, dtype=torch.bfloat16, **new), torch.zeros(1, 1, 4, **new)
+    lens = torch.ones(1, dtype=torch.int32, **new)
+    table = torch.zeros(1, 3, dtype=torch.int32, **new)
+    for page, L in (((1 << 32) + 4, 4), (1 << 31, 4), (1 << 31, (1 << 32) + 4), (1 << 30, 0x7FFFF001)):
+        with pytest.raises(ValueError, match="page_size must be"):
+            ets.attend_paged(q, codes, scales, codes, scales, table, lens, page, L)
+        with pytest.raises(ValueError, match="page_size must be"):
+            ets.index_scores(q, w, codes, scales, table, lens, page, L)
+    many = q[:, :, :1].expand(1, (1 << 32) + 1, 1, 64)  # one token's memory
+    with pytest.raises(ValueError, match="tokens"):
+        ets.index_scores(many, w[:, :, :1].expand(1, (1 << 32) + 1, 1), codes, scales, table, lens, 4, 0)
+    with pytest.raises(ValueError, match="rows"):
+        ets.attend_paged(many, codes, scales, codes, scales, table, lens, 4, 4)
+    x = torch.zeros(1, 1, 64, dtype=torch.bfloat16, **new).expand(1, (1 << 32) + 1, 64)
+    with pytest.raises(ValueError, match="heads"):
+        ets.rope(x, lens, torch.zeros(2, dtype=torch.float64, **new), out=x)
