@@ -11,8 +11,9 @@ constexpr int kAttendThreads = 256;
 constexpr int kAttendWaves = 4;
 constexpr int kAttendTile = 32;  // keys of a step
 constexpr float kNegInf = -__builtin_inff();
-// How far (log2) a score may pass the reference that its softmax is taken relative to, before the reference
-// follows: probabilities up to 2^24 are as exact as those up to 1, and a list raises its reference once or twice.
+// How far (log2) the reference that a softmax is taken relative to is put above the score that raises it: the largest
+// probability lies between 2^-24 and 1 from then on, as exact as one of 1, sums of values stay as far from overflow as the
+// values' own sum, and a list raises its reference once or twice.
 constexpr float kSlack = 24.0f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
@@ -150,7 +151,9 @@ __device__ __forceinline__ void clear_odd(void* eight) {  // in LDS
 }
 
 __device__ __forceinline__ float attend_lse(float reference, float sum) {
-  return sum == 0.0f ? kNegInf : (reference + __builtin_amdgcn_logf(sum)) * kLn2;
+  // the sum's exponent first: it may cancel the reference's distance from the largest score
+  const float whole = reference + static_cast<float>(__builtin_amdgcn_frexp_expf(sum));
+  return sum == 0.0f ? kNegInf : (whole + __builtin_amdgcn_logf(__builtin_amdgcn_frexp_mantf(sum))) * kLn2;
 }
 __device__ __forceinline__ float attend_inverse(float sum) {
   return sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;

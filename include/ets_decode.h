@@ -121,8 +121,10 @@ ets_status ets_index_scores(const void* q, int64_t q_b, int64_t q_t, int64_t q_h
  *     page_table[b][p / page_size] * page_size + p % page_size;
  *   - tree_slots != NULL: also tree_slots[b][j] for each j < T with bit j of
  *     tree_mask[b][t] set.
- * Products are exact in the type of the matrix instructions; scores, softmax
- * statistics and output sums are held in 32 bits.
+ * Scores, softmax statistics and output sums are held in 32 bits: sums of p_j
+ * v_j with 0 <= p_j <= 1 and the largest p_j at least 2^-24, so that they are
+ * finite where the sum of the values is, and lose what lies beneath 2^-100 in
+ * values.
  */
 typedef struct ets_attend_args {
   int32_t B, T, Hq, Hkv, D, Dv;

@@ -153,3 +153,33 @@ def test_sizes_are_not_cut_to_32_bits():
     x = torch.zeros(1, 1, 64, dtype=torch.bfloat16, **new).expand(1, (1 << 32) + 1, 64)
     with pytest.raises(ValueError, match="heads"):
         ets.rope(x, lens, torch.zeros(2, dtype=torch.float64, **new), out=x)
+
+
+def every_list(q, kc, ks, vc, vs, slots, sample, **kw):
+    """attend_selected of all rows, with the oracle's results for the sampled sequences: (out, lse, want)."""
+    kg, ksg = kc.to(dev()), ks.to(dev())
+    vg, vsg = (kg[..., :vc.shape[2]], ksg[..., :vs.shape[2]]) if vc.data_ptr() == kc.data_ptr() else (vc.to(dev()), vs.to(dev()))
+    out, lse = ets.attend_selected(q.to(dev()), kg, ksg, vg, vsg, slots.to(dev()), **kw)
+    want = two_parts(q[sample], kc, ks, vc, vs, [[slots[b, t] for t in range(q.shape[1])] for b in sample])
+    return out[sample], lse[sample], want
+
+
+@pytest.mark.parametrize("size", [2.0 ** 112, 1.0, 2.0 ** -90])
+@pytest.mark.parametrize("order", ["rising", "falling", "mixed"])
+@pytest.mark.parametrize("shape", [(600, 1, 64, 64), (600, 20, 128, 128), (600, 20, 256, 256), (300, 4, 576, 512), (300, 64, 576, 512),
+                                   (300, 2, 320, 320)])
+def test_values_near_the_ends_of_the_range(shape, order, size):
+    """Many lists, so that a wave takes several tiles: scores pass each other by up to 2^20, values reach 2^115 and 2^-90."""
+    B, Hq, D, Dv = shape
+    g, n = gen(25), 400
+    x = torch.randn(n, 1, D, generator=g, dtype=torch.float64) * size
+    x[..., D - 32:] = 0
+    x[..., D - 1] = 20 * torch.arange(n).double().view(n, 1) / n / math.log2(math.e) * math.sqrt(D)  # the score of a query's last channel
+    kc, ks = ref.quantise(x)
+    vc, vs = (kc[..., :Dv], ks[..., :Dv // 32]) if Dv == 512 else ref.quantise(x[..., torch.arange(Dv) % (D - 32)])
+    q = torch.zeros(B, 1, Hq, D, dtype=BF16)
+    q[..., D - 1] = (torch.arange(B * Hq).view(B, 1, Hq) % 5 - 2) / 2
+    slots = {"rising": torch.arange(n), "falling": torch.arange(n).flip(0), "mixed": torch.randperm(n, generator=g)}[order]
+    out, lse, want = every_list(q, kc, ks, vc, vs, slots.to(torch.int32).expand(B, 1, n).contiguous(), [0, B // 2, B - 1])
+    close(out, want[0], want[2], BF16)
+    close(lse, want[1], want[3], FP32)
