@@ -237,7 +237,7 @@ __global__ __launch_bounds__(kThreads, attend_per_unit(NP, MT)) void attend_kern
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         x[j] = __builtin_fmaf(score[m][j >> 2][j & 3], p.scale_log2, -top[m]);
-        high = fmaxf(high, x[j]);
+        high = __builtin_elementwise_maximum(high, x[j]);  // no number (a score of -inf less a reference of -inf) passes no test
       }
       if (seen_now != ~0u || tile >= main_tiles || !__all(high <= 0.0f)) {
         uint32_t vis = seen_now;

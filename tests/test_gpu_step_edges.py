@@ -183,3 +183,28 @@ def test_values_near_the_ends_of_the_range(shape, order, size):
     out, lse, want = every_list(q, kc, ks, vc, vs, slots.to(torch.int32).expand(B, 1, n).contiguous(), [0, B // 2, B - 1])
     close(out, want[0], want[2], BF16)
     close(lse, want[1], want[3], FP32)
+
+
+@pytest.mark.parametrize("behind", [True, False])
+@pytest.mark.parametrize("shape", [(16, 64, 64), (32, 128, 128), (16, 256, 256), (64, 576, 512), (32, 320, 320)])
+def test_scores_of_minus_infinity(shape, behind):
+    """Keys whose score leaves the 32-bit range: alone in a list they are nothing, before others they weigh nothing."""
+    Hq, D, Dv = shape
+    g, n = gen(26), 200
+    x = torch.zeros(n, 1, D, dtype=torch.float64)
+    x[..., :D - 32] = torch.randn(n, 1, D - 32, generator=g)
+    x[..., D - 1] = 8.0
+    if behind:
+        x[160:, 0, D - 1] = 2.0 ** -126 * (torch.arange(40) % 5).double()
+    kc, ks = ref.quantise(x)
+    vc, vs = (kc[..., :Dv], ks[..., :Dv // 32]) if Dv == 512 else ref.quantise(torch.randn(n, 1, Dv, generator=g).double())
+    q = torch.zeros(300, 1, Hq, D, dtype=BF16)
+    q[..., D - 1] = -2.0 ** 127
+    slots = torch.arange(n, dtype=torch.int32).expand(300, 1, n).contiguous()
+    kg, ksg = kc.to(dev()), ks.to(dev())
+    vg, vsg = (kg[..., :Dv], ksg[..., :Dv // 32]) if Dv == 512 else (vc.to(dev()), vs.to(dev()))
+    out, lse = ets.attend_selected(q.to(dev()), kg, ksg, vg, vsg, slots.to(dev()))
+    want = two_parts(q[:1], kc, ks, vc, vs, [[torch.arange(160, n) if behind else torch.arange(0)]])
+    for b in (0, 299):
+        close(out[b:b + 1], want[0], want[2], BF16)
+        close(lse[b:b + 1], want[1], want[3], FP32)
