@@ -258,7 +258,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendParams p
 #pragma unroll
         for (int m = 0; m < MQ; ++m) {
           uint32_t vis = seen;
-          if (at >= spot.main_tiles) vis &= static_cast<uint32_t>(tree_bits[m] >> (kTile * (at - spot.main_tiles) + 16 * team));
+          if (at >= spot.main_tiles) vis &= static_cast<uint32_t>(tree_bits[m] >> (kTile * (at - spot.main_tiles) + 16 * team & 63));
           if (!SHARED && forked && g == 0) lds.sees[half][team][(MQ * hg + m) * 16 + col] = vis;
           vis >>= 4 * g;
           float high = kNegInf;
