@@ -19,6 +19,7 @@ import ctypes
 from typing import Optional, Tuple
 
 import torch
+from torch.autograd import forward_ad as _forward
 
 from . import _check, _load, _on, _require, _rows, _same_device, _stream, _vec
 
@@ -101,9 +102,12 @@ def _run(index: int, what: str, fn, *args) -> None:
         _check(st, what)
 
 
-def _no_grad(t: torch.Tensor, name: str, what: str) -> None:
+def _no_grad(t: torch.Tensor, name: str, what: str, instead: str = "call it under torch.no_grad()") -> None:
+    """Refuses a tensor whose gradient or tangent the call would drop."""
     if t.requires_grad and torch.is_grad_enabled():
-        raise ValueError("%s has no gradient: detach %s, or call it under torch.no_grad()" % (what, name))
+        raise ValueError("%s records no gradient: detach %s, or %s" % (what, name, instead))
+    if _forward._current_level >= 0 and _forward.unpack_dual(t).tangent is not None:
+        raise ValueError("%s has no forward-mode derivative: take the primal of %s" % (what, name))
 
 
 def _cache(codes: torch.Tensor, scales: torch.Tensor, name: str) -> Tuple[int, int, int]:
@@ -149,8 +153,7 @@ def rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, layou
     ``x`` is bf16, fp16 or fp32; ``out`` may be ``x``.
     """
     kind = _floats(x, "x", 3)
-    if x.requires_grad and torch.is_grad_enabled():
-        raise ValueError("rope records no gradient: detach x, and take its gradient as rope(grad, ..., inverse=True)")
+    _no_grad(x, "x", "rope", "take its gradient as rope(grad, ..., inverse=True)")
     N, H, D = x.shape
     strides = x.stride()
     index = x.get_device()
@@ -159,6 +162,7 @@ def rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, layou
             and inv_freq.get_device() == index):
         _require(inv_freq, "inv_freq", torch.float64, 1)
         _same_device(index, (inv_freq, "inv_freq"))
+    _no_grad(inv_freq, "inv_freq", "rope")
     R = 2 * inv_freq.shape[0]
     if R > 2 and inv_freq.stride(0) != 1:
         raise ValueError("inv_freq must be contiguous")
@@ -174,6 +178,7 @@ def rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, layou
         to_n, to_h = H * D, D
     else:
         _floats(out, "out", 3)
+        _no_grad(out, "out", "rope")
         if out.shape != x.shape or out.dtype is not x.dtype or out.get_device() != index:
             raise ValueError("out must have the shape, type and device of x")
         if _overlaps(out):
@@ -227,6 +232,8 @@ def cache_read(codes: torch.Tensor, scales: torch.Tensor, slots: torch.Tensor, d
         out = codes.new_empty((N, H, D), dtype=dtype)
     elif out.dtype is not dtype or out.shape != (N, H, D) or out.get_device() != index or not out.is_contiguous():
         raise ValueError("out must be contiguous %s [%d, %d, %d] on cuda:%d" % (dtype, N, H, D, index))
+    else:
+        _no_grad(out, "out", "cache_read")
     codes_s, codes_h, _ = codes.stride()
     scales_s, scales_h, _ = scales.stride()
     _run(index, "ets_cache_read", _lib().ets_cache_read, codes.data_ptr(), codes_s, codes_h, scales.data_ptr(), scales_s,
@@ -279,6 +286,7 @@ def index_scores(q: torch.Tensor, weights: torch.Tensor, codes: torch.Tensor, sc
         out = torch.empty((B * T, L), dtype=torch.float32, device=q.device)
     else:
         _require(out, "out", torch.float32, 2)
+        _no_grad(out, "out", "index_scores")
         if out.shape != (B * T, L) or out.get_device() != index:
             raise ValueError("out must be float32 [%d, %d] on cuda:%d" % (B * T, L, index))
         if B * T > 1 and out.stride(0) < L:

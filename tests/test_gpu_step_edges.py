@@ -208,3 +208,37 @@ def test_scores_of_minus_infinity(shape, behind):
     for b in (0, 299):
         close(out[b:b + 1], want[0], want[2], BF16)
         close(lse[b:b + 1], want[1], want[3], FP32)
+
+
+def test_derivatives_are_refused_not_dropped():
+    """Inputs and outputs that require gradients, and inputs that carry a tangent."""
+    import torch.autograd.forward_ad as forward
+    g = gen(27)
+    _, _, kg, ksg = cache(8, 1, 64, g)
+    q = torch.randn(1, 1, 4, 64, generator=g).to(BF16).to(dev())
+    x = torch.randn(2, 1, 64, generator=g).to(dev())
+    w, i2 = torch.ones(1, 1, 4, device=dev()), torch.arange(2, dtype=torch.int32, device=dev())
+    freq = torch.ones(8, dtype=torch.float64, device=dev())
+    table, lens = torch.zeros(1, 1, dtype=torch.int32, device=dev()), torch.ones(1, dtype=torch.int32, device=dev())
+    slots = torch.zeros(1, 1, 3, dtype=torch.int32, device=dev())
+    calls = [(x, lambda t: ets.rope(t, i2, freq)), (freq, lambda t: ets.rope(x, i2, t)), (x, lambda t: ets.cache_write(t, i2, kg, ksg)),
+             (q, lambda t: ets.index_scores(t, w, kg, ksg, table, lens, 4, 4)),
+             (w, lambda t: ets.index_scores(q, t, kg, ksg, table, lens, 4, 4)),
+             (q, lambda t: ets.attend_selected(t, kg, ksg, kg, ksg, slots)),
+             (q, lambda t: ets.attend_paged(t, kg, ksg, kg, ksg, table, lens, 4, 4))]
+    outs = [lambda: ets.rope(x, i2, freq, out=torch.zeros_like(x, requires_grad=True)),
+            lambda: ets.index_scores(q, w, kg, ksg, table, lens, 4, 4, out=torch.zeros(1, 4, device=dev(), requires_grad=True)),
+            lambda: ets.cache_read(kg, ksg, i2, out=torch.zeros(2, 1, 64, dtype=BF16, device=dev(), requires_grad=True))]
+    for t, call in calls:
+        call(t)
+        with pytest.raises(ValueError, match="gradient"):
+            call(t.clone().requires_grad_())
+        with torch.no_grad():
+            call(t.clone().requires_grad_())
+        with forward.dual_level():
+            call(t)
+            with pytest.raises(ValueError, match="forward-mode"):
+                call(forward.make_dual(t, torch.ones_like(t)))
+    for call in outs:
+        with pytest.raises(ValueError, match="gradient"):
+            call()
