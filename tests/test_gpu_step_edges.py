@@ -242,3 +242,27 @@ def test_derivatives_are_refused_not_dropped():
     for call in outs:
         with pytest.raises(ValueError, match="gradient"):
             call()
+
+
+@pytest.mark.parametrize("layout,offset,R", [("half", 0, 64), ("interleaved", 8, 48), ("half", 3, 42), ("interleaved", 1, 62)])
+@pytest.mark.parametrize("inverse", [False, True])
+@pytest.mark.parametrize("span", [64, 1 << 20, (1 << 31) - 1])
+def test_rope_coefficients_are_rounded_once(span, inverse, layout, offset, R):
+    """Cosine and sine times the scale within half a step of 32 bits, at positions near and far."""
+    g = gen(28)
+    N, H, D, scale = 500, 2, 64, 1.3
+    x = torch.randn(N, H, D, generator=g)
+    pos = torch.randint(-span, span, (N,), generator=g).to(torch.int32)
+    freq = 10000.0 ** (-torch.arange(0, R, 2, dtype=torch.float64) / R)
+    want, _ = ref.rope(x, pos, freq, layout, offset, scale, inverse)
+    # two coefficients, two products, each off by half a step of its size; the series beneath 2^-36
+    i = torch.arange(R // 2)
+    ia, ib = (offset + 2 * i, offset + 2 * i + 1) if layout == "interleaved" else (offset + i, offset + R // 2 + i)
+    angle = pos.double()[:, None, None] * freq
+    c, s = angle.cos().abs() * scale, angle.sin().abs() * scale
+    a, b = x.double().abs()[..., ia], x.double().abs()[..., ib]
+    bound = torch.zeros_like(want)
+    bound[..., ia], bound[..., ib] = a * c + b * s, b * c + a * s
+    bound = bound * 2 * ref.U32 * (1 + ref.U32) + bound.amax(-1, keepdim=True) * 2.0 ** -36
+    got = ets.rope(x.to(dev()), pos.to(dev()), freq.to(dev()), layout=layout, offset=offset, scale=scale, inverse=inverse)
+    close(got, want, bound, FP32)
