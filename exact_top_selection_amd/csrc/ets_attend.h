@@ -11,10 +11,13 @@ constexpr int kAttendThreads = 256;
 constexpr int kAttendWaves = 4;
 constexpr int kAttendTile = 32;  // keys of a step
 constexpr float kNegInf = -__builtin_inff();
-// How far (log2) the reference that a softmax is taken relative to is put above the score that raises it: the largest
-// probability lies between 2^-24 and 1 from then on, as exact as one of 1, sums of values stay as far from overflow as the
-// values' own sum, and a list raises its reference once or twice.
+// How far (log2) a score may pass the reference that its softmax is taken relative to, before the reference
+// follows: probabilities up to 2^24 are as exact as those up to 1, and a list raises its reference once or twice.
+// They enter the product with the values times 2^-24, so that the sums stay as far from overflow as the values' own.
+// (A reference put 2^24 above the score instead left arguments of the exponential near -24: log-sum-exps of few keys were
+// off by twice as much.)
 constexpr float kSlack = 24.0f;
+constexpr float kDown = 0x1p-24f, kUp = 0x1p24f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
 struct AttendParams {
@@ -151,12 +154,13 @@ __device__ __forceinline__ void clear_odd(void* eight) {  // in LDS
 }
 
 __device__ __forceinline__ float attend_lse(float reference, float sum) {
-  // the sum's exponent first: it may cancel the reference's distance from the largest score
-  const float whole = reference + static_cast<float>(__builtin_amdgcn_frexp_expf(sum));
-  return sum == 0.0f ? kNegInf : (whole + __builtin_amdgcn_logf(__builtin_amdgcn_frexp_mantf(sum))) * kLn2;
+  // the sum's exponent first: it may cancel most of the reference
+  const float whole = reference + static_cast<float>(__builtin_amdgcn_frexp_expf(sum) - 1);
+  return sum == 0.0f ? kNegInf : (whole + __builtin_amdgcn_logf(2.0f * __builtin_amdgcn_frexp_mantf(sum))) * kLn2;
 }
+// What sums of values times kDown are multiplied by.
 __device__ __forceinline__ float attend_inverse(float sum) {
-  return sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+  return sum > 0.0f || sum != sum ? kUp / sum : 0.0f;
 }
 
 inline uint32_t attend_grid(const AttendParams& p) {

@@ -20,9 +20,9 @@ constexpr int attend_per_unit(int np, int mt) { return mt == 1 && np <= 2 ? 3 : 
 
 // One wave goes over its tiles of 32 keys alone, with the softmax's reference
 // and running sum, and the four waves of a workgroup join at the end.  The
-// reference lies up to 2^24 above the largest score so far, and is raised only
-// when one passes it: a step in which none does, and all keys are seen, needs
-// no largest score over the lanes and no rescaling.
+// reference is the largest score so far, raised only when one passes it by
+// more than 2^24: a step in which none does, and all keys are seen, needs no
+// largest score over the lanes and no rescaling.
 //
 // Scores are formed as K Q^T: a lane holds a head (l % 16) and 8 of the 32
 // keys, so a head's statistics are per lane (two row swaps join the four lanes
@@ -239,7 +239,7 @@ __global__ __launch_bounds__(kThreads, attend_per_unit(NP, MT)) void attend_kern
         x[j] = __builtin_fmaf(score[m][j >> 2][j & 3], p.scale_log2, -top[m]);
         high = __builtin_elementwise_maximum(high, x[j]);  // no number (a score of -inf less a reference of -inf) passes no test
       }
-      if (seen_now != ~0u || tile >= main_tiles || !__all(high <= 0.0f)) {
+      if (seen_now != ~0u || tile >= main_tiles || !__all(high <= kSlack)) {
         uint32_t vis = seen_now;
         if (tile >= main_tiles) vis &= static_cast<uint32_t>(tree_bits[m] >> (kTile * (tile - main_tiles) & 63));
         vis >>= 4 * g;  // bits 0..3: keys 4 g + e; bits 16..19: keys 16 + 4 g + e
@@ -250,8 +250,8 @@ __global__ __launch_bounds__(kThreads, attend_per_unit(NP, MT)) void attend_kern
           high = fmaxf(high, x[j]);
         }
         high = rows_max(high);
-        if (__any(high > top[m])) {
-          const float next = high > top[m] ? high + kSlack : top[m];
+        if (__any(high > top[m] + kSlack || top[m] == kNegInf)) {
+          const float next = high > top[m] + kSlack || top[m] == kNegInf ? high : top[m];
           const float fade = __builtin_amdgcn_exp2f(top[m] - (next == kNegInf ? 0.0f : next));
           sum[m] *= fade;
 #pragma unroll
@@ -266,6 +266,7 @@ __global__ __launch_bounds__(kThreads, attend_per_unit(NP, MT)) void attend_kern
       for (int j = 0; j < 8; ++j) {
         x[j] = __builtin_amdgcn_exp2f(x[j]);
         sum[m] += x[j];
+        x[j] *= kDown;
         prob[m][j] = static_cast<__bf16>(x[j]);
         rest[m][j] = static_cast<__bf16>(x[j] - static_cast<float>(prob[m][j]));
       }

@@ -54,8 +54,8 @@ struct WideLds {
 // has one barrier; within it one wave lays out rows while the other multiplies.
 //
 // The softmax is taken relative to a whole-numbered reference that each team
-// puts 2^24 above a score that passes it, and that follows the other team's of
-// the step before.  While no score does and all keys are seen,
+// raises only when a score passes it by more than 2^24, and that follows the
+// other team's of the step before.  While no score does and all keys are seen,
 // a step needs no largest score and no rescaling; where a reference has
 // changed, or the two differ, sums and probabilities are brought together by
 // powers of two, which is exact.  (With 2^8 every second step of 64 rows had
@@ -252,7 +252,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendParams p
 #pragma unroll
         for (int e = 0; e < 4; ++e) y[m][e] = __builtin_fmaf(x[m][e], p.scale_log2, -ref[m]);
         const float high = fmaxf(fmaxf(y[m][0], y[m][1]), fmaxf(y[m][2], y[m][3]));
-        stays = stays && high <= 0.0f && other[m] <= ref[m];
+        stays = stays && high <= kSlack && other[m] <= ref[m];
       }
       if (seen != 0xffffu || at >= spot.main_tiles || !__all(stays)) {
 #pragma unroll
@@ -269,7 +269,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendParams p
           }
           high = rows_max(high);
           float next = fmaxf(ref[m], other[m]);
-          if (high > next) next = ceilf(high) + kSlack;
+          if (high > next + kSlack || next == kNegInf) next = ceilf(high);
           const float fade = ref[m] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(ref[m] - next);
           sum[m] *= fade;
           ref[m] = next;
@@ -283,8 +283,9 @@ __global__ __launch_bounds__(kThreads, 2) void attend_wide_kernel(AttendParams p
         B4 prob, rest;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float z = __builtin_amdgcn_exp2f(y[m][e]);
+          float z = __builtin_amdgcn_exp2f(y[m][e]);
           sum[m] += z;
+          z *= kDown;
           prob[e] = static_cast<__bf16>(z);
           rest[e] = static_cast<__bf16>(z - static_cast<float>(prob[e]));
         }

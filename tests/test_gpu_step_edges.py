@@ -266,3 +266,20 @@ def test_rope_coefficients_are_rounded_once(span, inverse, layout, offset, R):
     bound = bound * 2 * ref.U32 * (1 + ref.U32) + bound.amax(-1, keepdim=True) * 2.0 ** -36
     got = ets.rope(x.to(dev()), pos.to(dev()), freq.to(dev()), layout=layout, offset=offset, scale=scale, inverse=inverse)
     close(got, want, bound, FP32)
+
+
+@pytest.mark.parametrize("shape", [(16, 64, 64), (64, 128, 128), (8, 256, 256), (64, 576, 512), (16, 576, 512), (8, 320, 320)])
+def test_log_sum_exp_of_one_key(shape):
+    """It is the score itself: a product of one channel, its scaling, and the way through the exponential and back."""
+    Hq, D, Dv = shape
+    g, n = gen(29), 200
+    kc, ks, kg, ksg = cache(n, 1, D, g)
+    vc, vs, vg, vsg = (kc[..., :Dv], ks[..., :Dv // 32], kg[..., :Dv], ksg[..., :Dv // 32]) if Dv == 512 else cache(n, 1, Dv, g)
+    q = torch.zeros(n, 1, Hq, D, dtype=BF16)
+    q[..., 7] = (torch.randn(n, 1, Hq, generator=g) * 0.05).to(BF16)
+    slots = torch.arange(n, dtype=torch.int32).view(n, 1, 1)
+    _, lse = ets.attend_selected(q.to(dev()), kg, ksg, vg, vsg, slots.to(dev()))
+    want = q[..., 7].double() * ref.values(kc, ks)[:, :, 7].view(n, 1, 1) / math.sqrt(D)
+    # steps of the score: the scale, the product and two factors of ln 2, with their results; of 1: argument and result of
+    # the exponential (two), the logarithm (two), and two sums
+    assert ((lse.cpu().double() - want).abs() <= (6 * want.abs() + 8) * ref.U32).all()
