@@ -41,10 +41,10 @@ constexpr int attend_per_unit(int np, int mt) { return mt == 1 && np <= 2 ? 3 : 
 // (which saves a quarter of a step's vector instructions) and a row's scale
 // bytes come in one load (64.0 to 58.4 us on the first case below).
 //
-// Measured: 58 us and 5 us of join for 16 sequences of 7 drafted tokens, 1024
+// Measured: 59 us and 5 us of join for 16 sequences of 7 drafted tokens, 1024
 // slots each, 32 heads on 8 of 128 channels, fp16 (265 MB brought for 235 MB of
-// rows, the rest being the lines of the scales: 4.5 TB/s); 23 us and 4 us for
-// one sequence of 32771, 64 heads on 8, bf16 (70 MB: 3.0 TB/s).  Rows of 128
+// rows, the rest being the lines of the scales: 4.5 TB/s); 24 us and 4 us for
+// one sequence of 32771, 64 heads on 8, bf16 (70 MB: 2.9 TB/s).  Rows of 128
 // bytes come at 5.5 to 6.2 TB/s alone.  The bound is memory, less 5 to 8 us
 // until the first rows are there (slots, then rows), which weighs most on the
 // short case.  A wave has one tile under way while it works on another, twelve
@@ -495,8 +495,8 @@ ets_status make_plan(const ets_attend_args* a, Plan* plan) {
   p.G = a->Hq / a->Hkv;
   p.rows = paged ? a->T * p.G : p.G;
   p.units = a->B * a->Hkv * (paged ? 1 : a->T);
-  // 16-row tiles of a workgroup: four leave a wave a SIMD (8 heads of 7 sequences of 10296, 40 rows each: 101 us against
-  // 73), and so do two of 192 channels (14 us against 9.5 for 40 rows of 160 channels)
+  // 16-row tiles of a workgroup: four leave a wave a SIMD (8 heads of 7 sequences of 10296, 40 rows each, probabilities of
+  // one part: 73 us against 64), and so do two of 192 channels (14 us against 9.5 for 40 rows of 160 channels)
   const int most = plan->width == 3 ? 1 : 2;
   plan->mt = 1;
   while (plan->mt < most && 16 * plan->mt < p.rows) plan->mt *= 2;

@@ -63,13 +63,13 @@ struct WideLds {
 //
 // Probabilities are the sum of two bf16 numbers (16 bits), and fp16 queries are
 // so too, exactly (kTwo).  One part of 8 bits took 62 us on the case below in
-// the place of 71, but its results were off by up to 3.4 times their own
+// the place of 70, but its results were off by up to 3.4 times their own
 // rounding to bf16 with few keys, and 1.1 times when divided by the sum of the
 // rounded probabilities.
 //
-// Measured: 71 us for 64 sequences, 128 heads on one latent head of 576
-// channels, 2048 slots each (36.5 GFLOP: 515 TFLOP/s), and 11 us for the join
-// of its two shares.  Of the 71, 8 go by until the first product (queries and
+// Measured: 70 us for 64 sequences, 128 heads on one latent head of 576
+// channels, 2048 slots each (36.5 GFLOP: 520 TFLOP/s), and 11 us for the join
+// of its two shares.  Of the 70, 8 go by until the first product (queries and
 // first rows come at once, 28 MB) and 4 after the last (33 MB of sums).  A step
 // of 32 keys is 100 matrix instructions a SIMD (1600 cycles), and those of one
 // wave leave another wave of their SIMD every second vector slot.

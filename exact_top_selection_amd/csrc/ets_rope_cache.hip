@@ -84,10 +84,11 @@ __device__ __forceinline__ Turn turn_of(double angle) {
 // of a vector's channels come from there as one or two vectors at any address.
 //
 // Measured: 42 us for 16384 x 32 heads of 128 channels in bf16 (268 MB, 6.4
-// TB/s; a copy of 1 GiB reaches 5.2), 6.7 us for the transposed map of 4099 x 9
-// x 96 in fp32 (28 MB), 3 us for a single token (the launch); staged: 43 us for
-// 8344 x 10 x 480 in bf16 from channel 259 on (160 MB; 74 us with partners read
-// one by one).
+// TB/s; a copy of 1 GiB reaches 5.2), 7.2 us for the transposed map of 4099 x 9
+// x 96 in fp32 (28 MB), 3 us for a single token (the launch); staged: 46 us for
+// 8344 x 10 x 480 in bf16, 200 channels from 259 on (160 MB: 3.5 TB/s), bound by
+// vector instructions, which take 87000 of a SIMD's 98000 cycles (choosing each
+// channel's partner, coefficient and sign).
 template <class T, int MODE>
 __global__ __launch_bounds__(kThreads) void rope_kernel(RopeParams p) {
   constexpr int V = Vec<T>::n;
@@ -273,7 +274,7 @@ __device__ __forceinline__ float quad(float x) {
 // take no part in it.
 //
 // Measured: 19 us for 32768 rows of 8 x 128 in fp16 to random slots (102 MB,
-// 5.3 TB/s), as long as a copy takes; 2.6 us for 64 rows of 576 (the launch).
+// 5.3 TB/s), as long as a copy takes; 4 us for 64 rows of 576 (the launch).
 template <class T>
 __global__ __launch_bounds__(kThreads) void cache_write_kernel(CacheParams p) {
   typedef T V8 __attribute__((ext_vector_type(8)));

@@ -64,7 +64,8 @@ extern "C" {
  *              (the same pointer and strides), and must not overlap otherwise.
  *   positions  int32 [N].   inv_freq  double [R / 2], radians a position.
  *   R          even, 0 <= offset, offset + R <= D.
- * Angles are formed and reduced in 64 bits, everything else in 32.
+ * Angles, cosines and sines times scale are formed in 64 bits and rounded to
+ * 32 once; products and sums are 32 bits.
  */
 ets_status ets_rope(const void* x, int64_t x_n, int64_t x_h, void* out, int64_t out_n, int64_t out_h,
                     int64_t N, int32_t H, int32_t D, const int32_t* positions, const double* inv_freq,
@@ -95,7 +96,9 @@ ets_status ets_cache_read(const uint8_t* codes, int64_t codes_s, int64_t codes_h
  * for positions p < min(seq_lens[b], L), minus infinity for the other p < L.
  * key(b, p) is the row of the cache's head 0 at slot page_table[b][p /
  * page_size] * page_size + p % page_size; a slot outside [0, S) scores minus
- * infinity.  Sums are held in 32 bits.
+ * infinity.  Sums are held in 32 bits; products are exact, but with fp16
+ * queries what lies beneath 2^-26 of a key's largest value (2^-33 in rows that
+ * ets_cache_write made) is rounded.
  *   q        [B][T][H][D], bf16 or fp16.   weights  float [B][T][H].
  *   codes    row of slot s at s * codes_s.  D <= ETS_MAX_INDEX_DIM,
  *            H <= ETS_MAX_INDEX_HEADS, B <= 65535, L <= ETS_MAX_LENGTH.
@@ -121,10 +124,12 @@ ets_status ets_index_scores(const void* q, int64_t q_b, int64_t q_t, int64_t q_h
  *     page_table[b][p / page_size] * page_size + p % page_size;
  *   - tree_slots != NULL: also tree_slots[b][j] for each j < T with bit j of
  *     tree_mask[b][t] set.
- * Scores, softmax statistics and output sums are held in 32 bits: sums of p_j
- * v_j with 0 <= p_j <= 1 and the largest p_j at least 2^-24, so that they are
- * finite where the sum of the values is, and lose what lies beneath 2^-100 in
- * values.
+ * Scores (with products as in ets_index_scores), softmax statistics and output
+ * sums are held in 32 bits: sums of p_j v_j with 0 <= p_j <= 1 and the largest
+ * p_j at least 2^-24, so that they are finite where the sum of the values is,
+ * and lose what lies beneath 2^-100 in values.  The p_j of these sums have 16
+ * bits (two bf16 numbers).  A value or key that is NaN reaches the rows that
+ * see it and no others.
  */
 typedef struct ets_attend_args {
   int32_t B, T, Hq, Hkv, D, Dv;
