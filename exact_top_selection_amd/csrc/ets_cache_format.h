@@ -135,12 +135,14 @@ __device__ __forceinline__ float rows_max(float x) {
 template <int NP, bool FULL>
 __device__ __forceinline__ uint32_t row_top(const uint32_t (&w)[RowScales<NP, FULL>::n], const u32v4 (&codes)[NP], int g) {
   typedef RowScales<NP, FULL> R;
-  bool small = false;
+  uint32_t least = ~0u;  // 0: some 16 codes without one of 2
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
     const u32v4 c = codes[i];
-    small = small || (((c[0] | c[1] | c[2] | c[3]) & 0x40404040u) == 0 && R::byte(w, i, g) != 0);
+    const uint32_t any = (c[0] | c[1] | c[2] | c[3]) & 0x40404040u;
+    least = min(least, FULL || R::byte(w, i, g) ? any : ~0u);
   }
+  const bool small = least == 0 && (!FULL || w[0] != 0);
   uint32_t top = 0;
   if (__any(small)) {
     typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));

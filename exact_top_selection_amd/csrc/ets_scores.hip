@@ -53,7 +53,7 @@ struct ScoreParams {
 //
 // Measured: 56 us for 64 sequences of up to 32768 positions, 64 heads of 128
 // channels (218 MB, 3.9 TB/s, 460 TFLOP/s), 47 us for 4 tokens of each of 4
-// sequences of up to 262144, 32 heads in fp16 (129 MB, 590 TFLOP/s; 1.3 of them
+// sequences of up to 262144, 32 heads in fp16 (129 MB, 590 TFLOP/s; 1.5 of them
 // for finding blocks that say nothing of a row's size).  Beyond the
 // last-level cache a further 2^21 keys take 72 us with 1 head as with 64: it
 // is bound by how fast half lines of rows come in (4 TB/s), and with few keys
