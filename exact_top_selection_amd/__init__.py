@@ -15,7 +15,11 @@ Entry points (same names as the C ABI without the ``ets_`` prefix):
 
 The operators around the selection in a sparse decode step (``rope``,
 ``cache_write``, ``cache_read``, ``index_scores``, ``attend_selected``,
-``attend_paged``; C ABI in ``include/ets_decode.h``) are bound in ``_decode.py``.
+``attend_paged``; C ABI in ``include/ets_decode.h``) are bound in ``_decode.py``;
+those of a speculative step over a pool of cache pages (``block_write``,
+``block_keep``, ``attend_blocks``, ``verify_drafts``, ``pages_copy``,
+``pages_extend``, ``pages_free``, ``pages_fork``, ``pages_compact``; C ABI in
+``include/ets_speculate.h``) in ``_speculate.py``.
 
 Each output row holds min(k, n) selected entries in unspecified order followed
 by -1 padding.  Scores are ranked by their order-preserving 32-bit key; among
@@ -34,7 +38,9 @@ __all__ = ["topk_raw", "topk_paged", "topk_ragged", "topk_paged_noalloc", "works
            "floor_launch", "device_limits", "group_cap", "ticket_cap",
            "new_workspace", "workspace_init", "workspace_error", "workspace_error_async",
            "library_path", "MAX_K", "NOALLOC_SCRATCH_BYTES", "ERROR_BITS", "EtsError",
-           "rope", "cache_write", "cache_read", "index_scores", "attend_selected", "attend_paged"]
+           "rope", "cache_write", "cache_read", "index_scores", "attend_selected", "attend_paged",
+           "block_write", "block_keep", "attend_blocks", "verify_drafts",
+           "pages_copy", "pages_extend", "pages_free", "pages_fork", "pages_compact"]
 
 MAX_K = 2048
 NOALLOC_SCRATCH_BYTES = 4 << 20  # ETS_NOALLOC_SCRATCH_BYTES: topk_paged_noalloc's static scratch
@@ -499,3 +505,5 @@ def floor_launch(B: int, max_row_len: int, device: Optional[torch.device] = None
 
 
 from ._decode import attend_paged, attend_selected, cache_read, cache_write, index_scores, rope  # noqa: E402
+from ._speculate import (attend_blocks, block_keep, block_write, pages_compact, pages_copy, pages_extend,  # noqa: E402
+                         pages_fork, pages_free, verify_drafts)

@@ -3,6 +3,8 @@
 #ifndef ETS_ATTEND_H
 #define ETS_ATTEND_H
 
+#include <type_traits>
+
 #include "ets_cache_format.h"
 
 namespace ets {
@@ -36,6 +38,11 @@ struct AttendParams {
   float* part;       // [unit][row group][split][group_rows][Dv] sums
   f32x2* stat;       // [unit][row group][split][group_rows] (reference, sum)
 };
+// ... over a cache whose scales belong to blocks of slots
+struct AttendBlocksParams : AttendParams {
+  const int32_t* first;  // where a sequence's tokens stand, or null
+  FastDiv by_block;
+};
 
 // Where a workgroup stands: its list, its query rows, its share of the keys.
 // Workgroups are dealt out to the 8 XCDs in turn.  Those that read the same
@@ -51,8 +58,11 @@ struct AttendSpot {
   bool paged;
   int n, main_tiles, tiles, first, last;
   uint64_t tree;  // drafted tokens that stand in the list
+  int64_t begin;  // block caches: position of the first token
+  int edge;       // block caches: positions from here on are not seen by all rows
 };
-__device__ __forceinline__ AttendSpot attend_spot(const AttendParams& p) {
+template <class P>
+__device__ __forceinline__ AttendSpot attend_spot(const P& p) {
   const ets_attend_args& a = p.a;
   AttendSpot s;
   s.paged = a.slots == nullptr;
@@ -69,6 +79,18 @@ __device__ __forceinline__ AttendSpot attend_spot(const AttendParams& p) {
   s.t = s.paged ? 0 : static_cast<int>(bt) - s.b * a.T;
   if (!s.live) return s;
   s.n = s.paged ? min(max(a.seq_lens[s.b], 0), a.L) : a.K;
+  if constexpr (std::is_same_v<P, AttendBlocksParams>) {
+    s.begin = 0, s.edge = INT32_MAX;
+    if (p.first) {
+      // the workgroup's tokens, and how far they see
+      s.begin = p.first[s.b];
+      const int t0 = static_cast<int>(div_by(s.row0, p.by_G)), t1 = static_cast<int>(div_by(min(s.row0 + p.group_rows, p.rows) - 1, p.by_G));
+      const int64_t clear = s.begin + (a.tree_mask ? 0 : t0 + 1), reach = s.begin + (a.tree_mask ? a.T : t1 + 1);
+      const int n = s.begin + t0 < s.n ? static_cast<int>(min(static_cast<int64_t>(s.n), max(reach, static_cast<int64_t>(0)))) : 0;
+      s.edge = s.begin + t1 < s.n ? static_cast<int>(max(clear, static_cast<int64_t>(0))) : 0;  // padding sees nothing
+      s.n = n;
+    }
+  }
   s.main_tiles = (s.n + kAttendTile - 1) / kAttendTile;
   s.tiles = s.main_tiles + p.tree_tiles;
   const int per = (s.tiles + p.splits - 1) / p.splits;
