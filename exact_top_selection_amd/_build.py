@@ -10,7 +10,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SOURCES = [os.path.join(PKG, "csrc", name) for name in
            ("ets_topk.hip", "ets_rope_cache.hip", "ets_scores.hip", "ets_attend.hip", "ets_attend_wide.hip",
-            "ets_attend_blocks.hip", "ets_block_cache.hip", "ets_verify.hip", "ets_pages.hip")]
+            "ets_attend_blocks.hip", "ets_attend_rows.hip", "ets_block_cache.hip", "ets_verify.hip", "ets_pages.hip")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libets_topk.so")
 

@@ -42,6 +42,7 @@ struct AttendParams {
 struct AttendBlocksParams : AttendParams {
   const int32_t* first;  // where a sequence's tokens stand, or null
   FastDiv by_block;
+  int dealt;  // the kernel for many rows: 1, lists are dealt out to the XCDs; 2, workgroups are; 0: the other kernel's way
 };
 
 // Where a workgroup stands: its list, its query rows, its share of the keys.
@@ -61,18 +62,38 @@ struct AttendSpot {
   int64_t begin;  // block caches: position of the first token
   int edge;       // block caches: positions from here on are not seen by all rows
 };
+__device__ __forceinline__ uint32_t attend_deal(const AttendParams& p, AttendSpot* s) {
+  const uint32_t y = blockIdx.x >> 3, eight = div_by(y, p.by_inner), in = y - eight * p.by_inner.d;
+  const uint32_t share = eight * 8 + (blockIdx.x & 7), bt = div_by(share, p.by_splits);
+  s->bt = bt;
+  s->split = static_cast<int>(share - bt * p.splits);
+  const int heads = static_cast<int>(div_by(in, p.by_groups));
+  s->hk = heads * p.heads;
+  s->group = static_cast<int>(in) - heads * p.row_groups;
+  return bt;
+}
 template <class P>
 __device__ __forceinline__ AttendSpot attend_spot(const P& p) {
   const ets_attend_args& a = p.a;
   AttendSpot s;
   s.paged = a.slots == nullptr;
-  const uint32_t y = blockIdx.x >> 3, eight = div_by(y, p.by_inner), in = y - eight * p.by_inner.d;
-  const uint32_t share = eight * 8 + (blockIdx.x & 7), bt = div_by(share, p.by_splits);
-  s.bt = bt;
-  s.split = static_cast<int>(share - bt * p.splits);
-  const int heads = static_cast<int>(div_by(in, p.by_groups));
-  s.hk = heads * p.heads;
-  s.group = static_cast<int>(in) - heads * p.row_groups;
+  uint32_t bt;
+  if constexpr (std::is_same_v<P, AttendBlocksParams>) {
+    if (p.dealt) {
+      // all row groups of a list read the same rows, so they follow each other on one XCD where there are lists for all
+      const uint32_t i = p.dealt == 1 ? blockIdx.x >> 3 : blockIdx.x, turn = div_by(i, p.by_groups);
+      const uint32_t list = p.dealt == 1 ? turn * 8 + (blockIdx.x & 7) : turn, share = div_by(list, p.by_heads);
+      bt = div_by(share, p.by_splits);
+      s.bt = bt;
+      s.split = static_cast<int>(share - bt * p.splits);
+      s.hk = static_cast<int>(list - share * a.Hkv);
+      s.group = static_cast<int>(i - turn * p.row_groups);
+    } else {
+      bt = attend_deal(p, &s);
+    }
+  } else {
+    bt = attend_deal(p, &s);
+  }
   s.row0 = s.group * p.group_rows;
   s.live = bt * a.Hkv < static_cast<uint32_t>(p.units);
   s.b = s.paged ? static_cast<int>(bt) : static_cast<int>(div_by(bt, p.by_tokens));

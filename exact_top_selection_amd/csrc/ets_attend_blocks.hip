@@ -8,10 +8,13 @@
 namespace ets {
 namespace {
 
+constexpr int kManyRows = 32;  // the narrow kernel's rows of a workgroup: more would decode each key again
+
 struct BlocksPlan {
   AttendBlocksParams p;
   int width;  // 64-channel steps of the instance: 1 to 4
-  int mt;
+  int mt;     // tiles of 16 query rows of a wave
+  bool many;  // rows for the kernel of ets_attend_rows.hip
   size_t bytes;
 };
 
@@ -47,22 +50,32 @@ ets_status make_plan(const ets_attend_blocks_args* a, BlocksPlan* plan) {
   p.G = a->Hq / a->Hkv;
   p.rows = a->T * p.G;
   p.units = a->B * a->Hkv;
-  const int most = plan->width == 3 ? 1 : 2;
-  plan->mt = 1;
-  while (plan->mt < most && 16 * plan->mt < p.rows) plan->mt *= 2;
-  p.group_rows = 16 * plan->mt;
-  p.row_groups = (p.rows + p.group_rows - 1) / p.group_rows;
+  plan->many = p.rows > kManyRows;
   const int tiles = (a->L + kAttendTile - 1) / kAttendTile;
+  int fits = 1, waves_rows = 1;
+  if (plan->many) {
+    plan->mt = plan->width <= kRowsWide && p.rows > 16 * kRowsThreads / 64 ? 2 : 1;
+    waves_rows = kRowsThreads / 64;
+  } else {
+    const int most = plan->width == 3 ? 1 : 2;
+    plan->mt = 1;
+    while (plan->mt < most && 16 * plan->mt < p.rows) plan->mt *= 2;
+    fits = attend_per_unit(plan->width, plan->mt);
+  }
+  p.group_rows = 16 * plan->mt * waves_rows;
+  p.row_groups = (p.rows + p.group_rows - 1) / p.group_rows;
   const int64_t lists = static_cast<int64_t>(p.units) * p.row_groups;
-  const int fits = attend_per_unit(plan->width, plan->mt);
   const int64_t room = static_cast<int64_t>(cu) * (fits < 2 ? fits : 2);
-  p.heads = tiles * lists <= 8 * room * kAttendWaves ? 1 : a->Hkv % 4 == 0 ? 4 : a->Hkv % 2 == 0 ? 2 : 1;
+  p.heads = plan->many || tiles * lists <= 8 * room * kAttendWaves ? 1 : a->Hkv % 4 == 0 ? 4 : a->Hkv % 2 == 0 ? 2 : 1;
   const int64_t groups = lists / p.heads;
   int64_t splits = (room + groups - 1) / groups;
   if (groups * splits > static_cast<int64_t>(cu) * fits && splits > 1) splits = static_cast<int64_t>(cu) * fits / groups;
-  const int64_t cap = (tiles + kAttendWaves / p.heads - 1) / (kAttendWaves / p.heads);
+  const int64_t cap = plan->many ? (tiles + 3) / 4 : (tiles + kAttendWaves / p.heads - 1) / (kAttendWaves / p.heads);
   splits = splits > cap ? cap : splits;
   p.splits = static_cast<int>(splits < 1 ? 1 : splits);
+  // seven XCDs with one list more than the eighth do no harm where each has many
+  const int64_t dealt = static_cast<int64_t>(p.units) * p.splits;
+  p.dealt = !plan->many ? 0 : dealt % 8 == 0 || dealt >= 64 ? 1 : 2;
   if (lists * (p.splits + 8) > INT32_MAX / 16) return ETS_ERR_INVALID_ARG;
   p.scale_log2 = static_cast<float>(1.4426950408889634074 / __builtin_sqrt(static_cast<double>(a->D)));
   p.by_page = fast_div(a->page_size);
@@ -81,7 +94,7 @@ ets_status make_plan(const ets_attend_blocks_args* a, BlocksPlan* plan) {
   p.by_lanes = fast_div(p.join_lanes);
   p.by_parts = fast_div(a->Dv / 4 / p.join_lanes);
   p.by_unit_rows = fast_div(p.rows);
-  if (p.splits > 1) plan->bytes = static_cast<size_t>(lists) * p.splits * 16 * plan->mt * (a->Dv * 4 + 8);
+  if (p.splits > 1) plan->bytes = static_cast<size_t>(lists) * p.splits * p.group_rows * (a->Dv * 4 + 8);
   return ETS_OK;
 }
 
@@ -109,11 +122,15 @@ void launch_width(const BlocksPlan& plan, hipStream_t s) {
 template <class T>
 void launch_type(const BlocksPlan& plan, hipStream_t s) {
   const AttendBlocksParams& p = plan.p;
-  switch (plan.width) {
-    case 1: launch_width<T, 1>(plan, s); break;
-    case 2: launch_width<T, 2>(plan, s); break;
-    case 3: launch_width<T, 3>(plan, s); break;
-    default: launch_width<T, 4>(plan, s);
+  if (plan.many) {
+    launch_attend_rows(p, plan.width, plan.mt, s);
+  } else {
+    switch (plan.width) {
+      case 1: launch_width<T, 1>(plan, s); break;
+      case 2: launch_width<T, 2>(plan, s); break;
+      case 3: launch_width<T, 3>(plan, s); break;
+      default: launch_width<T, 4>(plan, s);
+    }
   }
   if (p.splits > 1) {
     const int64_t parts = static_cast<int64_t>(p.units) * p.rows * p.by_parts.d;
@@ -147,7 +164,7 @@ ets_status ets_attend_blocks(const ets_attend_blocks_args* args, void* workspace
   if (plan.bytes) {
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15) || workspace_bytes < plan.bytes) return ETS_ERR_WORKSPACE;
     plan.p.part = static_cast<float*>(workspace);
-    const int64_t rows = static_cast<int64_t>(plan.p.units) * plan.p.row_groups * plan.p.splits * 16 * plan.mt;
+    const int64_t rows = static_cast<int64_t>(plan.p.units) * plan.p.row_groups * plan.p.splits * plan.p.group_rows;
     plan.p.stat = reinterpret_cast<f32x2*>(plan.p.part + rows * a.Dv);
   }
   auto s = static_cast<hipStream_t>(stream);

@@ -3,7 +3,7 @@
 #ifndef ETS_ATTEND_NARROW_H
 #define ETS_ATTEND_NARROW_H
 
-#include "ets_attend.h"
+#include "ets_attend_rows.h"
 
 namespace ets {
 
@@ -106,31 +106,12 @@ __global__ __launch_bounds__(kAttendThreads, attend_per_unit(NP, MT)) void atten
       }
       if (!BLOCKS && a.tree_slots) tree_bits[m] = static_cast<uint64_t>(a.tree_mask[b * a.mask_b + t]);
     }
-    if constexpr (BLOCKS) {
-      upto[m] = INT32_MAX;
-      if (p.first) {
-        const bool alive = r < p.rows && spot.begin + t < min(a.seq_lens[b], a.L);
-        const int64_t to = spot.begin + (a.tree_mask ? 0 : t + 1);
-        upto[m] = alive ? static_cast<int>(min(max(to, static_cast<int64_t>(0)), static_cast<int64_t>(INT32_MAX))) : 0;
-        if (a.tree_mask && alive) {
-          tree_bits[m] = static_cast<uint64_t>(a.tree_mask[b * a.mask_b + t]);
-          if (a.T < 64) tree_bits[m] &= (1ull << a.T) - 1;
-        }
-      }
-    }
+    if constexpr (BLOCKS) attend_sight(p, spot, r < p.rows, t, &upto[m], &tree_bits[m]);
   }
   // the keys of a tile, one bit each, that row m sees where rows differ
   const auto seen_by = [&](int m, int tile) -> uint32_t {
     if constexpr (BLOCKS) {
-      const int ahead = upto[m] - tile * kAttendTile;
-      uint32_t vis = ahead >= 32 ? ~0u : ahead > 0 ? (1u << ahead) - 1 : 0;
-      const int64_t to = spot.begin - static_cast<int64_t>(tile) * kAttendTile;
-      if (to >= 0) {
-        vis |= to < 32 ? static_cast<uint32_t>(tree_bits[m] << to) : 0;
-      } else {
-        vis |= to > -64 ? static_cast<uint32_t>(tree_bits[m] >> -to) : 0;
-      }
-      return vis;
+      return attend_seen_by(spot, upto[m], tree_bits[m], tile * kAttendTile);
     } else {
       return static_cast<uint32_t>(tree_bits[m] >> (kAttendTile * (tile - main_tiles) & 63));
     }

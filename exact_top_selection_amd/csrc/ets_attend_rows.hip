@@ -1,0 +1,339 @@
+// ets_attend_rows.hip -- attention of many query rows that share a list of
+// keys over a block cache: pieces of prompts, wide trees, many heads on one
+// head of the cache (gfx950).
+#include "ets_attend_rows.h"
+
+namespace ets {
+namespace {
+
+constexpr int kThreads = kRowsThreads;
+constexpr int kKeys = 64;  // of a step
+// How far (log2) a score may pass its softmax's reference here, and what values are multiplied by for it: 2^-8 leaves
+// values down to 2^-110 their bits where it is part of their scale, which 2^-24 would not.
+constexpr float kRowsSlack = 8.0f;
+constexpr uint32_t kRowsDown = 8;
+constexpr float kToDown = 0x1p-16f;  // to what the other kernels' sums are multiplied by
+
+// Bytes of a key's decoded channels in LDS (16 rows start in different banks),
+// of half a value's, and of a value's (as in the narrow kernel).
+constexpr int key_pitch(int n) { return 128 * n + 16; }
+constexpr int rows_plane(int n) { return 64 * n + (n % 4 ? 0 : 64); }
+constexpr int value_pitch(int n) { return 2 * rows_plane(n) + 16; }
+constexpr int step_bytes(int n) { return kKeys * (key_pitch(n) + value_pitch(n)) + kKeys * 8; }
+
+// Eight waves share a step of 64 keys and values, decoded once into LDS, and
+// take 16 NT query rows each.  A step is brought two steps ahead into
+// registers and decoded one step ahead into the other half of LDS, so one
+// barrier a step is enough.
+//
+// Scores are K Q^T and results V^T P^T, as in the narrow kernel: a lane holds
+// one query row's column, probabilities stay in registers between the
+// products, and the softmax's reference follows the largest score only when
+// one passes it by 2^8.  The 2^-8 that keeps sums of values finite is part of
+// the values' scale.
+template <class T, int N, int NT>
+__global__ __launch_bounds__(kThreads, 1) void attend_rows_kernel(AttendBlocksParams p) {
+  typedef Mat<T> M;
+  typedef typename M::V8 V8;
+  constexpr int kKeyPitch = key_pitch(N), kPlane = rows_plane(N), kPitch = value_pitch(N);
+  constexpr int kPieces = 4 * N;  // 16 channels each, of a key or a value
+  extern __shared__ __align__(16) char lds[];
+  const ets_attend_args& a = p.a;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 15, g = lane >> 4;
+  const AttendSpot spot = attend_spot(p);
+  if (!spot.live) return;
+  const int b = spot.b, hk = spot.hk;
+  const int k0 = spot.first * kAttendTile, k1 = min(spot.last * kAttendTile, spot.n);
+  const int steps = k1 > k0 ? (k1 - k0 + kKeys - 1) / kKeys : 0;
+
+  // queries: lane (row col, g) holds channels 32 i + 8 g .. + 7
+  V8 q[NT][2 * N];
+  uint64_t tree_bits[NT];
+  int upto[NT];
+#pragma unroll
+  for (int m = 0; m < NT; ++m) {
+    const int r = spot.row0 + (wave * NT + m) * 16 + col;
+    int t, h;
+    attend_row(p, spot, hk, r, &t, &h);
+    const char* src = static_cast<const char*>(a.q) + 2 * (b * a.q_b + t * a.q_t + h * a.q_h);
+#pragma unroll
+    for (int i = 0; i < 2 * N; ++i) {
+      q[m][i] = V8{};
+      if (r < p.rows && 32 * i + 8 * g < a.D) q[m][i] = load_any<V8>(src + 64 * i + 16 * g);
+    }
+    attend_sight(p, spot, r < p.rows, t, &upto[m], &tree_bits[m]);
+  }
+
+  // A thread's part of a step: N pieces of 16 codes, keys' before values'; a wave's pieces are of one kind.
+  const uint64_t nothing = reinterpret_cast<uint64_t>(&kNothing[0]);
+  const int32_t* table = a.page_table + b * a.pt_b;
+  auto is_value = [&](int j) { return N % 2 == 0 ? j >= N / 2 : 2 * (wave + 8 * j) >= 8 * N; };
+  auto number = [&](int j) {  // among the pieces of its kind
+    const int i = static_cast<int>(threadIdx.x) + j * kThreads;
+    return is_value(j) ? i - kKeys * kPieces : i;
+  };
+  int32_t asked[N], slot[N];
+  u32v4 code[N];
+  uint32_t byte[N];
+  auto ask = [&](int step) {  // pages of a step's keys, of the last one for those past the end
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int at = min(k0 + step * kKeys + number(j) / kPieces, k1 - 1);
+      asked[j] = table[div_by(static_cast<uint32_t>(at), p.by_page)];
+    }
+  };
+  auto fetch = [&](int step) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int at = k0 + step * kKeys + number(j) / kPieces, piece = number(j) % kPieces;
+      const uint32_t page = div_by(static_cast<uint32_t>(min(at, k1 - 1)), p.by_page);
+      const int64_t s = static_cast<int64_t>(asked[j]) * a.page_size + (at - static_cast<int>(page * p.by_page.d));
+      const bool there = at < k1 && asked[j] >= 0 && s < a.S;
+      slot[j] = there ? static_cast<int32_t>(s) : -1;
+      const uint32_t n = static_cast<uint32_t>(s) & 0x7fffffffu;
+      const bool value = is_value(j);
+      // formed first and chosen then: an expression inside the choice would become a branch
+      const uint64_t row = reinterpret_cast<uint64_t>(value ? a.v_codes + hk * a.v_h : a.k_codes + hk * a.k_h);
+      const uint64_t scales = reinterpret_cast<uint64_t>(value ? a.v_scales + hk * a.vs_h : a.k_scales + hk * a.ks_h);
+      const uint64_t from = row + static_cast<uint64_t>(n) * static_cast<uint32_t>(value ? a.v_s : a.k_s) + 16 * piece;
+      const uint64_t scale = scales + static_cast<uint64_t>(div_by(n, p.by_block)) * static_cast<uint32_t>(value ? a.vs_s : a.ks_s);
+      const bool in = there && 16 * piece < (value ? a.Dv : a.D);
+      code[j] = load_global<u32v4>(in ? from : nothing);
+      byte[j] = load_global<uint8_t>(there ? scale : nothing);
+    }
+  };
+  auto decode = [&](char* to) {
+    char* values = to + kKeys * kKeyPitch;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int key = number(j) / kPieces, piece = number(j) % kPieces;
+      const u32v4 c = code[j];
+      if (is_value(j)) {
+        const float f = __uint_as_float(byte[j] > kRowsDown ? (byte[j] - kRowsDown) << 23 : 0);
+        char* dst = values + key * kPitch + 16 * piece;
+        *reinterpret_cast<bf16x8*>(dst) = codes_bf16(c[0], c[1], f);
+        *reinterpret_cast<bf16x8*>(dst + kPlane) = codes_bf16(c[2], c[3], f);
+      } else {
+        const float f = M::kRowScale ? 1.0f : __uint_as_float(byte[j] << 23);
+        V8* dst = reinterpret_cast<V8*>(to + key * kKeyPitch + 32 * piece);
+        dst[0] = M::keys(c[0], c[1], f);
+        dst[1] = M::keys(c[2], c[3], f);
+        // all lanes of a key say the same
+        reinterpret_cast<float*>(values + kKeys * kPitch)[key] = __uint_as_float(byte[j] << 23);
+        reinterpret_cast<int32_t*>(values + kKeys * kPitch)[kKeys + key] = slot[j];
+      }
+    }
+  };
+
+  f32x4 out[NT][4 * N];
+  float top[NT], sum[NT];
+#pragma unroll
+  for (int m = 0; m < NT; ++m) {
+    top[m] = kNegInf, sum[m] = 0.0f;
+#pragma unroll
+    for (int c = 0; c < 4 * N; ++c) out[m][c] = f32x4{};
+  }
+
+  auto work = [&](const char* from, int at, uint32_t here) {  // 32 keys from position `at` on; here: those that are there
+    const char* values = from + (kKeys - (at - k0 & 32)) * kKeyPitch + (at - k0 & 32) * kPitch;
+    const bool ragged = at + 32 > spot.edge;
+    f32x4 score[NT][2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+#pragma unroll
+      for (int m = 0; m < NT; ++m) score[m][s] = f32x4{};
+#pragma unroll
+      for (int i = 0; i < 2 * N; ++i) {
+        const V8 k = *reinterpret_cast<const V8*>(from + (16 * s + col) * kKeyPitch + 64 * i + 16 * g);
+#pragma unroll
+        for (int m = 0; m < NT; ++m) score[m][s] = M::mma(k, q[m][i], score[m][s]);
+      }
+    }
+    if constexpr (M::kRowScale) {
+      const char* scale = from + (kKeys - (at - k0 & 32)) * kKeyPitch + kKeys * kPitch + 4 * (at - k0 & 32);
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const f32x4 f = *reinterpret_cast<const f32x4*>(scale + 64 * s + 16 * g);
+#pragma unroll
+        for (int m = 0; m < NT; ++m) score[m][s] *= f;
+      }
+    }
+    bf16x8 prob[NT], rest[NT];
+    uint32_t sees[NT];
+#pragma unroll
+    for (int m = 0; m < NT; ++m) {
+      // x: what goes into the exponential.  First as if all keys were seen and the reference stayed.
+      float x[8], high = kNegInf;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        x[j] = __builtin_fmaf(score[m][j >> 2][j & 3], p.scale_log2, -top[m]);
+        high = __builtin_elementwise_maximum(high, x[j]);  // no number passes no test
+      }
+      sees[m] = ~0u;
+      if (here != ~0u || ragged || !__all(high <= kRowsSlack)) {
+        uint32_t vis = here;
+        if (ragged) vis &= attend_seen_by(spot, upto[m], tree_bits[m], at);
+        vis >>= 4 * g;  // bits 0..3: keys 4 g + e; bits 16..19: keys 16 + 4 g + e
+        sees[m] = vis;
+        high = kNegInf;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          x[j] = (vis >> (16 * (j >> 2) + (j & 3))) & 1 ? score[m][j >> 2][j & 3] * p.scale_log2 : kNegInf;
+          high = fmaxf(high, x[j]);
+        }
+        high = rows_max(high);
+        if (__any(high > top[m] + kRowsSlack || top[m] == kNegInf)) {
+          const float next = high > top[m] + kRowsSlack || top[m] == kNegInf ? high : top[m];
+          const float fade = __builtin_amdgcn_exp2f(top[m] - (next == kNegInf ? 0.0f : next));
+          sum[m] *= fade;
+#pragma unroll
+          for (int c = 0; c < 4 * N; ++c) out[m][c] *= fade;
+          top[m] = next;
+        }
+        const float base = top[m] == kNegInf ? 0.0f : top[m];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] -= base;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        x[j] = __builtin_amdgcn_exp2f(x[j]);
+        sum[m] += x[j];
+        prob[m][j] = static_cast<__bf16>(x[j]);
+        rest[m][j] = static_cast<__bf16>(x[j] - static_cast<float>(prob[m][j]));
+      }
+    }
+    const char* src = values + (4 * g + (col >> 2)) * kPitch + kPlane * ((col >> 1) & 1) + 8 * (col & 1);
+    auto value = [&](int c) {
+      typedef __attribute__((address_space(3))) s16x4* Lds4;
+      typedef short s16x8 __attribute__((ext_vector_type(8)));
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds4)(src + 16 * c));
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds4)(src + 16 * kPitch + 16 * c));
+      return __builtin_bit_cast(bf16x8, s16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
+    };
+    if (ragged) {
+      // values that are no numbers reach the rows that see them, and leave the product of the others
+      uint32_t any = 0;
+#pragma unroll
+      for (int c = 0; c < 4 * N; ++c) {
+        const u16x8 bits = __builtin_bit_cast(u16x8, value(c));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) any |= no_number(bits[e]);
+      }
+      if (__any(any != 0)) {
+#pragma unroll
+        for (int c = 0; c < 4 * N; ++c) {
+          const bf16x8 v = value(c), odd = odd_places(v);
+          u16x8 bits = __builtin_bit_cast(u16x8, v);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) bits[e] = no_number(bits[e]) ? 0 : bits[e];
+          const bf16x8 clear = __builtin_bit_cast(bf16x8, bits);
+#pragma unroll
+          for (int m = 0; m < NT; ++m) {
+            out[m][c] = spoilt(out[m][c], odd, seen_places(sees[m]));
+            out[m][c] = Mat<__bf16>::mma(clear, prob[m], out[m][c]);
+            out[m][c] = Mat<__bf16>::mma(clear, rest[m], out[m][c]);
+          }
+        }
+        return;
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < 4 * N; ++c) {
+      const bf16x8 v = value(c);
+#pragma unroll
+      for (int m = 0; m < NT; ++m) {
+        out[m][c] = Mat<__bf16>::mma(v, prob[m], out[m][c]);
+        out[m][c] = Mat<__bf16>::mma(v, rest[m], out[m][c]);
+      }
+    }
+  };
+
+  if (steps > 0) {
+    ask(0);
+    fetch(0);
+    ask(1);
+    decode(lds);
+    fetch(1);
+    ask(2);
+    for (int step = 0; step < steps; ++step) {
+      __syncthreads();  // this step is decoded, and nobody reads the other half any more
+      decode(lds + ((step + 1) & 1) * step_bytes(N));  // past the end: zeros
+      fetch(step + 2);
+      ask(step + 3);
+      const char* from = lds + (step & 1) * step_bytes(N);
+      const int32_t* slots = reinterpret_cast<const int32_t*>(from + kKeys * (kKeyPitch + kPitch)) + kKeys;
+      const uint64_t here = __ballot(slots[lane] >= 0);
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half)
+        work(from + 32 * half * kKeyPitch, k0 + step * kKeys + 32 * half, static_cast<uint32_t>(here >> (32 * half)));
+    }
+  }
+
+#pragma unroll
+  for (int m = 0; m < NT; ++m) {
+    sum[m] = rows_sum(sum[m]);
+    const int in_group = (wave * NT + m) * 16 + col, r = spot.row0 + in_group;
+    if (r >= p.rows) continue;
+    if (p.splits > 1) {
+      const int64_t place = attend_place(p, spot, hk) * p.group_rows + in_group;
+#pragma unroll
+      for (int c = 0; c < 4 * N; ++c) {
+        if (16 * c + 4 * g < a.Dv) store_any(p.part + place * a.Dv + 16 * c + 4 * g, out[m][c] * kToDown);
+      }
+      if (g == 0) p.stat[place] = f32x2{top[m], sum[m]};
+    } else {
+      int t, h;
+      attend_row(p, spot, hk, r, &t, &h);
+      const int64_t place = (static_cast<int64_t>(b) * a.T + t) * a.Hq + h;
+      const float inv = attend_inverse(sum[m]) * kToDown;
+      typedef T V4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+      for (int c = 0; c < 4 * N; ++c) {
+        if (16 * c + 4 * g >= a.Dv) continue;
+        V4 y;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = static_cast<T>(out[m][c][e] * inv);
+        store_any(static_cast<T*>(a.out) + place * a.Dv + 16 * c + 4 * g, y);
+      }
+      if (g == 0) a.lse[place] = attend_lse(top[m], sum[m]);
+    }
+  }
+}
+
+template <class T, int N, int NT>
+void launch(const AttendBlocksParams& p, hipStream_t s) {
+  const int64_t lists = static_cast<int64_t>(p.units) * p.splits;
+  const uint32_t grid = static_cast<uint32_t>((p.dealt == 1 ? (lists + 7) / 8 * 8 : lists) * p.row_groups);
+  hipLaunchKernelGGL((attend_rows_kernel<T, N, NT>), dim3(grid), dim3(kThreads), 2 * step_bytes(N), s, p);
+}
+
+template <class T, int N>
+void launch_tiles(const AttendBlocksParams& p, int tiles, hipStream_t s) {
+  if (tiles == 1) {
+    launch<T, N, 1>(p, s);
+  } else if constexpr (N <= kRowsWide) {
+    launch<T, N, 2>(p, s);
+  }
+}
+
+template <class T>
+void launch_type(const AttendBlocksParams& p, int width, int tiles, hipStream_t s) {
+  switch (width) {
+    case 1: launch_tiles<T, 1>(p, tiles, s); break;
+    case 2: launch_tiles<T, 2>(p, tiles, s); break;
+    case 3: launch_tiles<T, 3>(p, tiles, s); break;
+    default: launch_tiles<T, 4>(p, tiles, s);
+  }
+}
+
+}  // namespace
+
+void launch_attend_rows(const AttendBlocksParams& p, int width, int tiles, hipStream_t s) {
+  if (p.a.dtype == ETS_BF16) {
+    launch_type<__bf16>(p, width, tiles, s);
+  } else {
+    launch_type<_Float16>(p, width, tiles, s);
+  }
+}
+
+}  // namespace ets
