@@ -60,7 +60,7 @@ struct AttendSpot {
   int n, main_tiles, tiles, first, last;
   uint64_t tree;  // drafted tokens that stand in the list
   int64_t begin;  // block caches: position of the first token
-  int edge;       // block caches: positions from here on are not seen by all rows
+  int edge;       // block caches: positions from here on are not seen by all rows (but those of padding, which see none)
 };
 __device__ __forceinline__ uint32_t attend_deal(const AttendParams& p, AttendSpot* s) {
   const uint32_t y = blockIdx.x >> 3, eight = div_by(y, p.by_inner), in = y - eight * p.by_inner.d;
@@ -108,7 +108,7 @@ __device__ __forceinline__ AttendSpot attend_spot(const P& p) {
       const int t0 = static_cast<int>(div_by(s.row0, p.by_G)), t1 = static_cast<int>(div_by(min(s.row0 + p.group_rows, p.rows) - 1, p.by_G));
       const int64_t clear = s.begin + (a.tree_mask ? 0 : t0 + 1), reach = s.begin + (a.tree_mask ? a.T : t1 + 1);
       const int n = s.begin + t0 < s.n ? static_cast<int>(min(static_cast<int64_t>(s.n), max(reach, static_cast<int64_t>(0)))) : 0;
-      s.edge = s.begin + t1 < s.n ? static_cast<int>(max(clear, static_cast<int64_t>(0))) : 0;  // padding sees nothing
+      s.edge = static_cast<int>(min(max(clear, static_cast<int64_t>(0)), static_cast<int64_t>(INT32_MAX)));
       s.n = n;
     }
   }

@@ -381,6 +381,13 @@ __global__ __launch_bounds__(kAttendThreads, attend_per_unit(NP, MT)) void atten
   // join the waves
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
+    if constexpr (BLOCKS) {
+      if (attend_blind(upto[m], tree_bits[m])) {
+        top[m] = kNegInf, sum[m] = 0.0f;
+#pragma unroll
+        for (int c = 0; c < 4 * NV; ++c) out[m][c] = f32x4{};
+      }
+    }
     sum[m] = rows_sum(sum[m]);
     if (g == 0) stats[(wave * MT + m) * 16 + col] = f32x2{top[m], sum[m]};
   }

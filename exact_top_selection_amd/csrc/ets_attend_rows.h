@@ -22,6 +22,9 @@ __device__ __forceinline__ void attend_sight(const AttendBlocksParams& p, const 
   }
 }
 
+// Rows of padding are masked only where other rows are: what they gather before is thrown away at the end.
+__device__ __forceinline__ bool attend_blind(int upto, uint64_t bits) { return upto == 0 && bits == 0; }
+
 // The 32 keys from position `at` on, one bit each, that such a row sees.
 __device__ __forceinline__ uint32_t attend_seen_by(const AttendSpot& spot, int upto, uint64_t bits, int at) {
   const int ahead = upto - at;

@@ -19,7 +19,9 @@ constexpr float kToDown = 0x1p-16f;  // to what the other kernels' sums are mult
 constexpr int key_pitch(int n) { return 128 * n + 16; }
 constexpr int rows_plane(int n) { return 64 * n + (n % 4 ? 0 : 64); }
 constexpr int value_pitch(int n) { return 2 * rows_plane(n) + 16; }
-constexpr int step_bytes(int n) { return kKeys * (key_pitch(n) + value_pitch(n)) + kKeys * 8; }
+constexpr int step_bytes(int n) { return kKeys * (key_pitch(n) + value_pitch(n)); }
+constexpr int kTurn = kThreads;  // keys whose slots and scales are found at a time, one a lane
+constexpr int lds_bytes(int n) { return 2 * step_bytes(n) + 2 * kTurn * 8; }
 
 // Eight waves share a step of 64 keys and values, decoded once into LDS, and
 // take 16 NT query rows each.  A step is brought two steps ahead into
@@ -64,63 +66,76 @@ __global__ __launch_bounds__(kThreads, 1) void attend_rows_kernel(AttendBlocksPa
     attend_sight(p, spot, r < p.rows, t, &upto[m], &tree_bits[m]);
   }
 
-  // A thread's part of a step: N pieces of 16 codes, keys' before values'; a wave's pieces are of one kind.
+  // Slots and scales of kTurn keys at a time, found by a lane each in three turns (page, then slot and scale bytes, then LDS)
+  // and kept for the steps to read: slot, -1 for a key that is not there, and both scales' upper halves as floats.
+  int32_t* slots = reinterpret_cast<int32_t*>(lds + 2 * step_bytes(N));  // [2][kTurn]
+  uint32_t* scales = reinterpret_cast<uint32_t*>(slots + 2 * kTurn);     // [2][kTurn]
   const uint64_t nothing = reinterpret_cast<uint64_t>(&kNothing[0]);
-  const int32_t* table = a.page_table + b * a.pt_b;
-  auto is_value = [&](int j) { return N % 2 == 0 ? j >= N / 2 : 2 * (wave + 8 * j) >= 8 * N; };
-  auto number = [&](int j) {  // among the pieces of its kind
-    const int i = static_cast<int>(threadIdx.x) + j * kThreads;
-    return is_value(j) ? i - kKeys * kPieces : i;
+  int32_t asked = 0, found = -1;
+  uint32_t key_byte = 0, value_byte = 0;
+  auto ask = [&](int turn) {  // past the end: the last key's page
+    const int at = min(k0 + turn * kTurn + static_cast<int>(threadIdx.x), k1 - 1);
+    asked = a.page_table[b * a.pt_b + div_by(static_cast<uint32_t>(at), p.by_page)];
   };
-  int32_t asked[N], slot[N];
+  auto find = [&](int turn) {
+    const int at = k0 + turn * kTurn + static_cast<int>(threadIdx.x);
+    const uint32_t page = div_by(static_cast<uint32_t>(min(at, k1 - 1)), p.by_page);
+    const int64_t slot = static_cast<int64_t>(asked) * a.page_size + (at - static_cast<int>(page * p.by_page.d));
+    const bool there = at < k1 && asked >= 0 && slot < a.S;
+    const uint64_t block = div_by(static_cast<uint32_t>(slot) & 0x7fffffffu, p.by_block);
+    const uint64_t k = reinterpret_cast<uint64_t>(a.k_scales + hk * a.ks_h) + block * static_cast<uint32_t>(a.ks_s);
+    const uint64_t v = reinterpret_cast<uint64_t>(a.v_scales + hk * a.vs_h) + block * static_cast<uint32_t>(a.vs_s);
+    found = there ? static_cast<int32_t>(slot) : -1;
+    key_byte = load_global<uint8_t>(there ? k : nothing);
+    value_byte = load_global<uint8_t>(there ? v : nothing);
+  };
+  auto keep = [&](int turn) {
+    const int to = (turn & 1) * kTurn + static_cast<int>(threadIdx.x);
+    slots[to] = found;
+    scales[to] = key_byte << 23 | (value_byte > kRowsDown ? (value_byte - kRowsDown) << 7 : 0);
+  };
+
+  // A thread's part of a step: N pieces of 16 codes, keys' before values'; a wave's pieces are of one kind.
+  uint64_t row[N];
+  uint32_t stride[N];
+  bool is_value[N];
+  int key[N], piece[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    is_value[j] = N % 2 == 0 ? j >= N / 2 : wave + 8 * j >= 4 * N;
+    const int i = static_cast<int>(threadIdx.x) + j * kThreads - (is_value[j] ? kKeys * kPieces : 0);
+    key[j] = i / kPieces, piece[j] = i % kPieces;
+    row[j] = reinterpret_cast<uint64_t>(is_value[j] ? a.v_codes + hk * a.v_h : a.k_codes + hk * a.k_h) + 16 * piece[j];
+    stride[j] = static_cast<uint32_t>(is_value[j] ? a.v_s : a.k_s);
+    if (16 * piece[j] >= (is_value[j] ? a.Dv : a.D)) row[j] = nothing, stride[j] = 0;  // channels that are not there
+  }
   u32v4 code[N];
-  uint32_t byte[N];
-  auto ask = [&](int step) {  // pages of a step's keys, of the last one for those past the end
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const int at = min(k0 + step * kKeys + number(j) / kPieces, k1 - 1);
-      asked[j] = table[div_by(static_cast<uint32_t>(at), p.by_page)];
-    }
-  };
+  uint32_t scale[N];
   auto fetch = [&](int step) {
+    const int from = (step * kKeys) & (2 * kTurn - 1);
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      const int at = k0 + step * kKeys + number(j) / kPieces, piece = number(j) % kPieces;
-      const uint32_t page = div_by(static_cast<uint32_t>(min(at, k1 - 1)), p.by_page);
-      const int64_t s = static_cast<int64_t>(asked[j]) * a.page_size + (at - static_cast<int>(page * p.by_page.d));
-      const bool there = at < k1 && asked[j] >= 0 && s < a.S;
-      slot[j] = there ? static_cast<int32_t>(s) : -1;
-      const uint32_t n = static_cast<uint32_t>(s) & 0x7fffffffu;
-      const bool value = is_value(j);
-      // formed first and chosen then: an expression inside the choice would become a branch
-      const uint64_t row = reinterpret_cast<uint64_t>(value ? a.v_codes + hk * a.v_h : a.k_codes + hk * a.k_h);
-      const uint64_t scales = reinterpret_cast<uint64_t>(value ? a.v_scales + hk * a.vs_h : a.k_scales + hk * a.ks_h);
-      const uint64_t from = row + static_cast<uint64_t>(n) * static_cast<uint32_t>(value ? a.v_s : a.k_s) + 16 * piece;
-      const uint64_t scale = scales + static_cast<uint64_t>(div_by(n, p.by_block)) * static_cast<uint32_t>(value ? a.vs_s : a.ks_s);
-      const bool in = there && 16 * piece < (value ? a.Dv : a.D);
-      code[j] = load_global<u32v4>(in ? from : nothing);
-      byte[j] = load_global<uint8_t>(there ? scale : nothing);
+      const int32_t slot = slots[from + key[j]];
+      scale[j] = scales[from + key[j]];
+      const uint64_t at = row[j] + static_cast<uint64_t>(static_cast<uint32_t>(slot)) * stride[j];
+      code[j] = load_global<u32v4>(slot >= 0 ? at : nothing);
     }
   };
   auto decode = [&](char* to) {
     char* values = to + kKeys * kKeyPitch;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      const int key = number(j) / kPieces, piece = number(j) % kPieces;
       const u32v4 c = code[j];
-      if (is_value(j)) {
-        const float f = __uint_as_float(byte[j] > kRowsDown ? (byte[j] - kRowsDown) << 23 : 0);
-        char* dst = values + key * kPitch + 16 * piece;
+      if (is_value[j]) {
+        const float f = __uint_as_float(scale[j] << 16);
+        char* dst = values + key[j] * kPitch + 16 * piece[j];
         *reinterpret_cast<bf16x8*>(dst) = codes_bf16(c[0], c[1], f);
         *reinterpret_cast<bf16x8*>(dst + kPlane) = codes_bf16(c[2], c[3], f);
       } else {
-        const float f = M::kRowScale ? 1.0f : __uint_as_float(byte[j] << 23);
-        V8* dst = reinterpret_cast<V8*>(to + key * kKeyPitch + 32 * piece);
+        const float f = M::kRowScale ? 1.0f : __uint_as_float(scale[j] & 0xffff0000u);
+        V8* dst = reinterpret_cast<V8*>(to + key[j] * kKeyPitch + 32 * piece[j]);
         dst[0] = M::keys(c[0], c[1], f);
         dst[1] = M::keys(c[2], c[3], f);
-        // all lanes of a key say the same
-        reinterpret_cast<float*>(values + kKeys * kPitch)[key] = __uint_as_float(byte[j] << 23);
-        reinterpret_cast<int32_t*>(values + kKeys * kPitch)[kKeys + key] = slot[j];
       }
     }
   };
@@ -134,32 +149,34 @@ __global__ __launch_bounds__(kThreads, 1) void attend_rows_kernel(AttendBlocksPa
     for (int c = 0; c < 4 * N; ++c) out[m][c] = f32x4{};
   }
 
-  auto work = [&](const char* from, int at, uint32_t here) {  // 32 keys from position `at` on; here: those that are there
-    const char* values = from + (kKeys - (at - k0 & 32)) * kKeyPitch + (at - k0 & 32) * kPitch;
+  // 32 keys from position `at` on: keys and values in LDS, which of them are there, their scales
+  auto work = [&](const char* keys, char* values, int at, uint32_t here, const uint32_t* key_scale) {
     const bool ragged = at + 32 > spot.edge;
     f32x4 score[NT][2];
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < 2; ++s)
 #pragma unroll
       for (int m = 0; m < NT; ++m) score[m][s] = f32x4{};
 #pragma unroll
-      for (int i = 0; i < 2 * N; ++i) {
-        const V8 k = *reinterpret_cast<const V8*>(from + (16 * s + col) * kKeyPitch + 64 * i + 16 * g);
+    for (int i = 0; i < 2 * N; ++i) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const V8 k = *reinterpret_cast<const V8*>(keys + (16 * s + col) * kKeyPitch + 64 * i + 16 * g);
 #pragma unroll
         for (int m = 0; m < NT; ++m) score[m][s] = M::mma(k, q[m][i], score[m][s]);
       }
     }
     if constexpr (M::kRowScale) {
-      const char* scale = from + (kKeys - (at - k0 & 32)) * kKeyPitch + kKeys * kPitch + 4 * (at - k0 & 32);
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        const f32x4 f = *reinterpret_cast<const f32x4*>(scale + 64 * s + 16 * g);
+        const u32v4 f = *reinterpret_cast<const u32v4*>(key_scale + 16 * s + 4 * g);
 #pragma unroll
-        for (int m = 0; m < NT; ++m) score[m][s] *= f;
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int m = 0; m < NT; ++m) score[m][s][e] *= __uint_as_float(f[e] & 0xffff0000u);
       }
     }
     bf16x8 prob[NT], rest[NT];
-    uint32_t sees[NT];
 #pragma unroll
     for (int m = 0; m < NT; ++m) {
       // x: what goes into the exponential.  First as if all keys were seen and the reference stayed.
@@ -169,12 +186,10 @@ __global__ __launch_bounds__(kThreads, 1) void attend_rows_kernel(AttendBlocksPa
         x[j] = __builtin_fmaf(score[m][j >> 2][j & 3], p.scale_log2, -top[m]);
         high = __builtin_elementwise_maximum(high, x[j]);  // no number passes no test
       }
-      sees[m] = ~0u;
       if (here != ~0u || ragged || !__all(high <= kRowsSlack)) {
         uint32_t vis = here;
         if (ragged) vis &= attend_seen_by(spot, upto[m], tree_bits[m], at);
         vis >>= 4 * g;  // bits 0..3: keys 4 g + e; bits 16..19: keys 16 + 4 g + e
-        sees[m] = vis;
         high = kNegInf;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -194,13 +209,18 @@ __global__ __launch_bounds__(kThreads, 1) void attend_rows_kernel(AttendBlocksPa
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] -= base;
       }
+      u32v4 first, second;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        x[j] = __builtin_amdgcn_exp2f(x[j]);
-        sum[m] += x[j];
-        prob[m][j] = static_cast<__bf16>(x[j]);
-        rest[m][j] = static_cast<__bf16>(x[j] - static_cast<float>(prob[m][j]));
+      for (int j = 0; j < 4; ++j) {
+        const float y = __builtin_amdgcn_exp2f(x[2 * j]), z = __builtin_amdgcn_exp2f(x[2 * j + 1]);
+        sum[m] += y;
+        sum[m] += z;
+        first[j] = __builtin_bit_cast(uint32_t, bf16x2{static_cast<__bf16>(y), static_cast<__bf16>(z)});
+        second[j] = __builtin_bit_cast(uint32_t, bf16x2{static_cast<__bf16>(y - __uint_as_float(first[j] << 16)),
+                                                        static_cast<__bf16>(z - __uint_as_float(first[j] & 0xffff0000u))});
       }
+      prob[m] = __builtin_bit_cast(bf16x8, first);
+      rest[m] = __builtin_bit_cast(bf16x8, second);
     }
     const char* src = values + (4 * g + (col >> 2)) * kPitch + kPlane * ((col >> 1) & 1) + 8 * (col & 1);
     auto value = [&](int c) {
@@ -211,7 +231,7 @@ __global__ __launch_bounds__(kThreads, 1) void attend_rows_kernel(AttendBlocksPa
       return __builtin_bit_cast(bf16x8, s16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
     };
     if (ragged) {
-      // values that are no numbers reach the rows that see them, and leave the product of the others
+      // values that are no numbers: every wave sees the same ones, so all of them come to these barriers or none
       uint32_t any = 0;
 #pragma unroll
       for (int c = 0; c < 4 * N; ++c) {
@@ -221,56 +241,73 @@ __global__ __launch_bounds__(kThreads, 1) void attend_rows_kernel(AttendBlocksPa
       }
       if (__any(any != 0)) {
 #pragma unroll
-        for (int c = 0; c < 4 * N; ++c) {
-          const bf16x8 v = value(c), odd = odd_places(v);
-          u16x8 bits = __builtin_bit_cast(u16x8, v);
+        for (int m = 0; m < NT; ++m) {
+          const bf16x8 sees = seen_places((here & attend_seen_by(spot, upto[m], tree_bits[m], at)) >> (4 * g));
 #pragma unroll
-          for (int e = 0; e < 8; ++e) bits[e] = no_number(bits[e]) ? 0 : bits[e];
-          const bf16x8 clear = __builtin_bit_cast(bf16x8, bits);
-#pragma unroll
-          for (int m = 0; m < NT; ++m) {
-            out[m][c] = spoilt(out[m][c], odd, seen_places(sees[m]));
-            out[m][c] = Mat<__bf16>::mma(clear, prob[m], out[m][c]);
-            out[m][c] = Mat<__bf16>::mma(clear, rest[m], out[m][c]);
-          }
+          for (int c = 0; c < 4 * N; ++c) out[m][c] = spoilt(out[m][c], odd_places(value(c)), sees);
         }
-        return;
+        __syncthreads();
+        for (int i = threadIdx.x; i < 32 * 8 * N; i += kThreads) {
+          const int r = i / (8 * N), eight = i % (8 * N);
+          clear_odd(values + r * kPitch + (eight & 1) * kPlane + 16 * (eight >> 1));
+        }
+        __syncthreads();
       }
     }
 #pragma unroll
-    for (int c = 0; c < 4 * N; ++c) {
-      const bf16x8 v = value(c);
+    for (int c = 0; c < 4 * N; c += 2) {
+      const bf16x8 v = value(c), w = value(c + 1);
 #pragma unroll
       for (int m = 0; m < NT; ++m) {
         out[m][c] = Mat<__bf16>::mma(v, prob[m], out[m][c]);
+        out[m][c + 1] = Mat<__bf16>::mma(w, prob[m], out[m][c + 1]);
+      }
+#pragma unroll
+      for (int m = 0; m < NT; ++m) {
         out[m][c] = Mat<__bf16>::mma(v, rest[m], out[m][c]);
+        out[m][c + 1] = Mat<__bf16>::mma(w, rest[m], out[m][c + 1]);
       }
     }
   };
 
   if (steps > 0) {
     ask(0);
-    fetch(0);
+    find(0);
     ask(1);
+    keep(0);
+    find(1);
+    ask(2);
+    __syncthreads();
+    fetch(0);
     decode(lds);
     fetch(1);
-    ask(2);
     for (int step = 0; step < steps; ++step) {
       __syncthreads();  // this step is decoded, and nobody reads the other half any more
+      const int turn = step / (kTurn / kKeys);
+      if (step % (kTurn / kKeys) == 0) {  // the last turn's half of the slots is read no more
+        keep(turn + 1);
+        find(turn + 2);
+        ask(turn + 3);
+      }
       decode(lds + ((step + 1) & 1) * step_bytes(N));  // past the end: zeros
-      fetch(step + 2);
-      ask(step + 3);
-      const char* from = lds + (step & 1) * step_bytes(N);
-      const int32_t* slots = reinterpret_cast<const int32_t*>(from + kKeys * (kKeyPitch + kPitch)) + kKeys;
-      const uint64_t here = __ballot(slots[lane] >= 0);
+      fetch(step + 2);  // its slots were kept at least two barriers ago
+      char* from = lds + (step & 1) * step_bytes(N);
+      const int in = (step * kKeys) & (2 * kTurn - 1);
+      const uint64_t here = __ballot(slots[in + lane] >= 0);
 #pragma unroll 1
       for (int half = 0; half < 2; ++half)
-        work(from + 32 * half * kKeyPitch, k0 + step * kKeys + 32 * half, static_cast<uint32_t>(here >> (32 * half)));
+        work(from + 32 * half * kKeyPitch, from + kKeys * kKeyPitch + 32 * half * kPitch, k0 + step * kKeys + 32 * half,
+             static_cast<uint32_t>(here >> (32 * half)), scales + in + 32 * half);
     }
   }
 
 #pragma unroll
   for (int m = 0; m < NT; ++m) {
+    if (attend_blind(upto[m], tree_bits[m])) {
+      top[m] = kNegInf, sum[m] = 0.0f;
+#pragma unroll
+      for (int c = 0; c < 4 * N; ++c) out[m][c] = f32x4{};
+    }
     sum[m] = rows_sum(sum[m]);
     const int in_group = (wave * NT + m) * 16 + col, r = spot.row0 + in_group;
     if (r >= p.rows) continue;
@@ -304,7 +341,7 @@ template <class T, int N, int NT>
 void launch(const AttendBlocksParams& p, hipStream_t s) {
   const int64_t lists = static_cast<int64_t>(p.units) * p.splits;
   const uint32_t grid = static_cast<uint32_t>((p.dealt == 1 ? (lists + 7) / 8 * 8 : lists) * p.row_groups);
-  hipLaunchKernelGGL((attend_rows_kernel<T, N, NT>), dim3(grid), dim3(kThreads), 2 * step_bytes(N), s, p);
+  hipLaunchKernelGGL((attend_rows_kernel<T, N, NT>), dim3(grid), dim3(kThreads), lds_bytes(N), s, p);
 }
 
 template <class T, int N>
