@@ -42,7 +42,7 @@ struct AttendParams {
 struct AttendBlocksParams : AttendParams {
   const int32_t* first;  // where a sequence's tokens stand, or null
   FastDiv by_block;
-  int dealt;  // the kernel for many rows: 1, lists are dealt out to the XCDs; 2, workgroups are; 0: the other kernel's way
+  int dealt;  // to the XCDs: 0, shares with all their heads; 1, lists; 2, workgroups
 };
 
 // Where a workgroup stands: its list, its query rows, its share of the keys.
@@ -79,7 +79,7 @@ __device__ __forceinline__ AttendSpot attend_spot(const P& p) {
   s.paged = a.slots == nullptr;
   uint32_t bt;
   if constexpr (std::is_same_v<P, AttendBlocksParams>) {
-    if (p.dealt) {
+    if (p.dealt == 1 || p.dealt == 2) {
       // all row groups of a list read the same rows, so they follow each other on one XCD where there are lists for all
       const uint32_t i = p.dealt == 1 ? blockIdx.x >> 3 : blockIdx.x, turn = div_by(i, p.by_groups);
       const uint32_t list = p.dealt == 1 ? turn * 8 + (blockIdx.x & 7) : turn, share = div_by(list, p.by_heads);

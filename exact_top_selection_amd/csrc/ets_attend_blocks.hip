@@ -15,6 +15,7 @@ struct BlocksPlan {
   int width;  // 64-channel steps of the instance: 1 to 4
   int mt;     // tiles of 16 query rows of a wave
   bool many;  // rows for the kernel of ets_attend_rows.hip
+  RowsShape shape;
   size_t bytes;
 };
 
@@ -54,8 +55,14 @@ ets_status make_plan(const ets_attend_blocks_args* a, BlocksPlan* plan) {
   const int tiles = (a->L + kAttendTile - 1) / kAttendTile;
   int fits = 1, waves_rows = 1;
   if (plan->many) {
-    plan->mt = plan->width <= kRowsWide && p.rows > 16 * kRowsThreads / 64 ? 2 : 1;
-    waves_rows = kRowsThreads / 64;
+    // Two workgroups of four waves share a compute unit, and one works while the other waits at its barrier.  Eight waves
+    // decode each key for twice the rows, which pays where there are workgroups for several turns of the device (8
+    // sequences of 8192, 1024 tokens each: 1412 us against 1598; 2 of them of uneven length: 373 against 340).
+    const int64_t wide = static_cast<int64_t>(p.units) * ((p.rows + 255) / 256);
+    plan->shape = {plan->width, plan->width <= 2 && wide >= 2 * cu ? 8 : 4, p.rows > 64 || plan->width > 2 ? 2 : 1};
+    plan->mt = plan->shape.tiles;
+    waves_rows = plan->shape.waves;
+    fits = rows_per_unit(plan->width, waves_rows);
   } else {
     const int most = plan->width == 3 ? 1 : 2;
     plan->mt = 1;
@@ -73,9 +80,10 @@ ets_status make_plan(const ets_attend_blocks_args* a, BlocksPlan* plan) {
   const int64_t cap = plan->many ? (tiles + 3) / 4 : (tiles + kAttendWaves / p.heads - 1) / (kAttendWaves / p.heads);
   splits = splits > cap ? cap : splits;
   p.splits = static_cast<int>(splits < 1 ? 1 : splits);
-  // seven XCDs with one list more than the eighth do no harm where each has many
-  const int64_t dealt = static_cast<int64_t>(p.units) * p.splits;
-  p.dealt = !plan->many ? 0 : dealt % 8 == 0 || dealt >= 64 ? 1 : 2;
+  // Heads of a slot lie side by side in memory, so they are read on one XCD where there are shares for all 8 (seven with
+  // one more than the eighth do no harm where each has many).
+  const int64_t shares = static_cast<int64_t>(a->B) * p.splits, all = shares * a->Hkv;
+  p.dealt = !plan->many || shares % 8 == 0 || shares >= 64 ? 0 : all % 8 == 0 || all >= 64 ? 1 : 2;
   if (lists * (p.splits + 8) > INT32_MAX / 16) return ETS_ERR_INVALID_ARG;
   p.scale_log2 = static_cast<float>(1.4426950408889634074 / __builtin_sqrt(static_cast<double>(a->D)));
   p.by_page = fast_div(a->page_size);
@@ -123,7 +131,7 @@ template <class T>
 void launch_type(const BlocksPlan& plan, hipStream_t s) {
   const AttendBlocksParams& p = plan.p;
   if (plan.many) {
-    launch_attend_rows(p, plan.width, plan.mt, s);
+    launch_attend_rows(p, plan.shape, s);
   } else {
     switch (plan.width) {
       case 1: launch_width<T, 1>(plan, s); break;

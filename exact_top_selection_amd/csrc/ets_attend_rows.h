@@ -38,11 +38,15 @@ __device__ __forceinline__ uint32_t attend_seen_by(const AttendSpot& spot, int u
   return vis;
 }
 
-constexpr int kRowsThreads = 512;
-constexpr int kRowsWide = 2;  // 64-channel steps up to which a wave takes two tiles of query rows
+// What the kernel for many rows (ets_attend_rows.hip) takes of them: a workgroup's waves, a wave's tiles of 16.
+struct RowsShape {
+  int width;  // 64-channel steps: 1 to 4
+  int waves, tiles;
+};
+// Workgroups of a compute unit, by LDS and registers.
+constexpr int rows_per_unit(int width, int waves) { return waves == 4 && width <= 2 ? 2 : 1; }
 
-// The launch of the kernel for many rows (ets_attend_rows.hip); width: 64-channel steps, tiles: of 16 query rows of a wave.
-void launch_attend_rows(const AttendBlocksParams& p, int width, int tiles, hipStream_t s);
+void launch_attend_rows(const AttendBlocksParams& p, const RowsShape& r, hipStream_t s);
 
 }  // namespace ets
 

@@ -6,13 +6,12 @@
 namespace ets {
 namespace {
 
-constexpr int kThreads = kRowsThreads;
 constexpr int kKeys = 64;  // of a step
-// How far (log2) a score may pass its softmax's reference here, and what values are multiplied by for it: 2^-8 leaves
-// values down to 2^-110 their bits where it is part of their scale, which 2^-24 would not.
-constexpr float kRowsSlack = 8.0f;
-constexpr uint32_t kRowsDown = 8;
-constexpr float kToDown = 0x1p-16f;  // to what the other kernels' sums are multiplied by
+// How far (log2) a score may pass its softmax's reference here, and what values are multiplied by for it.  As part of a
+// block's scale 2^-18 takes the bits of values under 448 * 2^(18 - 127) < 2^-100 only, which 2^-24 would not.
+constexpr float kRowsSlack = 18.0f;
+constexpr uint32_t kRowsDown = 18;
+constexpr float kToDown = 0x1p-6f;  // to what the other kernels' sums are multiplied by
 
 // Bytes of a key's decoded channels in LDS (16 rows start in different banks),
 // of half a value's, and of a value's (as in the narrow kernel).
@@ -20,8 +19,7 @@ constexpr int key_pitch(int n) { return 128 * n + 16; }
 constexpr int rows_plane(int n) { return 64 * n + (n % 4 ? 0 : 64); }
 constexpr int value_pitch(int n) { return 2 * rows_plane(n) + 16; }
 constexpr int step_bytes(int n) { return kKeys * (key_pitch(n) + value_pitch(n)); }
-constexpr int kTurn = kThreads;  // keys whose slots and scales are found at a time, one a lane
-constexpr int lds_bytes(int n) { return 2 * step_bytes(n) + 2 * kTurn * 8; }
+constexpr int lds_bytes(int n, int waves) { return 2 * step_bytes(n) + 2 * 64 * waves * 8; }
 
 // Eight waves share a step of 64 keys and values, decoded once into LDS, and
 // take 16 NT query rows each.  A step is brought two steps ahead into
@@ -31,14 +29,18 @@ constexpr int lds_bytes(int n) { return 2 * step_bytes(n) + 2 * kTurn * 8; }
 // Scores are K Q^T and results V^T P^T, as in the narrow kernel: a lane holds
 // one query row's column, probabilities stay in registers between the
 // products, and the softmax's reference follows the largest score only when
-// one passes it by 2^8.  The 2^-8 that keeps sums of values finite is part of
+// one passes it by 2^18.  The 2^-18 that keeps sums of values finite is part of
 // the values' scale.
-template <class T, int N, int NT>
-__global__ __launch_bounds__(kThreads, 1) void attend_rows_kernel(AttendBlocksParams p) {
+// KB: 32-key parts of a step that a wave has in its registers at once.
+template <class T, int N, int NT, int KB, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, rows_per_unit(N, WAVES)) void attend_rows_kernel(AttendBlocksParams p) {
   typedef Mat<T> M;
   typedef typename M::V8 V8;
   constexpr int kKeyPitch = key_pitch(N), kPlane = rows_plane(N), kPitch = value_pitch(N);
-  constexpr int kPieces = 4 * N;  // 16 channels each, of a key or a value
+  constexpr int kThreads = 64 * WAVES;
+  constexpr int kTurn = kThreads;           // keys whose slots and scales are found at a time, one a lane
+  constexpr int kPieces = 4 * N;            // 16 channels each, of a key or a value
+  constexpr int kItems = 2 * kPieces / WAVES;  // pieces of a step that a thread brings
   extern __shared__ __align__(16) char lds[];
   const ets_attend_args& a = p.a;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 15, g = lane >> 4;
@@ -95,26 +97,26 @@ __global__ __launch_bounds__(kThreads, 1) void attend_rows_kernel(AttendBlocksPa
     scales[to] = key_byte << 23 | (value_byte > kRowsDown ? (value_byte - kRowsDown) << 7 : 0);
   };
 
-  // A thread's part of a step: N pieces of 16 codes, keys' before values'; a wave's pieces are of one kind.
-  uint64_t row[N];
-  uint32_t stride[N];
-  bool is_value[N];
-  int key[N], piece[N];
+  // A thread's part of a step: pieces of 16 codes, keys' before values'; a wave's pieces are of one kind.
+  uint64_t row[kItems];
+  uint32_t stride[kItems];
+  bool is_value[kItems];
+  int key[kItems], piece[kItems];
 #pragma unroll
-  for (int j = 0; j < N; ++j) {
-    is_value[j] = N % 2 == 0 ? j >= N / 2 : wave + 8 * j >= 4 * N;
+  for (int j = 0; j < kItems; ++j) {
+    is_value[j] = kItems % 2 == 0 ? j >= kItems / 2 : wave + WAVES * j >= kPieces;
     const int i = static_cast<int>(threadIdx.x) + j * kThreads - (is_value[j] ? kKeys * kPieces : 0);
     key[j] = i / kPieces, piece[j] = i % kPieces;
     row[j] = reinterpret_cast<uint64_t>(is_value[j] ? a.v_codes + hk * a.v_h : a.k_codes + hk * a.k_h) + 16 * piece[j];
     stride[j] = static_cast<uint32_t>(is_value[j] ? a.v_s : a.k_s);
     if (16 * piece[j] >= (is_value[j] ? a.Dv : a.D)) row[j] = nothing, stride[j] = 0;  // channels that are not there
   }
-  u32v4 code[N];
-  uint32_t scale[N];
+  u32v4 code[kItems];
+  uint32_t scale[kItems];
   auto fetch = [&](int step) {
     const int from = (step * kKeys) & (2 * kTurn - 1);
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
+    for (int j = 0; j < kItems; ++j) {
       const int32_t slot = slots[from + key[j]];
       scale[j] = scales[from + key[j]];
       const uint64_t at = row[j] + static_cast<uint64_t>(static_cast<uint32_t>(slot)) * stride[j];
@@ -124,7 +126,7 @@ __global__ __launch_bounds__(kThreads, 1) void attend_rows_kernel(AttendBlocksPa
   auto decode = [&](char* to) {
     char* values = to + kKeys * kKeyPitch;
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
+    for (int j = 0; j < kItems; ++j) {
       const u32v4 c = code[j];
       if (is_value[j]) {
         const float f = __uint_as_float(scale[j] << 16);
@@ -149,18 +151,19 @@ __global__ __launch_bounds__(kThreads, 1) void attend_rows_kernel(AttendBlocksPa
     for (int c = 0; c < 4 * N; ++c) out[m][c] = f32x4{};
   }
 
-  // 32 keys from position `at` on: keys and values in LDS, which of them are there, their scales
-  auto work = [&](const char* keys, char* values, int at, uint32_t here, const uint32_t* key_scale) {
-    const bool ragged = at + 32 > spot.edge;
-    f32x4 score[NT][2];
+  // 32 KB keys from position `at` on: keys and values in LDS, which of them are there, their scales
+  auto work = [&](const char* keys, char* values, int at, uint64_t here, const uint32_t* key_scale) {
+    constexpr uint64_t kAll = KB == 2 ? ~0ull : 0xffffffffull;
+    const bool ragged = at + 32 * KB > spot.edge;
+    f32x4 score[NT][2 * KB];
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
+    for (int s = 0; s < 2 * KB; ++s)
 #pragma unroll
       for (int m = 0; m < NT; ++m) score[m][s] = f32x4{};
 #pragma unroll
     for (int i = 0; i < 2 * N; ++i) {
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
+      for (int s = 0; s < 2 * KB; ++s) {
         const V8 k = *reinterpret_cast<const V8*>(keys + (16 * s + col) * kKeyPitch + 64 * i + 16 * g);
 #pragma unroll
         for (int m = 0; m < NT; ++m) score[m][s] = M::mma(k, q[m][i], score[m][s]);
@@ -168,7 +171,7 @@ __global__ __launch_bounds__(kThreads, 1) void attend_rows_kernel(AttendBlocksPa
     }
     if constexpr (M::kRowScale) {
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
+      for (int s = 0; s < 2 * KB; ++s) {
         const u32v4 f = *reinterpret_cast<const u32v4*>(key_scale + 16 * s + 4 * g);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -176,25 +179,28 @@ __global__ __launch_bounds__(kThreads, 1) void attend_rows_kernel(AttendBlocksPa
           for (int m = 0; m < NT; ++m) score[m][s][e] *= __uint_as_float(f[e] & 0xffff0000u);
       }
     }
-    bf16x8 prob[NT], rest[NT];
+    bf16x8 prob[NT][KB], rest[NT][KB];
 #pragma unroll
     for (int m = 0; m < NT; ++m) {
       // x: what goes into the exponential.  First as if all keys were seen and the reference stayed.
-      float x[8], high = kNegInf;
+      float x[8 * KB], high = kNegInf;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < 8 * KB; ++j) {
         x[j] = __builtin_fmaf(score[m][j >> 2][j & 3], p.scale_log2, -top[m]);
         high = __builtin_elementwise_maximum(high, x[j]);  // no number passes no test
       }
-      if (here != ~0u || ragged || !__all(high <= kRowsSlack)) {
-        uint32_t vis = here;
-        if (ragged) vis &= attend_seen_by(spot, upto[m], tree_bits[m], at);
-        vis >>= 4 * g;  // bits 0..3: keys 4 g + e; bits 16..19: keys 16 + 4 g + e
+      if (here != kAll || ragged || !__all(high <= kRowsSlack)) {
         high = kNegInf;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          x[j] = (vis >> (16 * (j >> 2) + (j & 3))) & 1 ? score[m][j >> 2][j & 3] * p.scale_log2 : kNegInf;
-          high = fmaxf(high, x[j]);
+        for (int k = 0; k < KB; ++k) {
+          uint32_t vis = static_cast<uint32_t>(here >> (32 * k));
+          if (ragged) vis &= attend_seen_by(spot, upto[m], tree_bits[m], at + 32 * k);
+          vis >>= 4 * g;  // bits 0..3: keys 4 g + e; bits 16..19: keys 16 + 4 g + e
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            x[8 * k + j] = (vis >> (16 * (j >> 2) + (j & 3))) & 1 ? score[m][2 * k + (j >> 2)][j & 3] * p.scale_log2 : kNegInf;
+            high = fmaxf(high, x[8 * k + j]);
+          }
         }
         high = rows_max(high);
         if (__any(high > top[m] + kRowsSlack || top[m] == kNegInf)) {
@@ -207,67 +213,79 @@ __global__ __launch_bounds__(kThreads, 1) void attend_rows_kernel(AttendBlocksPa
         }
         const float base = top[m] == kNegInf ? 0.0f : top[m];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] -= base;
+        for (int j = 0; j < 8 * KB; ++j) x[j] -= base;
       }
-      u32v4 first, second;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float y = __builtin_amdgcn_exp2f(x[2 * j]), z = __builtin_amdgcn_exp2f(x[2 * j + 1]);
-        sum[m] += y;
-        sum[m] += z;
-        first[j] = __builtin_bit_cast(uint32_t, bf16x2{static_cast<__bf16>(y), static_cast<__bf16>(z)});
-        second[j] = __builtin_bit_cast(uint32_t, bf16x2{static_cast<__bf16>(y - __uint_as_float(first[j] << 16)),
-                                                        static_cast<__bf16>(z - __uint_as_float(first[j] & 0xffff0000u))});
+      for (int k = 0; k < KB; ++k) {
+        u32v4 first, second;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float y = __builtin_amdgcn_exp2f(x[8 * k + 2 * j]), z = __builtin_amdgcn_exp2f(x[8 * k + 2 * j + 1]);
+          sum[m] += y;
+          sum[m] += z;
+          first[j] = __builtin_bit_cast(uint32_t, bf16x2{static_cast<__bf16>(y), static_cast<__bf16>(z)});
+          asm("" : "+v"(first[j]));  // else the compiler converts y once more for its half
+          second[j] = __builtin_bit_cast(uint32_t, bf16x2{static_cast<__bf16>(y - __uint_as_float(first[j] << 16)),
+                                                          static_cast<__bf16>(z - __uint_as_float(first[j] & 0xffff0000u))});
+        }
+        prob[m][k] = __builtin_bit_cast(bf16x8, first);
+        rest[m][k] = __builtin_bit_cast(bf16x8, second);
       }
-      prob[m] = __builtin_bit_cast(bf16x8, first);
-      rest[m] = __builtin_bit_cast(bf16x8, second);
     }
     const char* src = values + (4 * g + (col >> 2)) * kPitch + kPlane * ((col >> 1) & 1) + 8 * (col & 1);
-    auto value = [&](int c) {
+    auto value = [&](int k, int c) {
       typedef __attribute__((address_space(3))) s16x4* Lds4;
       typedef short s16x8 __attribute__((ext_vector_type(8)));
-      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds4)(src + 16 * c));
-      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds4)(src + 16 * kPitch + 16 * c));
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds4)(src + 32 * k * kPitch + 16 * c));
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds4)(src + (32 * k + 16) * kPitch + 16 * c));
       return __builtin_bit_cast(bf16x8, s16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
     };
     if (ragged) {
       // values that are no numbers: every wave sees the same ones, so all of them come to these barriers or none
       uint32_t any = 0;
 #pragma unroll
-      for (int c = 0; c < 4 * N; ++c) {
-        const u16x8 bits = __builtin_bit_cast(u16x8, value(c));
+      for (int k = 0; k < KB; ++k)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) any |= no_number(bits[e]);
-      }
+        for (int c = 0; c < 4 * N; ++c) {
+          const u16x8 bits = __builtin_bit_cast(u16x8, value(k, c));
+#pragma unroll
+          for (int e = 0; e < 8; ++e) any |= no_number(bits[e]);
+        }
       if (__any(any != 0)) {
 #pragma unroll
-        for (int m = 0; m < NT; ++m) {
-          const bf16x8 sees = seen_places((here & attend_seen_by(spot, upto[m], tree_bits[m], at)) >> (4 * g));
+        for (int k = 0; k < KB; ++k)
 #pragma unroll
-          for (int c = 0; c < 4 * N; ++c) out[m][c] = spoilt(out[m][c], odd_places(value(c)), sees);
-        }
+          for (int m = 0; m < NT; ++m) {
+            const uint32_t vis = static_cast<uint32_t>(here >> (32 * k)) & attend_seen_by(spot, upto[m], tree_bits[m], at + 32 * k);
+            const bf16x8 sees = seen_places(vis >> (4 * g));
+#pragma unroll
+            for (int c = 0; c < 4 * N; ++c) out[m][c] = spoilt(out[m][c], odd_places(value(k, c)), sees);
+          }
         __syncthreads();
-        for (int i = threadIdx.x; i < 32 * 8 * N; i += kThreads) {
+        for (int i = threadIdx.x; i < 32 * KB * 8 * N; i += kThreads) {
           const int r = i / (8 * N), eight = i % (8 * N);
           clear_odd(values + r * kPitch + (eight & 1) * kPlane + 16 * (eight >> 1));
         }
         __syncthreads();
       }
     }
+    // two channels' products side by side: each waits for the one before it of its own sum
 #pragma unroll
-    for (int c = 0; c < 4 * N; c += 2) {
-      const bf16x8 v = value(c), w = value(c + 1);
+    for (int k = 0; k < KB; ++k)
 #pragma unroll
-      for (int m = 0; m < NT; ++m) {
-        out[m][c] = Mat<__bf16>::mma(v, prob[m], out[m][c]);
-        out[m][c + 1] = Mat<__bf16>::mma(w, prob[m], out[m][c + 1]);
+      for (int c = 0; c < 4 * N; c += 2) {
+        const bf16x8 v = value(k, c), w = value(k, c + 1);
+#pragma unroll
+        for (int m = 0; m < NT; ++m) {
+          out[m][c] = Mat<__bf16>::mma(v, prob[m][k], out[m][c]);
+          out[m][c + 1] = Mat<__bf16>::mma(w, prob[m][k], out[m][c + 1]);
+        }
+#pragma unroll
+        for (int m = 0; m < NT; ++m) {
+          out[m][c] = Mat<__bf16>::mma(v, rest[m][k], out[m][c]);
+          out[m][c + 1] = Mat<__bf16>::mma(w, rest[m][k], out[m][c + 1]);
+        }
       }
-#pragma unroll
-      for (int m = 0; m < NT; ++m) {
-        out[m][c] = Mat<__bf16>::mma(v, rest[m], out[m][c]);
-        out[m][c + 1] = Mat<__bf16>::mma(w, rest[m], out[m][c + 1]);
-      }
-    }
   };
 
   if (steps > 0) {
@@ -283,21 +301,21 @@ __global__ __launch_bounds__(kThreads, 1) void attend_rows_kernel(AttendBlocksPa
     fetch(1);
     for (int step = 0; step < steps; ++step) {
       __syncthreads();  // this step is decoded, and nobody reads the other half any more
-      const int turn = step / (kTurn / kKeys);
+      decode(lds + ((step + 1) & 1) * step_bytes(N));  // past the end: zeros
+      fetch(step + 2);  // its slots were kept at least two barriers ago
       if (step % (kTurn / kKeys) == 0) {  // the last turn's half of the slots is read no more
+        const int turn = step / (kTurn / kKeys);
         keep(turn + 1);
         find(turn + 2);
         ask(turn + 3);
       }
-      decode(lds + ((step + 1) & 1) * step_bytes(N));  // past the end: zeros
-      fetch(step + 2);  // its slots were kept at least two barriers ago
       char* from = lds + (step & 1) * step_bytes(N);
       const int in = (step * kKeys) & (2 * kTurn - 1);
       const uint64_t here = __ballot(slots[in + lane] >= 0);
 #pragma unroll 1
-      for (int half = 0; half < 2; ++half)
-        work(from + 32 * half * kKeyPitch, from + kKeys * kKeyPitch + 32 * half * kPitch, k0 + step * kKeys + 32 * half,
-             static_cast<uint32_t>(here >> (32 * half)), scales + in + 32 * half);
+      for (int part = 0; part < 2 / KB; ++part)
+        work(from + 32 * part * kKeyPitch, from + kKeys * kKeyPitch + 32 * part * kPitch, k0 + step * kKeys + 32 * part,
+             KB == 2 ? here : here >> (32 * part) & 0xffffffffull, scales + in + 32 * part);
     }
   }
 
@@ -337,39 +355,34 @@ __global__ __launch_bounds__(kThreads, 1) void attend_rows_kernel(AttendBlocksPa
   }
 }
 
-template <class T, int N, int NT>
+template <class T, int N, int NT, int KB, int WAVES>
 void launch(const AttendBlocksParams& p, hipStream_t s) {
   const int64_t lists = static_cast<int64_t>(p.units) * p.splits;
-  const uint32_t grid = static_cast<uint32_t>((p.dealt == 1 ? (lists + 7) / 8 * 8 : lists) * p.row_groups);
-  hipLaunchKernelGGL((attend_rows_kernel<T, N, NT>), dim3(grid), dim3(kThreads), lds_bytes(N), s, p);
-}
-
-template <class T, int N>
-void launch_tiles(const AttendBlocksParams& p, int tiles, hipStream_t s) {
-  if (tiles == 1) {
-    launch<T, N, 1>(p, s);
-  } else if constexpr (N <= kRowsWide) {
-    launch<T, N, 2>(p, s);
-  }
+  const uint32_t grid = p.dealt == 0 ? attend_grid(p) : static_cast<uint32_t>((p.dealt == 1 ? (lists + 7) / 8 * 8 : lists) * p.row_groups);
+  hipLaunchKernelGGL((attend_rows_kernel<T, N, NT, KB, WAVES>), dim3(grid), dim3(64 * WAVES), lds_bytes(N, WAVES), s, p);
 }
 
 template <class T>
-void launch_type(const AttendBlocksParams& p, int width, int tiles, hipStream_t s) {
-  switch (width) {
-    case 1: launch_tiles<T, 1>(p, tiles, s); break;
-    case 2: launch_tiles<T, 2>(p, tiles, s); break;
-    case 3: launch_tiles<T, 3>(p, tiles, s); break;
-    default: launch_tiles<T, 4>(p, tiles, s);
+void launch_type(const AttendBlocksParams& p, const RowsShape& r, hipStream_t s) {
+  switch (r.width) {
+    case 1:
+      if (r.waves == 8) return launch<T, 1, 2, 1, 8>(p, s);
+      return r.tiles == 1 ? launch<T, 1, 1, 2, 4>(p, s) : launch<T, 1, 2, 1, 4>(p, s);
+    case 2:
+      if (r.waves == 8) return launch<T, 2, 2, 1, 8>(p, s);
+      return r.tiles == 1 ? launch<T, 2, 1, 2, 4>(p, s) : launch<T, 2, 2, 1, 4>(p, s);
+    case 3: return launch<T, 3, 2, 1, 4>(p, s);
+    default: return launch<T, 4, 2, 1, 4>(p, s);
   }
 }
 
 }  // namespace
 
-void launch_attend_rows(const AttendBlocksParams& p, int width, int tiles, hipStream_t s) {
+void launch_attend_rows(const AttendBlocksParams& p, const RowsShape& r, hipStream_t s) {
   if (p.a.dtype == ETS_BF16) {
-    launch_type<__bf16>(p, width, tiles, s);
+    launch_type<__bf16>(p, r, s);
   } else {
-    launch_type<_Float16>(p, width, tiles, s);
+    launch_type<_Float16>(p, r, s);
   }
 }
 
