@@ -22,7 +22,7 @@ constexpr int step_bytes(int n) { return kKeys * (key_pitch(n) + value_pitch(n))
 constexpr int lds_bytes(int n, int waves) { return 2 * step_bytes(n) + 2 * 64 * waves * 8; }
 
 // Eight waves share a step of 64 keys and values, decoded once into LDS, and
-// take 16 NT query rows each.  A step is brought two steps ahead into
+// take 16 NT query rows each.  A step is brought three steps ahead into
 // registers and decoded one step ahead into the other half of LDS, so one
 // barrier a step is enough.
 //
@@ -111,30 +111,33 @@ __global__ __launch_bounds__(64 * WAVES, rows_per_unit(N, WAVES)) void attend_ro
     stride[j] = static_cast<uint32_t>(is_value[j] ? a.v_s : a.k_s);
     if (16 * piece[j] >= (is_value[j] ? a.Dv : a.D)) row[j] = nothing, stride[j] = 0;  // channels that are not there
   }
-  u32v4 code[kItems];
-  uint32_t scale[kItems];
-  auto fetch = [&](int step) {
+  struct Codes {
+    u32v4 code[kItems];
+    uint32_t scale[kItems];
+  };
+  auto fetch = [&](Codes& c, int step) {
     const int from = (step * kKeys) & (2 * kTurn - 1);
 #pragma unroll
     for (int j = 0; j < kItems; ++j) {
       const int32_t slot = slots[from + key[j]];
-      scale[j] = scales[from + key[j]];
+      c.scale[j] = scales[from + key[j]];
       const uint64_t at = row[j] + static_cast<uint64_t>(static_cast<uint32_t>(slot)) * stride[j];
-      code[j] = load_global<u32v4>(slot >= 0 ? at : nothing);
+      c.code[j] = load_global<u32v4>(slot >= 0 ? at : nothing);
     }
   };
-  auto decode = [&](char* to) {
+  auto decode = [&](const Codes& from, int step) {
+    char* to = lds + (step & 1) * step_bytes(N);
     char* values = to + kKeys * kKeyPitch;
 #pragma unroll
     for (int j = 0; j < kItems; ++j) {
-      const u32v4 c = code[j];
+      const u32v4 c = from.code[j];
       if (is_value[j]) {
-        const float f = __uint_as_float(scale[j] << 16);
+        const float f = __uint_as_float(from.scale[j] << 16);
         char* dst = values + key[j] * kPitch + 16 * piece[j];
         *reinterpret_cast<bf16x8*>(dst) = codes_bf16(c[0], c[1], f);
         *reinterpret_cast<bf16x8*>(dst + kPlane) = codes_bf16(c[2], c[3], f);
       } else {
-        const float f = M::kRowScale ? 1.0f : __uint_as_float(scale[j] & 0xffff0000u);
+        const float f = M::kRowScale ? 1.0f : __uint_as_float(from.scale[j] & 0xffff0000u);
         V8* dst = reinterpret_cast<V8*>(to + key[j] * kKeyPitch + 32 * piece[j]);
         dst[0] = M::keys(c[0], c[1], f);
         dst[1] = M::keys(c[2], c[3], f);
@@ -296,13 +299,16 @@ __global__ __launch_bounds__(64 * WAVES, rows_per_unit(N, WAVES)) void attend_ro
     find(1);
     ask(2);
     __syncthreads();
-    fetch(0);
-    decode(lds);
-    fetch(1);
-    for (int step = 0; step < steps; ++step) {
+    Codes even, odd;
+    fetch(even, 0);
+    fetch(odd, 1);
+    decode(even, 0);
+    fetch(even, 2);
+    // one step: `codes` hold the next one's, and then those of the step two behind it
+    auto advance = [&](Codes& codes, int step) {
       __syncthreads();  // this step is decoded, and nobody reads the other half any more
-      decode(lds + ((step + 1) & 1) * step_bytes(N));  // past the end: zeros
-      fetch(step + 2);  // its slots were kept at least two barriers ago
+      decode(codes, step + 1);  // past the end: zeros
+      fetch(codes, step + 3);   // its slots were kept at least one barrier ago
       if (step % (kTurn / kKeys) == 0) {  // the last turn's half of the slots is read no more
         const int turn = step / (kTurn / kKeys);
         keep(turn + 1);
@@ -316,6 +322,10 @@ __global__ __launch_bounds__(64 * WAVES, rows_per_unit(N, WAVES)) void attend_ro
       for (int part = 0; part < 2 / KB; ++part)
         work(from + 32 * part * kKeyPitch, from + kKeys * kKeyPitch + 32 * part * kPitch, k0 + step * kKeys + 32 * part,
              KB == 2 ? here : here >> (32 * part) & 0xffffffffull, scales + in + 32 * part);
+    };
+    for (int step = 0; step < steps; step += 2) {
+      advance(odd, step);
+      if (step + 1 < steps) advance(even, step + 1);
     }
   }
 
