@@ -120,13 +120,10 @@ __global__ __launch_bounds__(THREADS) void block_write_kernel(BlockParams p) {
   const int64_t first = p.first[b], end = first + min(p.counts[b], p.T);
   const int64_t start = (first / p.block + j) * p.block;
   if (first < 0 || start >= end) return;
-  const int64_t slot = block_slot(p, b, start);
-  if (slot < 0) return;
+  const int64_t slot = block_slot(p, b, start);  // on its way while the rows are read
   const int64_t low = first > start ? first : start, high = end < start + p.block ? end : start + p.block;
   const int stay = static_cast<int>(low - start), count = static_cast<int>(high - low);
   const char* src = p.x + b * p.x_b + (low - first) * p.x_t + h * p.x_h;
-  uint8_t* codes = p.codes + slot * p.codes_s + h * p.codes_h;
-  uint8_t* scale = p.scales + slot / p.block * p.scales_s + h * p.scales_h;
   const int row = p.D / 8, items = count * row;
   auto value = [&](int i) {
     const uint32_t r = div_by(i, p.by_row), v = i - r * row;
@@ -145,6 +142,9 @@ __global__ __launch_bounds__(THREADS) void block_write_kernel(BlockParams p) {
     kept[u] = V8{};
     if (i < items) kept[u] = value(i);
   }
+  if (slot < 0) return;
+  uint8_t* codes = p.codes + slot * p.codes_s + h * p.codes_h;
+  uint8_t* scale = p.scales + slot / p.block * p.scales_s + h * p.scales_h;
 #pragma unroll
   for (int u = 0; u < kKept; ++u) {
     float x[8];
@@ -305,7 +305,7 @@ ets_status ets_block_write(const void* x, int64_t x_b, int64_t x_t, int64_t x_h,
   p.blocks = static_cast<int32_t>(blocks);
   p.by_blocks = fast_div(p.blocks);
   // a wave alone has no barrier to wait at, and holds what a step brings
-  const bool narrow = most * D <= 64 * 8 * 2;
+  const bool narrow = most * D <= 64 * 8 * kKept;
   auto s = static_cast<hipStream_t>(stream);
   if (dtype == ETS_BF16) {
     launch_write<__bf16>(p, grid, narrow, s);
