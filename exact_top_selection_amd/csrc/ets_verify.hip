@@ -9,7 +9,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kEach = 16;                  // values of a lane
-constexpr int kChunk = kThreads * kEach;   // of a workgroup
+constexpr int kChunk = kThreads * kEach;   // whose sums are kept
+constexpr int kPerUnit = 4;                // workgroups of a compute unit
 
 // What the walk over a sequence's nodes leaves.
 struct Walk {
@@ -23,6 +24,7 @@ struct VerifyParams {
   const char* draft;
   int64_t p_b, p_t, q_b, q_t;  // bytes
   int32_t B, T, V, chunks;
+  int32_t each, groups;  // chunks of a workgroup, workgroups of a sequence
   const int32_t* tokens;
   int64_t tok_b;
   const float* uniform;
@@ -35,7 +37,7 @@ struct VerifyParams {
   int32_t* out_counts;
   f64x2* sums;  // [B][chunks]: of the last draw's weights, of the target's
   Walk* walks;  // [B]
-  FastDiv by_chunks;
+  FastDiv by_groups;
 };
 
 // A probability in 64 bits; negative ones, infinities and no numbers count as 0.
@@ -173,19 +175,26 @@ __device__ __forceinline__ double wave_sum(double x) {
   return x;
 }
 
-// Sums of the last draw's weights, chunk by chunk.  Every workgroup of a
-// sequence walks its line for itself: a launch of its own would cost more.
+// Sums of the last draw's weights, chunk by chunk; a workgroup takes a few chunks of one sequence, whose line it walks
+// for itself (a launch of its own would cost more), and reads them side by side: lane t holds vectors t, t + 256, .. of
+// a chunk.
+//
+// The walk is three loads in turn (line and tokens, probabilities, the row), so workgroups take as many chunks as leave
+// about kPerUnit of them to a compute unit.
 template <class T>
 __global__ __launch_bounds__(kThreads) void weigh_kernel(VerifyParams p) {
+  constexpr int n = 16 / sizeof(T), kVectors = kEach / n;
+  typedef T V __attribute__((ext_vector_type(n)));
   __shared__ Walk shared;
   __shared__ uint32_t refused[kChunk / 32];
-  __shared__ double part[2][kThreads / 64];
-  const int b = static_cast<int>(div_by(blockIdx.x, p.by_chunks)), chunk = static_cast<int>(blockIdx.x) - b * p.chunks;
+  __shared__ f64x2 part[2][kThreads / 64];
+  const int b = static_cast<int>(div_by(blockIdx.x, p.by_groups)), group = static_cast<int>(blockIdx.x) - b * p.groups;
+  const int first = group * p.each, end = min(first + p.each, p.chunks);
   if (threadIdx.x < 64) {
     uint64_t line;
     const Walk w = walk<T>(p, b, &line);
     if (threadIdx.x == 0) shared = w;
-    if (chunk == 0) {
+    if (group == 0) {
       if (threadIdx.x == 0) {
         p.walks[b] = w;
         p.out_counts[b] = w.count;
@@ -206,35 +215,77 @@ __global__ __launch_bounds__(kThreads) void weigh_kernel(VerifyParams p) {
   __syncthreads();
   const Walk w = shared;
   if (w.count == 0) return;
-  const int base = chunk * kChunk;
-  if (!p.draft) mark_refused(p, b, w.kids, base, refused);
-  double last[kEach], whole[kEach], a = 0.0, c = 0.0;
-  weights<T>(p, b, w, base, refused, last, whole);
+  const bool residue = p.draft && w.kids;
+  const char* target = p.probs + b * p.p_b + w.node * p.p_t;
+  const char* draft = p.draft + b * p.q_b + w.node * p.q_t;
+  for (int chunk = first; chunk < end; ++chunk) {
+    const int base = chunk * kChunk;
+    const bool marks = !p.draft && w.kids;
+    V x[kVectors], y[kVectors];
 #pragma unroll
-  for (int j = 0; j < kEach; ++j) a += last[j], c += whole[j];
-  a = wave_sum(a), c = wave_sum(c);
-  if ((threadIdx.x & 63) == 0) part[0][threadIdx.x >> 6] = a, part[1][threadIdx.x >> 6] = c;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    a = c = 0.0;
+    for (int i = 0; i < kVectors; ++i) {
+      const int at = base + (i * kThreads + static_cast<int>(threadIdx.x)) * n;
+      x[i] = y[i] = V{};
+      if (at + n <= p.V) {
+        x[i] = load_any<V>(target + at * static_cast<int64_t>(sizeof(T)));
+        if (residue) y[i] = load_any<V>(draft + at * static_cast<int64_t>(sizeof(T)));
+      } else {
 #pragma unroll
-    for (int i = 0; i < kThreads / 64; ++i) a += part[0][i], c += part[1][i];
-    p.sums[static_cast<int64_t>(b) * p.chunks + chunk] = f64x2{a, c};
+        for (int j = 0; j < n; ++j) {
+          if (at + j < p.V) {
+            x[i][j] = load_any<T>(target + (at + j) * static_cast<int64_t>(sizeof(T)));
+            if (residue) y[i][j] = load_any<T>(draft + (at + j) * static_cast<int64_t>(sizeof(T)));
+          }
+        }
+      }
+    }
+    if (marks) mark_refused(p, b, w.kids, base, refused);
+    double a = 0.0, c = 0.0;
+#pragma unroll
+    for (int i = 0; i < kVectors; ++i) {
+      const int in = (i * kThreads + static_cast<int>(threadIdx.x)) * n;
+      const uint32_t gone = marks ? refused[in >> 5] >> (in & 31) : 0;
+#pragma unroll
+      for (int j = 0; j < n; ++j) {
+        const double whole = clean(x[i][j]);
+        double last = whole;
+        if (residue) {
+          const double d = whole - clean(y[i][j]);
+          last = d > 0.0 ? d : 0.0;
+        }
+        if (gone >> j & 1) last = 0.0;
+        a += last, c += whole;
+      }
+    }
+    a = wave_sum(a), c = wave_sum(c);
+    if ((threadIdx.x & 63) == 0) part[chunk & 1][threadIdx.x >> 6] = f64x2{a, c};
+    __syncthreads();  // `part` of this chunk is there; that of the one before has been read, and so have its marks
+    if (threadIdx.x == 0) {
+      const f64x2* q = part[chunk & 1];
+      p.sums[static_cast<int64_t>(b) * p.chunks + chunk] = (q[0] + q[1]) + (q[2] + q[3]);
+    }
   }
 }
 
 // Exclusive running sums of x over the workgroup's lanes, and the total.
-__device__ __forceinline__ double before_lane(double x, double* waves, double* total) {
+template <class V>
+__device__ __forceinline__ V shift_up(V x, int by);
+template <>
+__device__ __forceinline__ double shift_up(double x, int by) { return __shfl_up(x, by); }
+template <>
+__device__ __forceinline__ f64x2 shift_up(f64x2 x, int by) { return f64x2{__shfl_up(x[0], by), __shfl_up(x[1], by)}; }
+template <class V>
+__device__ __forceinline__ V before_lane(V x, V* waves, V* total) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  double run = x;
+  V run = x;
 #pragma unroll
   for (int i = 1; i < 64; i *= 2) {
-    const double y = __shfl_up(run, i);
+    const V y = shift_up(run, i);
     if (lane >= i) run += y;
   }
   if (lane == 63) waves[wave] = run;
   __syncthreads();
-  double base = 0.0, all = 0.0;
+  V base = {}, all = {};
 #pragma unroll
   for (int i = 0; i < kThreads / 64; ++i) {
     if (i < wave) base += waves[i];
@@ -242,7 +293,7 @@ __device__ __forceinline__ double before_lane(double x, double* waves, double* t
   }
   __syncthreads();
   *total = all;
-  const double up = __shfl_up(run, 1);
+  const V up = shift_up(run, 1);
   return lane == 0 ? base : base + up;
 }
 
@@ -250,6 +301,7 @@ __device__ __forceinline__ double before_lane(double x, double* waves, double* t
 // mark, and the value in it.
 template <class T>
 __global__ __launch_bounds__(kThreads) void draw_kernel(VerifyParams p) {
+  __shared__ f64x2 both[kThreads / 64];
   __shared__ double waves[kThreads / 64];
   __shared__ uint32_t refused[kChunk / 32];
   __shared__ int found, fallback;
@@ -260,22 +312,17 @@ __global__ __launch_bounds__(kThreads) void draw_kernel(VerifyParams p) {
   const f64x2* sums = p.sums + static_cast<int64_t>(b) * p.chunks;
   const int per = (p.chunks + kThreads - 1) / kThreads;  // chunks of a lane, one after another
   const int from = min(static_cast<int>(threadIdx.x) * per, p.chunks), to = min(from + per, p.chunks);
-  double a = 0.0, c = 0.0, total, whole_total;
-  for (int i = from; i < to; ++i) a += sums[i][0], c += sums[i][1];
-  double base = before_lane(a, waves, &total);
-  const double whole_base = before_lane(c, waves, &whole_total);
-  const int which = total > 0.0 ? 0 : 1;
-  if (which) {
-    // nothing is left to draw from but the target's own distribution
-    a = c, base = whole_base, total = whole_total;
-    w.kids = 0;
-  }
+  f64x2 own = {}, totals;
+  for (int i = from; i < to; ++i) own += sums[i];
+  if (threadIdx.x == 0) found = INT32_MAX, fallback = -1;  // before the barriers below
+  const f64x2 bases = before_lane(own, both, &totals);
+  const int which = totals[0] > 0.0 ? 0 : 1;
+  if (which) w.kids = 0;  // nothing is left to draw from but the target's own distribution
+  const double base = bases[which], total = totals[which];
   int32_t* out = p.out_tokens + static_cast<int64_t>(b) * p.T + w.count - 1;
   if (!(total > 0.0)) return;  // stays -1
   const double u = static_cast<double>(p.uniform[b * p.u_b]);
   const double mark = u > 0.0 ? (u < 1.0 ? u * total : total) : u == u ? 0.0 : total;
-  if (threadIdx.x == 0) found = INT32_MAX, fallback = -1;
-  __syncthreads();
   // the first chunk whose running sum passes the mark, else the last one that weighs something
   {
     double run = base;
@@ -332,7 +379,7 @@ bool sizes_fit(int32_t B, int32_t T, int32_t V) {
 
 template <class T>
 void launch(const VerifyParams& p, hipStream_t s) {
-  hipLaunchKernelGGL(weigh_kernel<T>, dim3(static_cast<uint32_t>(p.B * p.chunks)), dim3(kThreads), 0, s, p);
+  hipLaunchKernelGGL(weigh_kernel<T>, dim3(static_cast<uint32_t>(p.B * p.groups)), dim3(kThreads), 0, s, p);
   hipLaunchKernelGGL(draw_kernel<T>, dim3(static_cast<uint32_t>(p.B)), dim3(kThreads), 0, s, p);
 }
 
@@ -371,7 +418,11 @@ ets_status ets_verify_drafts(const void* probs, int64_t p_b, int64_t p_t, const 
   p.out_tokens = out_tokens, p.out_path = out_path, p.out_counts = out_counts;
   p.sums = static_cast<f64x2*>(workspace);
   p.walks = reinterpret_cast<Walk*>(p.sums + static_cast<int64_t>(B) * p.chunks);
-  p.by_chunks = fast_div(p.chunks);
+  const int64_t work = static_cast<int64_t>(B) * p.chunks, room = static_cast<int64_t>(cu) * kPerUnit;
+  const int64_t each = (work + room - 1) / room;
+  p.each = static_cast<int32_t>(each < p.chunks ? each : p.chunks);
+  p.groups = (p.chunks + p.each - 1) / p.each;
+  p.by_groups = fast_div(p.groups);
   auto s = static_cast<hipStream_t>(stream);
   if (dtype == ETS_BF16) {
     launch<__bf16>(p, s);
