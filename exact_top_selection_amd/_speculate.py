@@ -14,6 +14,7 @@ on torch's current stream.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional, Sequence, Tuple
 
 import torch
@@ -178,16 +179,20 @@ def block_keep(codes: torch.Tensor, scales: torch.Tensor, page_table: torch.Tens
          _rows(path, "path"), many)
 
 
-def _space(what, index, like, workspace, size, *args):
-    """(address, bytes) of the workspace that `size(*args)` asks for, and what keeps it alive."""
+@functools.lru_cache(maxsize=256)
+def _bytes(what, index, size, *args):
+    """Bytes of workspace that `size` asks for on a device: a function of the sizes in `args` alone."""
     need = _sz(0)
-    if torch._C._cuda_getDevice() == index:
-        st = size(*args, ctypes.byref(need))
-    else:
-        st = _on(index, size, *args, ctypes.byref(need))
+    sizes = (ctypes.byref(_BlocksArgs(*args)),) if what == "ets_attend_blocks" else args
+    st = _on(index, getattr(_lib(), size), *sizes, ctypes.byref(need))
     if st:
         _check(st, what)
-    nbytes = need.value
+    return need.value
+
+
+def _space(what, index, like, workspace, size, *args):
+    """(address, bytes) of the workspace that `size` asks for, and what keeps it alive."""
+    nbytes = _bytes(what, index, size, *args)
     if workspace is not None:
         if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or not workspace.is_contiguous():
             raise TypeError("workspace must be a contiguous torch.Tensor on a HIP device")
@@ -245,14 +250,16 @@ def attend_blocks(q: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.Tensor
         mask, mask_b = tree_mask.data_ptr(), _rows(tree_mask, "tree_mask")
     out = q.new_empty((B, T, Hq, Dv))
     lse = q.new_empty((B, T, Hq), dtype=torch.float32)
+    q_b, q_t, q_h, _ = q.stride()
+    k_s, k_h, _ = k_codes.stride()
+    v_s, v_h, _ = v_codes.stride()
     args = ctypes.byref(_BlocksArgs(
-        B, T, Hq, Hkv, D, Dv, kind, block, L, page_size, S, q.data_ptr(), *q.stride()[:3],
-        k_codes.data_ptr(), *k_codes.stride()[:2], k_scales.data_ptr(), *k_scales.stride(),
-        v_codes.data_ptr(), *v_codes.stride()[:2], v_scales.data_ptr(), *v_scales.stride(),
+        B, T, Hq, Hkv, D, Dv, kind, block, L, page_size, S, q.data_ptr(), q_b, q_t, q_h,
+        k_codes.data_ptr(), k_s, k_h, k_scales.data_ptr(), *k_scales.stride(),
+        v_codes.data_ptr(), v_s, v_h, v_scales.data_ptr(), *v_scales.stride(),
         page_table.data_ptr(), pt_b, lens, start, mask, mask_b, out.data_ptr(), lse.data_ptr()))
-    lib = _lib()
-    at, nbytes, kept = _space("ets_attend_blocks", index, q, workspace, lib.ets_attend_blocks_workspace_size, args)
-    _run(index, "ets_attend_blocks", lib.ets_attend_blocks, args, at, nbytes)
+    at, nbytes, kept = _space("ets_attend_blocks", index, q, workspace, "ets_attend_blocks_workspace_size", B, T, Hq, Hkv, D, Dv, kind, block, L, page_size, S)
+    _run(index, "ets_attend_blocks", _lib().ets_attend_blocks, args, at, nbytes)
     return out, lse
 
 
@@ -309,11 +316,11 @@ def verify_drafts(probs: torch.Tensor, tokens: torch.Tensor, uniform: torch.Tens
     out = probs.new_empty((2, B, T), dtype=torch.int32)
     counts = probs.new_empty((B,), dtype=torch.int32)
     lib = _lib()
-    at, nbytes, kept = _space("ets_verify_drafts", index, probs, workspace, lib.ets_verify_workspace_size, B, T, V)
+    at, nbytes, kept = _space("ets_verify_drafts", index, probs, workspace, "ets_verify_workspace_size", B, T, V)
     _run(index, "ets_verify_drafts", lib.ets_verify_drafts, probs.data_ptr(), *probs.stride()[:2], draft, q_b, q_t, B, T, V,
          tokens.data_ptr(), _rows(tokens, "tokens"), uniform.data_ptr(), _rows(uniform, "uniform"), mask, mask_b, many,
          out.data_ptr(), out.data_ptr() + 4 * B * T, counts.data_ptr(), kind, at, nbytes)
-    return out[0], out[1], counts
+    return (*out.unbind(0), counts)
 
 
 def _pool(refs: torch.Tensor, table: torch.Tensor, what: str) -> Tuple[int, int]:
@@ -390,7 +397,7 @@ def pages_extend(refs: torch.Tensor, page_table: torch.Tensor, lens: torch.Tenso
         raise ValueError("page_size must be 1 to %d, got %s" % (_INT32, page_size))
     lacking = refs.new_empty((B,))
     lib = _lib()
-    at, nbytes, kept = _space("ets_pages_extend", index, refs, workspace, lib.ets_pages_workspace_size, P, B * M)
+    at, nbytes, kept = _space("ets_pages_extend", index, refs, workspace, "ets_pages_workspace_size", P, B * M)
     _run(index, "ets_pages_extend", lib.ets_pages_extend, refs.data_ptr(), P, page_table.data_ptr(), _rows(page_table, "page_table"),
          B, M, need, page_size, lacking.data_ptr(), at, nbytes)
     return lacking
@@ -438,7 +445,7 @@ def pages_fork(refs: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor,
     lacking = refs.new_empty((n,))
     held, count = _buffers(buffers, P, index)
     lib = _lib()
-    at, nbytes, kept = _space("ets_pages_fork", index, refs, workspace, lib.ets_pages_workspace_size, P, n)
+    at, nbytes, kept = _space("ets_pages_fork", index, refs, workspace, "ets_pages_workspace_size", P, n)
     _run(index, "ets_pages_fork", lib.ets_pages_fork, refs.data_ptr(), P, page_table.data_ptr(), _rows(page_table, "page_table"), B, M,
          have, page_size, of, n, out.data_ptr(), _rows(out, "out"), out.shape[1], lacking.data_ptr(), held, count, at, nbytes)
     return out, lacking
@@ -457,7 +464,7 @@ def pages_compact(refs: torch.Tensor, page_table: torch.Tensor, buffers: Sequenc
     moved = refs.new_empty((P,))
     held, count = _buffers(buffers, P, index)
     lib = _lib()
-    at, nbytes, kept = _space("ets_pages_compact", index, refs, workspace, lib.ets_pages_workspace_size, P, B * M)
+    at, nbytes, kept = _space("ets_pages_compact", index, refs, workspace, "ets_pages_workspace_size", P, B * M)
     _run(index, "ets_pages_compact", lib.ets_pages_compact, refs.data_ptr(), P, page_table.data_ptr(),
          _rows(page_table, "page_table"), B, M, moved.data_ptr(), held, count, at, nbytes)
     return moved

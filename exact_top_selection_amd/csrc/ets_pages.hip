@@ -9,7 +9,7 @@ namespace ets {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kEach = 16;                 // entries of a lane, kThreads apart
+constexpr int kEach = 8;                  // entries of a lane, kThreads apart
 constexpr int kChunk = kThreads * kEach;  // of a workgroup
 constexpr int64_t kMaxPages = static_cast<int64_t>(1) << 26;
 constexpr int kPiece = 16384;             // bytes of a page that a workgroup moves at a time
@@ -53,14 +53,8 @@ __device__ __forceinline__ int pages_of(const PoolParams& p, int len) {
 }
 __device__ __forceinline__ bool holds(const PoolParams& p, int entry) { return entry >= 0 && entry < p.P; }
 
-// Whether entry i wants a page: of the table (extend), or of the list of branches (fork).
-template <int KIND>
+// Whether branch i wants a page of its own.
 __device__ __forceinline__ bool wants(const PoolParams& p, int i) {
-  if (i >= p.entries) return false;
-  if (KIND == kExtend) {
-    const int b = static_cast<int>(div_by(i, p.by_M)), j = i - b * p.M;
-    return j < pages_of(p, p.lens[b]) && !holds(p, p.table[b * p.pt_b + j]);
-  }
   const int b = p.parents[i];
   if (b < 0 || b >= p.B) return false;
   const int len = max(p.lens[b], 0), full = static_cast<int>(div_by(len, p.by_page));
@@ -71,7 +65,7 @@ __device__ __forceinline__ bool wants(const PoolParams& p, int i) {
 __device__ __forceinline__ int places(uint32_t flags, int (&place)[kEach], int* counts) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   constexpr int kWaves = kThreads / 64, kParts = kEach * kWaves;
-  static_assert(kParts == 64, "one wave sums the parts");
+  static_assert(kParts <= 64, "one wave sums the parts");
 #pragma unroll
   for (int j = 0; j < kEach; ++j) {
     const uint64_t set = __ballot(flags >> j & 1);
@@ -80,15 +74,15 @@ __device__ __forceinline__ int places(uint32_t flags, int (&place)[kEach], int* 
   }
   __syncthreads();
   if (wave == 0) {
-    const int mine = counts[lane];
+    const int mine = lane < kParts ? counts[lane] : 0;
     int run = mine;
 #pragma unroll
-    for (int i = 1; i < 64; i *= 2) {
+    for (int i = 1; i < kParts; i *= 2) {
       const int y = __shfl_up(run, i);
       if (lane >= i) run += y;
     }
-    counts[lane] = run - mine;
-    if (lane == 63) counts[kParts] = run;
+    if (lane < kParts) counts[lane] = run - mine;
+    if (lane == kParts - 1) counts[kParts] = run;
   }
   __syncthreads();
 #pragma unroll
@@ -117,20 +111,42 @@ __device__ __forceinline__ void chunk_base(const int32_t* counts, int n, int min
 
 __device__ __forceinline__ uint32_t free_flags(const PoolParams& p, int chunk) {
   uint32_t flags = 0;
+  int refs[kEach];
 #pragma unroll
   for (int j = 0; j < kEach; ++j) {
     const int64_t i = static_cast<int64_t>(chunk) * kChunk + j * kThreads + threadIdx.x;
-    if (i < p.P && p.refs[i] <= 0) flags |= 1u << j;
+    refs[j] = i < p.P ? p.refs[i] : 1;
   }
+#pragma unroll
+  for (int j = 0; j < kEach; ++j) flags |= refs[j] <= 0 ? 1u << j : 0;
   return flags;
 }
 template <int KIND>
 __device__ __forceinline__ uint32_t want_flags(const PoolParams& p, int chunk) {
   uint32_t flags = 0;
+  if constexpr (KIND == kExtend) {
+    // all loads first, those of entries behind the last from the last
+    int len[kEach], entry[kEach], column[kEach];
 #pragma unroll
-  for (int j = 0; j < kEach; ++j) {
-    const int64_t i = static_cast<int64_t>(chunk) * kChunk + j * kThreads + threadIdx.x;
-    if (i < p.entries && wants<KIND>(p, static_cast<int>(i))) flags |= 1u << j;
+    for (int j = 0; j < kEach; ++j) {
+      const int64_t at = static_cast<int64_t>(chunk) * kChunk + j * kThreads + threadIdx.x;
+      const int i = at < p.entries ? static_cast<int>(at) : p.entries - 1;
+      const int b = static_cast<int>(div_by(i, p.by_M));
+      column[j] = i - b * p.M;
+      len[j] = p.lens[b];
+      entry[j] = p.table[b * p.pt_b + column[j]];
+    }
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+      const int64_t at = static_cast<int64_t>(chunk) * kChunk + j * kThreads + threadIdx.x;
+      if (at < p.entries && column[j] < pages_of(p, len[j]) && !holds(p, entry[j])) flags |= 1u << j;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+      const int64_t i = static_cast<int64_t>(chunk) * kChunk + j * kThreads + threadIdx.x;
+      if (i < p.entries && wants(p, static_cast<int>(i))) flags |= 1u << j;
+    }
   }
   return flags;
 }
@@ -220,13 +236,13 @@ __global__ __launch_bounds__(kThreads) void branch_kernel(PoolParams p) {
   int32_t* row = p.out + i * p.out_b;
   const bool there = b >= 0 && b < p.B;
   const int full = there ? static_cast<int>(div_by(max(p.lens[b], 0), p.by_page)) : 0;
-  const bool want = wants<kFork>(p, i);
+  const bool want = wants(p, i);
   // branches before this one that want a page
   int before = 0;
   if (want) {
     const int chunk = i / kChunk;
     for (int k = threadIdx.x; k < chunk; k += kThreads) before += p.entry_count[k];
-    for (int k = chunk * kChunk + static_cast<int>(threadIdx.x); k < i; k += kThreads) before += wants<kFork>(p, k);
+    for (int k = chunk * kChunk + static_cast<int>(threadIdx.x); k < i; k += kThreads) before += wants(p, k);
   }
 #pragma unroll
   for (int k = 1; k < 64; k *= 2) before += __shfl_xor(before, k);
@@ -286,7 +302,7 @@ __global__ __launch_bounds__(kThreads) void copy_kernel(Buffers buffers, const i
 // Fourth launch of fork: the pages that branches hold in part.
 __global__ __launch_bounds__(kThreads) void branch_copy_kernel(PoolParams p, Buffers buffers) {
   const uint32_t i = div_by(blockIdx.x, p.by_pieces);
-  if (!wants<kFork>(p, static_cast<int>(i))) return;
+  if (!wants(p, static_cast<int>(i))) return;
   const int b = p.parents[i], full = static_cast<int>(div_by(p.lens[b], p.by_page));
   const int to = p.out[i * p.out_b + full];
   if (to < 0) return;
