@@ -387,6 +387,74 @@ def test_attend_blocks_far_slots():
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+@pytest.mark.parametrize("T", [1, 40])
+@pytest.mark.parametrize("size", [112, 0, -90])  # powers of two: values to 448 * 2^112, and to 2^-90
+@pytest.mark.parametrize("order", ["rising", "falling"])
+@pytest.mark.parametrize("Hq,D", [(4, 64), (2, 128), (3, 192), (2, 256)])
+def test_values_near_the_ends_of_the_range(Hq, D, order, size, T):
+    """Scores pass each other by up to 2^20 while values stand near either end of what sums can hold."""
+    g, n = gen(60), 400
+    kc, ks = torch.zeros(n, 1, D, dtype=torch.uint8), torch.full((n // 8, 1), 127, dtype=torch.uint8)
+    at = torch.arange(n) if order == "rising" else torch.arange(n).flip(0)
+    kc[:, 0, 0] = spec.encode(at.double() / n * 40 - 20)
+    vc, vs = filled(n, 1, D, 8, g)
+    vc = vc & 0x7F if size == 112 else vc  # nothing cancels
+    vs = (vs.int() - vs.int().max() + 127 + size - (8 if size < 0 else 0)).clamp(1, 246).to(torch.uint8)
+    q = torch.zeros(1, T, Hq, D)
+    q[..., 0] = (torch.arange(T * Hq).view(1, T, Hq) % 5 - 2) / 2 * math.sqrt(D) / math.log2(math.e)
+    table = torch.arange(n // 8, dtype=torch.int32).view(1, -1)
+    check_blocks((q.to(BF16), kc, ks, vc, vs, table, ints(n), 8, n, ints(n - T) if T > 1 else None, None), BF16)
+
+
+@pytest.mark.parametrize("T", [1, 40])
+@pytest.mark.parametrize("behind", [True, False])
+def test_scores_of_minus_infinity(behind, T):
+    """Keys whose score leaves the 32-bit range: alone they are nothing, before others they weigh nothing."""
+    g, n, D = gen(61), 200, 64
+    kc, ks = torch.zeros(n, 1, D, dtype=torch.uint8), torch.full((n // 8, 1), 246, dtype=torch.uint8)
+    kc[:, 0, 0] = 0x7E
+    if behind:
+        ks[160 // 8:] = 1
+    vc, vs = filled(n, 1, D, 8, g)
+    q = torch.zeros(1, T, 2, D)
+    q[..., 0] = -3e4
+    table = torch.arange(n // 8, dtype=torch.int32).view(1, -1)
+    out, lse = run_blocks(q.to(BF16), kc, ks, vc, vs, table, ints(n), 8, n, ints(n - T) if T > 1 else None, None)
+    if not behind:
+        assert not out.any() and (lse == -math.inf).all()
+        return
+    sees = [torch.arange(160, n if T == 1 else n - T + t + 1) for t in range(T)]
+    want = spec.attend(q.to(BF16), kc, ks, vc, vs, [sees])
+    close(out, want[0], want[2], BF16)
+    close(lse, want[1], want[3], FP32)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("B,T,Hq,Hkv,D,L", [(32, 256, 16, 16, 64, 300), (32, 130, 32, 16, 128, 200),  # for several turns of the device
+                                            (1, 100, 8, 8, 64, 64), (1, 64, 3, 3, 128, 200), (9, 33, 1, 1, 256, 900),
+                                            (5, 70, 6, 3, 192, 150), (70, 1, 8, 8, 128, 700)])
+def test_attend_blocks_of_many_lists(B, T, Hq, Hkv, D, L, dtype):
+    """Batches that fill the device in its different ways; some rows of them next to the formula."""
+    g = gen(62)
+    table, P = pages(B, -(-L // 16), 1, g)
+    kc, ks = filled(P * 16, Hkv, D, 16, g)
+    vc, vs = filled(P * 16, Hkv, D, 16, g)
+    q = torch.randn(B, T, Hq, D, generator=g).to(dtype)
+    lens = torch.randint(max(1, L // 2), L + 1, (B,), generator=g, dtype=torch.int32)
+    first = lens - T // 2  # half of the tokens are padding
+    out, lse = run_blocks(q, kc, ks, vc, vs, table, lens, 16, L, first if T > 1 else None, None)
+    G = Hq // Hkv
+    for b in {0, B // 2, B - 1}:
+        for h in {0, Hkv - 1}:
+            lists = spec.seen(table[b:b + 1], 16, P, lens[b:b + 1], L, T, first[b:b + 1] if T > 1 else None)
+            some = sorted({0, 1, T // 3, T // 2 - 1, T // 2, T - 1} & set(range(T)))
+            want = spec.attend(q[b:b + 1, some, h * G:h * G + G], kc[:, h:h + 1], ks[:, h:h + 1], vc[:, h:h + 1], vs[:, h:h + 1],
+                               [[lists[0][t] for t in some]])
+            close(out[b:b + 1, some, h * G:h * G + G], want[0], want[2], dtype)
+            close(lse[b:b + 1, some, h * G:h * G + G], want[1], want[3], FP32)
+    assert torch.equal(out, run_blocks(q, kc, ks, vc, vs, table, lens, 16, L, first if T > 1 else None, None)[0])
+
+
 # ---- verify_drafts
 
 def check_verify(probs, tokens, uniform, draft=None, mask=None, lens=None):
