@@ -842,3 +842,50 @@ def test_refusals():
     ]:
         with pytest.raises(error):
             call()
+
+
+def test_the_example():
+    """examples/speculative_decode.py: graph replays follow the eager steps, attention is that of the cache, pages are counted."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "speculative_decode.py")
+    loader = importlib.util.spec_from_file_location("speculative_decode", path)
+    example = importlib.util.module_from_spec(loader)
+    loader.loader.exec_module(example)
+
+    def decoder():
+        d = example.SpeculativeDecoder(2, 3, 200, pages=100, heads=4, kv_heads=2, dim=64, drafts=10, vocabulary=50, page=16, block=8)
+        d.prefill(120, piece=48)
+        d.project()
+        return d
+
+    a, b = decoder(), decoder()
+    graph, held = a.capture()
+    for _ in range(4):
+        before, tree = b.lens.cpu(), b.tree.cpu()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in held]
+        # b's cache as attention sees it: with the tree's rows, before the accepted ones move
+        reach = b.lens + b.drafts
+        ets.pages_extend(b.refs, b.table, reach, b.page)
+        positions = b.lens[:, None] + b.depth
+        b._write(b._turned(b.key, positions), b.value, b.table, b.lens, b.drafts)
+        kc, ks, vc, vs = (t.view(torch.uint8).cpu() for t in b.pool)
+        lists = spec.seen(b.table.cpu(), b.page, 100, reach.cpu(), b.capacity, 10, before, tree)
+        want = spec.attend(b._turned(b.q, positions).cpu(), kc, ks, vc, vs, lists)
+        out, new, counts, lacking = b.step()
+        close(got[0], want[0], want[2], BF16)
+        for x, y in zip(got, (out, new, counts, lacking)):
+            assert torch.equal(x, y)
+        for x, y in zip((a.refs, a.table, a.lens, a.tokens), (b.refs, b.table, b.lens, b.tokens)):
+            assert torch.equal(x, y)
+        for x, y in zip(a.pool, b.pool):
+            assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+        table = a.table.cpu()
+        assert torch.equal(a.refs.cpu(), torch.bincount(table[table >= 0].long(), minlength=100).int())
+        a.project(), b.project()
+    assert int(got[2].max()) > 1 and int(got[3].sum()) == 0
+    a.finish()
+    used = int((a.refs > 0).sum())
+    assert used == int(((a.lens + 15) // 16).sum()) and (a.refs[:used] > 0).all() and int(a.table.max()) == used - 1
