@@ -110,7 +110,13 @@ __device__ __forceinline__ void raise_rows(const BlockParams& p, uint8_t* codes,
 
 // One workgroup takes the new rows of one block and head: they are looked at
 // twice, for their largest magnitude and for their codes, and up to kKept
-// vectors a lane (16384 values of 256 lanes) stay in registers between.
+// vectors a lane (16384 values of 256 lanes) stay in registers between.  Up to
+// 4096 values are one wave's, which waits at no barrier, and x is asked for
+// before the page is known.
+//
+// Measured: 20 us for pieces of 8192 tokens of four prompts, 8 x 128, fp16,
+// blocks of 32 (75 MB, 3.7 TB/s; 29 us with 256 lanes and the page first), in one
+// turn of waves, each with three loads in turn; 4.8 us for 64 rows (the loads).
 template <class T, int THREADS>
 __global__ __launch_bounds__(THREADS) void block_write_kernel(BlockParams p) {
   typedef T V8 __attribute__((ext_vector_type(8)));
@@ -178,6 +184,7 @@ __global__ __launch_bounds__(THREADS) void block_write_kernel(BlockParams p) {
 
 // One workgroup takes one sequence and head: the rows that move come into LDS
 // with their scales (64 rows of 256 codes at most), and go out block by block.
+// 7 us for 64 trees of 40, 8 x 128: five loads in turn and the barriers.
 __global__ __launch_bounds__(kThreads) void block_keep_kernel(BlockParams p) {
   __shared__ float waves[kThreads / 64];
   __shared__ __align__(16) u32v2 rows[ETS_MAX_TREE * ETS_MAX_BLOCK_DIM / 8];
