@@ -57,7 +57,7 @@ ets_status make_plan(const ets_attend_blocks_args* a, BlocksPlan* plan) {
   if (plan->many) {
     // Two workgroups of four waves share a compute unit, and one works while the other waits at its barrier.  Eight waves
     // decode each key for twice the rows, which pays where there are workgroups for several turns of the device (8
-    // sequences of 8192, 1024 tokens each: 1412 us against 1598; 2 of them of uneven length: 373 against 340).
+    // sequences of 8192, 1024 tokens each: 1508 us against 1598; 2 of them of uneven length: 373 against 340).
     const int64_t wide = static_cast<int64_t>(p.units) * ((p.rows + 255) / 256);
     plan->shape = {plan->width, plan->width <= 2 && p.rows >= 256 && wide >= 2 * cu ? 8 : 4, p.rows > 64 || plan->width > 2 ? 2 : 1};
     plan->mt = plan->shape.tiles;

@@ -34,7 +34,7 @@ struct PoolParams {
   const int32_t* parents;  // fork
   int32_t* out;
   int64_t out_b;
-  int32_t n, out_M;
+  int32_t out_M;
   int32_t* lacking;
   int32_t* moved;  // compact
   int32_t page_chunks, entries, entry_chunks;
@@ -497,7 +497,7 @@ ets_status ets_pages_fork(int32_t* refs, int64_t P, const int32_t* table, int64_
   int32_t cu = 0;
   if (ets_status st = device_ready(&cu); st != ETS_OK) return st;
   p.lens = lens, p.page_size = page_size, p.by_page = fast_div(page_size);
-  p.parents = parents, p.n = n, p.out = out, p.out_b = out_b, p.out_M = out_M, p.lacking = lacking;
+  p.parents = parents, p.out = out, p.out_b = out_b, p.out_M = out_M, p.lacking = lacking;
   auto s = static_cast<hipStream_t>(stream);
   hipLaunchKernelGGL(count_kernel<kFork>, dim3(grid_of(p.page_chunks + p.entry_chunks)), dim3(kThreads), 0, s, p);
   if (p.page_chunks) hipLaunchKernelGGL(list_kernel<kFork>, dim3(grid_of(p.page_chunks)), dim3(kThreads), 0, s, p);
