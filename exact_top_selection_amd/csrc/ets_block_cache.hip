@@ -123,9 +123,11 @@ __global__ __launch_bounds__(THREADS) void block_write_kernel(BlockParams p) {
   __shared__ float waves[THREADS / 64];
   const uint32_t bj = div_by(blockIdx.x, p.by_heads), h = blockIdx.x - bj * p.H;
   const uint32_t b = div_by(bj, p.by_blocks), j = bj - b * p.blocks;
-  const int64_t first = p.first[b], end = first + min(p.counts[b], p.T);
+  const int rows = min(p.counts[b], p.T);
+  const int64_t first = p.first[b], end = first + rows;
   const int64_t start = (first / p.block + j) * p.block;
-  if (first < 0 || start >= end) return;
+  // a sequence without rows does not own the block that its next position stands in
+  if (first < 0 || rows <= 0 || start >= end) return;
   const int64_t slot = block_slot(p, b, start);  // on its way while the rows are read
   const int64_t low = first > start ? first : start, high = end < start + p.block ? end : start + p.block;
   const int stay = static_cast<int>(low - start), count = static_cast<int>(high - low);
