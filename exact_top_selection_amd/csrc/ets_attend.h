@@ -206,10 +206,12 @@ __device__ __forceinline__ float attend_inverse(float sum) {
   return sum > 0.0f || sum != sum ? kUp / sum : 0.0f;
 }
 
-inline uint32_t attend_grid(const AttendParams& p) {
+inline int64_t attend_groups(const AttendParams& p) {
   const int64_t shares = static_cast<int64_t>(p.units / p.a.Hkv) * p.splits;
-  return static_cast<uint32_t>((shares + 7) / 8 * 8 * (p.a.Hkv / p.heads) * p.row_groups);
+  return (shares + 7) / 8 * 8 * (p.a.Hkv / p.heads) * p.row_groups;
 }
+// ... of which a launch holds fewer than 2^32 lanes, as the plans see to
+inline uint32_t attend_grid(const AttendParams& p) { return static_cast<uint32_t>(attend_groups(p)); }
 
 // The launch of the kernel for heads over 256 channels (ets_attend_wide.hip);
 // row_tiles: tiles of 16 query rows of a workgroup, as attend_wide_rows gives.

@@ -77,6 +77,8 @@ ets_status make_plan(const ets_attend_args* a, Plan* plan) {
   splits = splits > cap ? cap : splits;
   p.splits = static_cast<int>(splits < 1 ? 1 : splits);
   if (lists * (p.splits + 8) > INT32_MAX / 16) return ETS_ERR_INVALID_ARG;
+  // one launch, of fewer than 2^32 lanes
+  if (attend_groups(p) * (plan->width == 9 ? 2 * kThreads : kThreads) > UINT32_MAX) return ETS_ERR_INVALID_ARG;
   p.scale_log2 = static_cast<float>(1.4426950408889634074 / __builtin_sqrt(static_cast<double>(a->D)));
   p.by_page = fast_div(paged ? a->page_size : 1);
   p.by_heads = fast_div(a->Hkv);

@@ -85,6 +85,8 @@ ets_status make_plan(const ets_attend_blocks_args* a, BlocksPlan* plan) {
   const int64_t shares = static_cast<int64_t>(a->B) * p.splits, all = shares * a->Hkv;
   p.dealt = !plan->many || shares % 8 == 0 || shares >= 64 ? 0 : all % 8 == 0 || all >= 64 ? 1 : 2;
   if (lists * (p.splits + 8) > INT32_MAX / 16) return ETS_ERR_INVALID_ARG;
+  // one launch, of fewer than 2^32 lanes
+  if ((plan->many ? attend_rows_groups(p) * 64 * waves_rows : attend_groups(p) * kAttendThreads) > UINT32_MAX) return ETS_ERR_INVALID_ARG;
   p.scale_log2 = static_cast<float>(1.4426950408889634074 / __builtin_sqrt(static_cast<double>(a->D)));
   p.by_page = fast_div(a->page_size);
   p.by_block = fast_div(a->block);

@@ -46,6 +46,11 @@ struct RowsShape {
 // Workgroups of a compute unit, by LDS and registers.
 constexpr int rows_per_unit(int width, int waves) { return waves == 4 && width <= 2 ? 2 : 1; }
 
+inline int64_t attend_rows_groups(const AttendBlocksParams& p) {
+  const int64_t lists = static_cast<int64_t>(p.units) * p.splits;
+  return p.dealt == 0 ? attend_groups(p) : (p.dealt == 1 ? (lists + 7) / 8 * 8 : lists) * p.row_groups;
+}
+
 void launch_attend_rows(const AttendBlocksParams& p, const RowsShape& r, hipStream_t s);
 
 }  // namespace ets

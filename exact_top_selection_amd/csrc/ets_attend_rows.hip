@@ -379,8 +379,7 @@ __global__ __launch_bounds__(64 * WAVES, rows_per_unit(N, WAVES)) void attend_ro
 
 template <class T, int N, int NT, int KB, int WAVES>
 void launch(const AttendBlocksParams& p, hipStream_t s) {
-  const int64_t lists = static_cast<int64_t>(p.units) * p.splits;
-  const uint32_t grid = p.dealt == 0 ? attend_grid(p) : static_cast<uint32_t>((p.dealt == 1 ? (lists + 7) / 8 * 8 : lists) * p.row_groups);
+  const uint32_t grid = static_cast<uint32_t>(attend_rows_groups(p));
   hipLaunchKernelGGL((attend_rows_kernel<T, N, NT, KB, WAVES>), dim3(grid), dim3(64 * WAVES), lds_bytes(N, WAVES), s, p);
 }
 

@@ -25,6 +25,7 @@ struct BlockParams {
   const int32_t* path;  // keep
   int64_t path_b;
   int32_t blocks;  // that a sequence's new rows may touch
+  uint32_t group;  // the launch's first workgroup
   FastDiv by_blocks, by_heads, by_row;
 };
 
@@ -121,7 +122,7 @@ template <class T, int THREADS>
 __global__ __launch_bounds__(THREADS) void block_write_kernel(BlockParams p) {
   typedef T V8 __attribute__((ext_vector_type(8)));
   __shared__ float waves[THREADS / 64];
-  const uint32_t bj = div_by(blockIdx.x, p.by_heads), h = blockIdx.x - bj * p.H;
+  const uint32_t group = p.group + blockIdx.x, bj = div_by(group, p.by_heads), h = group - bj * p.H;
   const uint32_t b = div_by(bj, p.by_blocks), j = bj - b * p.blocks;
   const int rows = min(p.counts[b], p.T);
   const int64_t first = p.first[b], end = first + rows;
@@ -192,7 +193,7 @@ __global__ __launch_bounds__(kThreads) void block_keep_kernel(BlockParams p) {
   __shared__ __align__(16) u32v2 rows[ETS_MAX_TREE * ETS_MAX_BLOCK_DIM / 8];
   __shared__ int exponent[ETS_MAX_TREE];
   __shared__ int64_t source[ETS_MAX_TREE];
-  const uint32_t b = div_by(blockIdx.x, p.by_heads), h = blockIdx.x - b * p.H;
+  const uint32_t group = p.group + blockIdx.x, b = div_by(group, p.by_heads), h = group - b * p.H;
   const int64_t first = p.first[b];
   const int count = min(p.counts[b], p.T), lane = threadIdx.x & 63;
   if (first < 0 || count <= 0) return;
@@ -273,12 +274,15 @@ ets_status block_params(BlockParams* p, int32_t B, int32_t T, int32_t H, int32_t
 }
 
 template <class T>
-void launch_write(const BlockParams& p, int64_t grid, bool narrow, hipStream_t s) {
-  if (narrow) {
-    hipLaunchKernelGGL((block_write_kernel<T, 64>), dim3(static_cast<uint32_t>(grid)), dim3(64), 0, s, p);
-  } else {
-    hipLaunchKernelGGL((block_write_kernel<T, kThreads>), dim3(static_cast<uint32_t>(grid)), dim3(kThreads), 0, s, p);
-  }
+void launch_write(BlockParams p, int64_t groups, bool narrow, hipStream_t s) {
+  launch_in_turn(groups, narrow ? 64 : kThreads, [&](uint32_t first, uint32_t grid) {
+    p.group = first;
+    if (narrow) {
+      hipLaunchKernelGGL((block_write_kernel<T, 64>), dim3(grid), dim3(64), 0, s, p);
+    } else {
+      hipLaunchKernelGGL((block_write_kernel<T, kThreads>), dim3(grid), dim3(kThreads), 0, s, p);
+    }
+  });
 }
 
 }  // namespace
@@ -342,7 +346,10 @@ ets_status ets_block_keep(int32_t B, int32_t T, int32_t H, int32_t D, uint8_t* c
   int32_t cu = 0;
   if (ets_status st = device_ready(&cu); st != ETS_OK) return st;
   p.path = path, p.path_b = path_b;
-  hipLaunchKernelGGL(block_keep_kernel, dim3(static_cast<uint32_t>(B * H)), dim3(kThreads), 0, static_cast<hipStream_t>(stream), p);
+  launch_in_turn(static_cast<int64_t>(B) * H, kThreads, [&](uint32_t first_group, uint32_t grid) {
+    p.group = first_group;
+    hipLaunchKernelGGL(block_keep_kernel, dim3(grid), dim3(kThreads), 0, static_cast<hipStream_t>(stream), p);
+  });
   return hipGetLastError() == hipSuccess ? ETS_OK : ETS_ERR_HIP;
 }
 

@@ -224,6 +224,16 @@ struct Mat<_Float16> {
   }
 };
 
+// HIP launches fewer than 2^32 lanes at a time.  More workgroups than that go out in several launches, each told the
+// number of its first one: launch(first, how many).
+constexpr int64_t kMostLanes = static_cast<int64_t>(1) << 31;
+template <class F>
+void launch_in_turn(int64_t groups, int threads, F launch) {
+  const int64_t most = kMostLanes / threads;
+  for (int64_t first = 0; first < groups; first += most)
+    launch(static_cast<uint32_t>(first), static_cast<uint32_t>(groups - first < most ? groups - first : most));
+}
+
 inline bool dtype_known(int32_t dtype) { return dtype == ETS_BF16 || dtype == ETS_FP16 || dtype == ETS_FP32; }
 
 // ETS_OK where the current device is a gfx950; the device's compute units.

@@ -38,6 +38,7 @@ struct PoolParams {
   int32_t* lacking;
   int32_t* moved;  // compact
   int32_t page_chunks, entries, entry_chunks;
+  uint32_t group;  // the launch's first workgroup, where a launch does not hold them all
   // workspace
   int32_t* head;        // [0]: free pages under the number in use (compact)
   int32_t* page_count;  // free pages of each chunk
@@ -236,7 +237,7 @@ __global__ __launch_bounds__(kThreads) void extend_kernel(PoolParams p) {
 // Third launch of fork: a workgroup writes one branch's row.
 __global__ __launch_bounds__(kThreads) void branch_kernel(PoolParams p) {
   __shared__ int sums[8];
-  const int i = static_cast<int>(blockIdx.x);
+  const int i = static_cast<int>(p.group + blockIdx.x);
   const int b = p.parents[i];
   int32_t* row = p.out + i * p.out_b;
   const bool there = b >= 0 && b < p.B;
@@ -298,21 +299,21 @@ __device__ __forceinline__ void move_piece(const Buffers& buffers, int piece, in
   if (static_cast<int>(threadIdx.x) < n - tail) to[tail + threadIdx.x] = from[tail + threadIdx.x];
 }
 
-__global__ __launch_bounds__(kThreads) void copy_kernel(Buffers buffers, const int32_t* src, const int32_t* dst, int64_t P, FastDiv by_pieces) {
-  const uint32_t pair = div_by(blockIdx.x, by_pieces);
+__global__ __launch_bounds__(kThreads) void copy_kernel(Buffers buffers, const int32_t* src, const int32_t* dst, int64_t P, FastDiv by_pieces, uint32_t first) {
+  const uint32_t group = first + blockIdx.x, pair = div_by(group, by_pieces);
   const int64_t s = src[pair], d = dst[pair];
   if (s < 0 || s >= P || d < 0 || d >= P) return;
-  move_piece(buffers, static_cast<int>(blockIdx.x - pair * by_pieces.d), s, d);
+  move_piece(buffers, static_cast<int>(group - pair * by_pieces.d), s, d);
 }
 
 // Fourth launch of fork: the pages that branches hold in part.
 __global__ __launch_bounds__(kThreads) void branch_copy_kernel(PoolParams p, Buffers buffers) {
-  const uint32_t i = div_by(blockIdx.x, p.by_pieces);
+  const uint32_t group = p.group + blockIdx.x, i = div_by(group, p.by_pieces);
   if (!wants(p, static_cast<int>(i))) return;
   const int b = p.parents[i], full = static_cast<int>(div_by(p.lens[b], p.by_page));
   const int to = p.out[i * p.out_b + full];
   if (to < 0) return;
-  move_piece(buffers, static_cast<int>(blockIdx.x - i * p.by_pieces.d), p.table[b * p.pt_b + full], to);
+  move_piece(buffers, static_cast<int>(group - i * p.by_pieces.d), p.table[b * p.pt_b + full], to);
 }
 
 // Third launch of compact: page after page moves, the first workgroups' share, and table entries and counts follow.
@@ -416,8 +417,10 @@ ets_status ets_pages_copy(const ets_page_buffer* buffers, int32_t count, int64_t
   if (n > INT32_MAX / to.pieces) return ETS_ERR_INVALID_ARG;
   int32_t cu = 0;
   if (ets_status st = device_ready(&cu); st != ETS_OK) return st;
-  hipLaunchKernelGGL(copy_kernel, dim3(static_cast<uint32_t>(n * to.pieces)), dim3(kThreads), 0, static_cast<hipStream_t>(stream), to,
-                     src, dst, P, fast_div(to.pieces));
+  const FastDiv by_pieces = fast_div(to.pieces);
+  launch_in_turn(n * to.pieces, kThreads, [&](uint32_t first, uint32_t grid) {
+    hipLaunchKernelGGL(copy_kernel, dim3(grid), dim3(kThreads), 0, static_cast<hipStream_t>(stream), to, src, dst, P, by_pieces, first);
+  });
   return hipGetLastError() == hipSuccess ? ETS_OK : ETS_ERR_HIP;
 }
 
@@ -501,11 +504,15 @@ ets_status ets_pages_fork(int32_t* refs, int64_t P, const int32_t* table, int64_
   auto s = static_cast<hipStream_t>(stream);
   hipLaunchKernelGGL(count_kernel<kFork>, dim3(grid_of(p.page_chunks + p.entry_chunks)), dim3(kThreads), 0, s, p);
   if (p.page_chunks) hipLaunchKernelGGL(list_kernel<kFork>, dim3(grid_of(p.page_chunks)), dim3(kThreads), 0, s, p);
-  hipLaunchKernelGGL(branch_kernel, dim3(grid_of(n)), dim3(kThreads), 0, s, p);
-  if (held.pieces) {
-    p.by_pieces = fast_div(held.pieces);
-    hipLaunchKernelGGL(branch_copy_kernel, dim3(static_cast<uint32_t>(static_cast<int64_t>(n) * held.pieces)), dim3(kThreads), 0, s, p, held);
-  }
+  launch_in_turn(n, kThreads, [&](uint32_t first, uint32_t grid) {
+    p.group = first;
+    hipLaunchKernelGGL(branch_kernel, dim3(grid), dim3(kThreads), 0, s, p);
+  });
+  p.by_pieces = fast_div(held.pieces ? held.pieces : 1);
+  launch_in_turn(static_cast<int64_t>(n) * held.pieces, kThreads, [&](uint32_t first, uint32_t grid) {
+    p.group = first;
+    hipLaunchKernelGGL(branch_copy_kernel, dim3(grid), dim3(kThreads), 0, s, p, held);
+  });
   return hipGetLastError() == hipSuccess ? ETS_OK : ETS_ERR_HIP;
 }
 

@@ -25,6 +25,7 @@ struct VerifyParams {
   int64_t p_b, p_t, q_b, q_t;  // bytes
   int32_t B, T, V, chunks;
   int32_t each, groups;  // chunks of a workgroup, workgroups of a sequence
+  uint32_t group;        // the launch's first workgroup
   const int32_t* tokens;
   int64_t tok_b;
   const float* uniform;
@@ -192,7 +193,8 @@ __global__ __launch_bounds__(kThreads) void weigh_kernel(VerifyParams p) {
   __shared__ Walk shared;
   __shared__ uint32_t refused[kChunk / 32];
   __shared__ f64x2 part[2][kThreads / 64];
-  const int b = static_cast<int>(div_by(blockIdx.x, p.by_groups)), group = static_cast<int>(blockIdx.x) - b * p.groups;
+  const uint32_t at = p.group + blockIdx.x;
+  const int b = static_cast<int>(div_by(at, p.by_groups)), group = static_cast<int>(at) - b * p.groups;
   const int first = group * p.each, end = min(first + p.each, p.chunks);
   if (threadIdx.x < 64) {
     uint64_t line;
@@ -310,7 +312,7 @@ __global__ __launch_bounds__(kThreads) void draw_kernel(VerifyParams p) {
   __shared__ uint32_t refused[kChunk / 32];
   __shared__ int found, fallback;
   __shared__ double found_base;
-  const int b = blockIdx.x;
+  const int b = static_cast<int>(p.group + blockIdx.x);
   Walk w = p.walks[b];
   if (w.count == 0) return;
   const f64x2* sums = p.sums + static_cast<int64_t>(b) * p.chunks;
@@ -382,9 +384,15 @@ bool sizes_fit(int32_t B, int32_t T, int32_t V) {
 }
 
 template <class T>
-void launch(const VerifyParams& p, hipStream_t s) {
-  hipLaunchKernelGGL(weigh_kernel<T>, dim3(static_cast<uint32_t>(p.B * p.groups)), dim3(kThreads), 0, s, p);
-  hipLaunchKernelGGL(draw_kernel<T>, dim3(static_cast<uint32_t>(p.B)), dim3(kThreads), 0, s, p);
+void launch(VerifyParams p, hipStream_t s) {
+  launch_in_turn(static_cast<int64_t>(p.B) * p.groups, kThreads, [&](uint32_t first, uint32_t grid) {
+    p.group = first;
+    hipLaunchKernelGGL(weigh_kernel<T>, dim3(grid), dim3(kThreads), 0, s, p);
+  });
+  launch_in_turn(p.B, kThreads, [&](uint32_t first, uint32_t grid) {
+    p.group = first;
+    hipLaunchKernelGGL(draw_kernel<T>, dim3(grid), dim3(kThreads), 0, s, p);
+  });
 }
 
 }  // namespace

@@ -129,7 +129,8 @@ ets_status ets_index_scores(const void* q, int64_t q_b, int64_t q_t, int64_t q_h
  * p_j at least 2^-24, so that they are finite where the sum of the values is,
  * and lose what lies beneath 2^-100 in values.  The p_j of these sums have 16
  * bits (two bf16 numbers).  A value or key that is NaN reaches the rows that
- * see it and no others.
+ * see it and no others.  Sizes that need 2^32 lanes or more in the one launch
+ * (16 million workgroups) are refused.
  */
 typedef struct ets_attend_args {
   int32_t B, T, Hq, Hkv, D, Dv;

@@ -54,8 +54,9 @@ extern "C" {
  * infinities become +-448 * 2^e.  Rows of the block behind the new ones keep
  * their bytes and are taken for nothing.  A sequence with first[b] < 0 or
  * counts[b] <= 0 is left alone.  The pages that one call writes belong to one
- * sequence each.  H * D <= 2^28, D <= ETS_MAX_BLOCK_DIM, B * H and T up to
- * 2^31 - 1.  Rows of table_pages entries, pt_b apart.
+ * sequence each.  H * D <= 2^28, D <= ETS_MAX_BLOCK_DIM; T, and B * H times
+ * the blocks that T rows may touch, up to 2^31 - 1.  Rows of table_pages
+ * entries, pt_b apart.
  */
 ets_status ets_block_write(const void* x, int64_t x_b, int64_t x_t, int64_t x_h, int32_t B, int32_t T, int32_t H,
                            int32_t D, uint8_t* codes, int64_t codes_s, int64_t codes_h, uint8_t* scales,
@@ -88,7 +89,9 @@ ets_status ets_block_keep(int32_t B, int32_t T, int32_t H, int32_t D, uint8_t* c
  *     first[b], and first[b] + j for j <= t, or, with tree_mask, for j < T with
  *     bit j of tree_mask[b][t] set (T <= ETS_MAX_TREE then).
  * A row that sees nothing has out = 0 and lse = -inf.  Numerics are those of
- * ets_attend; products of keys are exact for bf16 and fp16 queries.
+ * ets_attend; products of keys are exact for bf16 and fp16 queries.  One launch
+ * takes a call, a workgroup of 256 or 512 lanes 16 to 256 rows of a list: sizes
+ * that need 2^32 lanes or more (16 million workgroups) are refused.
  */
 typedef struct ets_attend_blocks_args {
   int32_t B, T, Hq, Hkv, D, Dv;
@@ -160,7 +163,8 @@ typedef struct ets_page_buffer {
 
 /* Page dst[i] of every buffer becomes page src[i], i < n.  Pairs with a number
  * outside [0, P) are skipped; the destinations of one call differ from each
- * other and from its sources. */
+ * other and from its sources.  n times the buffers' pieces of 16 KB of a page is
+ * at most 2^31 - 1, here and for the branches of a fork. */
 ets_status ets_pages_copy(const ets_page_buffer* buffers, int32_t count, int64_t P, const int32_t* src, const int32_t* dst,
                           int64_t n, void* stream);
 

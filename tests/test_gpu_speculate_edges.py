@@ -32,3 +32,109 @@ def test_block_write_of_no_rows_writes_nothing(dtype, D, block):
     got = codes.to(dev()), scales.to(dev())
     ets.block_write(x.to(dev()), *got, table.to(dev()), first.to(dev()), counts.to(dev()), block)
     assert torch.equal(got[1].cpu(), want[1]) and torch.equal(got[0].cpu()[:5 * block], codes[:5 * block])
+
+
+# ---- more workgroups than a launch holds (2^32 lanes: 2^24 workgroups of 256 lanes, 2^26 of one wave)
+
+def test_copies_of_more_pieces_than_a_launch_holds():
+    n = (1 << 18) + 1
+    held = torch.randint(0, 256, (64, 2 * n, 3), dtype=torch.uint8, device=dev())
+    want = held.clone()
+    order = torch.randperm(2 * n, device=dev()).int()
+    src, dst = order[:n].contiguous(), order[n:].contiguous()
+    want[:, dst.long()] = held[:, src.long()]
+    ets.pages_copy(list(held.unbind(0)), src, dst, 2 * n)
+    assert torch.equal(held, want)
+
+
+def test_branches_of_more_pieces_than_a_launch_holds():
+    n = (1 << 18) + 1
+    held = torch.randint(0, 256, (64, n + 1, 5), dtype=torch.uint8, device=dev())
+    refs = torch.zeros(n + 1, dtype=torch.int32, device=dev())
+    refs[0] = 1
+    table, lens = torch.zeros(1, 1, dtype=torch.int32, device=dev()), torch.ones(1, dtype=torch.int32, device=dev())
+    parents = torch.zeros(n, dtype=torch.int32, device=dev())
+    rows, lacking = ets.pages_fork(refs, table, lens, 2, parents, list(held.unbind(0)))
+    assert torch.equal(rows[:, 0], torch.arange(1, n + 1, dtype=torch.int32, device=dev())) and not lacking.any()
+    assert (refs == 1).all() and torch.equal(held, held[:, :1].expand_as(held))
+    # more branches than that, of full pages
+    many = (1 << 24) + 5
+    of = torch.full((many,), -1, dtype=torch.int32, device=dev())
+    of[::2] = 0
+    rows, lacking = ets.pages_fork(refs, table, lens, 1, of)
+    assert torch.equal(rows[:, 0], of) and not lacking.any() and int(refs[0]) == 1 + (many + 1) // 2
+
+
+def test_writes_of_more_blocks_than_a_launch_holds():
+    # one wave a block: 2^26 and more of them
+    T, H = (1 << 13) + 1, 1 << 13
+    table = torch.randperm(129, device=dev()).int().view(1, 129)
+    x = torch.randn(1, T, 1, 32, device=dev()).to(BF16)
+    codes = torch.zeros(129 * 64, H, 32, dtype=torch.uint8, device=dev())
+    scales = torch.zeros(129 * 64, H, dtype=torch.uint8, device=dev())
+    one = codes[:, :1].clone(), scales[:, :1].clone()
+    at, n = ints(0).to(dev()), ints(T).to(dev())
+    ets.block_write(x.expand(1, T, H, 32), codes, scales, table, at, n, 64)
+    ets.block_write(x, *one, table, at, n, 64)
+    assert bool((codes.view(torch.int64) == one[0].view(torch.int64)).all()) and bool((scales == one[1]).all()) and bool(one[1].any())
+    # four waves a block, most of them of sequences without rows
+    B, T, H = (1 << 12) + 1, 1 << 14, 8
+    x = torch.randn(1, T, H, 256, device=dev()).to(BF16)
+    table = torch.full((B, 257), -1, dtype=torch.int32, device=dev())
+    table[0], table[-1] = torch.randperm(514, device=dev()).int().view(2, 257)
+    first, counts = torch.zeros(B, dtype=torch.int32, device=dev()), torch.zeros(B, dtype=torch.int32, device=dev())
+    first[-1] = 45
+    counts[::B - 1] = T
+    got, want = ((torch.zeros(514 * 64, H, 256, dtype=torch.uint8, device=dev()), torch.zeros(514 * 2, H, dtype=torch.uint8, device=dev()))
+                 for _ in range(2))
+    ets.block_write(x.expand(B, T, H, 256), *got, table, first, counts, 64)
+    ets.block_write(x.expand(2, T, H, 256), *want, table[::B - 1].contiguous(), first[::B - 1].contiguous(), counts[::B - 1].contiguous(), 64)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and int((got[1] > 0).sum()) == (512 + 513) * H
+
+
+def test_moves_of_more_rows_than_a_launch_holds():
+    B, H = (1 << 12) + 1, 1 << 12
+    codes = torch.randint(0, 256, (2 * B, H, 32), dtype=torch.uint8, device=dev()) & 0xF7  # numbers all
+    scales = torch.randint(100, 150, (2 * B, H), dtype=torch.uint8, device=dev())
+    table = torch.randperm(B, device=dev()).int().view(B, 1)
+    first, counts = torch.zeros(B, dtype=torch.int32, device=dev()), torch.ones(B, dtype=torch.int32, device=dev())
+    path = torch.ones(B, 2, dtype=torch.int32, device=dev())
+    want = codes.clone(), scales.clone()
+    for b in range(0, B, 1000):
+        part = slice(b, min(b + 1000, B))
+        ets.block_keep(*want, table[part], first[part], path[part], counts[part], 2)
+    assert not torch.equal(want[0][::2], codes[::2])
+    ets.block_keep(codes, scales, table, first, path, counts, 2)
+    assert torch.equal(codes, want[0]) and torch.equal(scales, want[1])
+
+
+def test_verification_of_more_sequences_than_a_launch_holds():
+    B = (1 << 24) + 3
+    pick = torch.randint(0, 2, (B, 1), device=dev())
+    probs = torch.zeros(B, 1, 2, dtype=FP16, device=dev()).scatter_(2, pick[:, None], 1.0)
+    tokens, path, counts = ets.verify_drafts(probs, torch.zeros(1, 1, dtype=torch.int32, device=dev()).expand(B, 1),
+                                             torch.full((1, 1), 0.5, device=dev()).expand(B, 1))
+    assert torch.equal(tokens, pick.int()) and not path.any() and (counts == 1).all()
+
+
+def test_attention_of_more_lists_than_a_launch_holds():
+    """Refused, in either cache's form; as many as a launch does hold are computed."""
+    one, page = ints(1).to(dev()), torch.zeros(1, 1, dtype=torch.int32, device=dev())
+
+    def heads(H):
+        q = torch.zeros(1, 1, 1, 32, dtype=BF16, device=dev()).expand(1, 1, H, 32)
+        codes = torch.randint(0, 127, (1, H, 32), dtype=torch.uint8, device=dev())
+        return q, codes, torch.randint(120, 134, (1, H), dtype=torch.uint8, device=dev())
+
+    for H in ((1 << 21) + 1, (1 << 22) + 1):  # odd numbers, so that a workgroup takes one
+        q, codes, scales = heads(H)
+        with pytest.raises(ets.EtsError):
+            ets.attend_blocks(q, codes, scales, codes, scales, page, one, 1, 1)
+        with pytest.raises(ets.EtsError):
+            ets.attend_paged(q, codes, scales.view(1, H, 1), codes, scales.view(1, H, 1), page, one, 1, 1)
+    q, codes, scales = heads((1 << 21) - 1)
+    want = (codes.view(torch.float8_e4m3fn).float() * torch.exp2(scales.float() - 127)[..., None]).to(BF16).view(1, 1, -1, 32)
+    out, lse = ets.attend_blocks(q, codes, scales, codes, scales, page, one, 1, 1)
+    assert torch.equal(out, want) and not lse.any()
+    out, lse = ets.attend_paged(q, codes, scales.view(1, -1, 1), codes, scales.view(1, -1, 1), page, one, 1, 1)
+    assert torch.equal(out, want) and not lse.any()
