@@ -345,6 +345,17 @@ def _written(table: torch.Tensor, what: str) -> None:
         raise ValueError("rows of %s must not overlap" % what)
 
 
+def _near(a: torch.Tensor, b: torch.Tensor) -> bool:
+    """Whether an entry of one 2-D int32 tensor lies between the first and the last of the other."""
+    def span(t):
+        (n, m), (sn, sm) = t.shape, t.stride()
+        return t.data_ptr(), t.data_ptr() + 4 * ((n - 1) * sn + (m - 1) * sm + 1)
+    if not a.numel() or not b.numel():
+        return False
+    (a0, a1), (b0, b1) = span(a), span(b)
+    return a0 < b1 and b0 < a1
+
+
 def _buffers(buffers: Sequence[torch.Tensor], P: int, index: int):
     """A pool's buffers as the C ABI takes them: P pages of equal size each, one after another."""
     if isinstance(buffers, torch.Tensor) or len(buffers) > MAX_BUFFERS:
@@ -422,8 +433,10 @@ def pages_fork(refs: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor,
 
     Row i shares the pages that the lens[b] positions of row b = parents[i] (int32 [n]) fill, which gain one in ``refs``
     each; a page that they fill in part is copied, in all ``buffers`` (as for :func:`pages_copy`), to a free one, lowest
-    first in the order of i.  Other entries are -1; all are where parents[i] is outside [0, B).  ``out`` may be rows of the
-    same table that are nobody's parents here; what they held before is not let go.
+    first in the order of i.  Other entries are -1; all are where parents[i] is outside [0, B).  ``out`` (int32 [n, any
+    width]) may be rows of the same table, parents among them: all are read before any is written (from a copy of the table,
+    where the two overlap).  What they held before is not let go.  A branch has the pages that its row of ``out`` has room
+    for; those behind them are not shared, and are not counted as lacking.
     """
     P, index = _pool(refs, page_table, "page_table")
     B, M = page_table.shape
@@ -442,6 +455,8 @@ def pages_fork(refs: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor,
         if out.shape[0] != n or out.shape[1] > _INT32:
             raise ValueError("out must have %d rows, got %d" % (n, out.shape[0]))
         _written(out, "out")
+        if _near(out, page_table):
+            page_table = page_table.clone()
     lacking = refs.new_empty((n,))
     held, count = _buffers(buffers, P, index)
     lib = _lib()

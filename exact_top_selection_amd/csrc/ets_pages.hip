@@ -394,6 +394,33 @@ ets_status pool_params(PoolParams* p, int32_t* refs, int64_t P, int32_t* table, 
   return ETS_OK;
 }
 
+// Whether rows of two tables share an entry: `n` rows of `width` entries, `pitch` apart.
+struct Rows {
+  const int32_t* data;
+  int64_t pitch, n, width;
+};
+bool rows_meet(Rows a, Rows b) {
+  if (a.n < 1 || b.n < 1 || a.width < 1 || b.width < 1) return false;
+  for (Rows* r : {&a, &b}) {
+    if (r->pitch < 0) r->data += r->pitch * (r->n - 1), r->pitch = -r->pitch;
+    if (r->pitch == 0) r->n = 1;
+  }
+  if (b.n < a.n) {
+    const Rows c = a;
+    a = b, b = c;
+  }
+  // in bytes, from b's first row
+  const int64_t start = static_cast<int64_t>(reinterpret_cast<intptr_t>(a.data) - reinterpret_cast<intptr_t>(b.data));
+  const int64_t wide = 4 * a.width, other = 4 * b.width, step = 4 * b.pitch;
+  if (start >= step * (b.n - 1) + other || start + 4 * a.pitch * (a.n - 1) + wide <= 0) return false;
+  for (int64_t i = 0; i < a.n; ++i) {
+    // b's first row that ends behind the start of this one
+    const int64_t at = start + 4 * a.pitch * i, j = at < other ? 0 : (at - other) / step + 1;
+    if (j < b.n && j * step < at + wide) return true;
+  }
+  return false;
+}
+
 uint32_t grid_of(int64_t n) { return static_cast<uint32_t>(n < 1 ? 1 : n); }
 
 }  // namespace
@@ -497,6 +524,8 @@ ets_status ets_pages_fork(int32_t* refs, int64_t P, const int32_t* table, int64_
   if (ets_status st = take_buffers(buffers, count, P, &held); st != ETS_OK) return st;
   if (n == 0) return ETS_OK;
   if (held.pieces && n > INT32_MAX / held.pieces) return ETS_ERR_INVALID_ARG;
+  // rows are read while others are written
+  if (rows_meet({table, pt_b, B, M}, {out, out_b, n, out_M})) return ETS_ERR_INVALID_ARG;
   int32_t cu = 0;
   if (ets_status st = device_ready(&cu); st != ETS_OK) return st;
   p.lens = lens, p.page_size = page_size, p.by_page = fast_div(page_size);

@@ -185,8 +185,11 @@ ets_status ets_pages_free(int32_t* refs, int64_t P, int32_t* table, int64_t pt_b
  * shares the pages that lens[b] positions fill, which gain one in refs each.
  * A last page that they fill in part is copied, in every buffer, to a free one
  * (lowest first, in order of i); lacking[i] is 1 where there was none, else
- * 0.  The other entries are -1, and so are those whose parent's hold no page, and all where parents[i] is outside [0, B).
- * What out held before is not looked at; out must not overlap the table rows. */
+ * 0.  The other entries are -1, and so are those whose parent's hold no page,
+ * and all where parents[i] is outside [0, B).  A branch has its first out_M
+ * pages alone: what lies behind them is not shared, not copied, and lacking
+ * does not count it.  What out held before is not looked at; an out that shares
+ * an entry with the table's rows is refused (ETS_ERR_INVALID_ARG). */
 ets_status ets_pages_fork(int32_t* refs, int64_t P, const int32_t* table, int64_t pt_b, int32_t B, int32_t M,
                           const int32_t* lens, int32_t page_size, const int32_t* parents, int32_t n, int32_t* out,
                           int64_t out_b, int32_t out_M, int32_t* lacking, const ets_page_buffer* buffers, int32_t count,

@@ -4,7 +4,7 @@ import torch
 
 import exact_top_selection_amd as ets
 from tests import speculate_reference as spec
-from tests.test_gpu_speculate import filled, ints
+from tests.test_gpu_speculate import filled, ints, same_pages
 from tests.test_gpu_step import BF16, FP16, FP32, dev, gen
 
 pytestmark = pytest.mark.gpu
@@ -138,3 +138,65 @@ def test_attention_of_more_lists_than_a_launch_holds():
     assert torch.equal(out, want) and not lse.any()
     out, lse = ets.attend_paged(q, codes, scales.view(1, -1, 1), codes, scales.view(1, -1, 1), page, one, 1, 1)
     assert torch.equal(out, want) and not lse.any()
+
+
+# ---- branches written over rows of the table
+
+@pytest.mark.parametrize("form", ["rows behind the parents", "every second row", "in place", "columns"])
+def test_fork_into_the_table_itself(form):
+    """All rows of parents are read before any is written."""
+    g = gen(72)
+    B, M, page = 40, 9, 4
+    P = B * M * 2
+    wide = torch.full((B, 2 * M), -1, dtype=torch.int32)
+    wide[:, :M] = torch.randperm(P, generator=g)[:B * M].view(B, M).int()
+    refs = torch.zeros(P, dtype=torch.int32)
+    refs[wide[:, :M].flatten().long()] = 1
+    lens = torch.randint(0, M * page + 1, (B,), generator=g, dtype=torch.int32)
+    buffers = [torch.randint(0, 256, (P, 37), generator=g, dtype=torch.uint8)]
+    read, write = {"rows behind the parents": (slice(None), slice(B // 2, B)), "every second row": (slice(None), slice(1, B, 2)),
+                   "in place": (slice(None), slice(None)), "columns": (slice(None), slice(None))}[form]
+    column = M if form == "columns" else 0
+    n = len(range(*write.indices(B)))
+    parents = torch.randint(0, B // 2 if form == "rows behind the parents" else B, (n,), generator=g, dtype=torch.int32)
+    want = spec.fork(refs, wide[:, :M], lens, page, parents, M)
+    there, got, on = wide.to(dev()), refs.to(dev()), [t.to(dev()) for t in buffers]
+    rows = there[write, column:column + M]
+    out, lacking = ets.pages_fork(got, there[read, :M], lens.to(dev()), page, parents.to(dev()), on, out=rows)
+    expect = wide.clone()
+    expect[write, column:column + M] = torch.tensor(want[1], dtype=torch.int32)
+    assert out is rows and torch.equal(there.cpu(), expect) and got.tolist() == want[0] and lacking.tolist() == want[2]
+    same_pages(on, buffers, want[3], P)
+
+
+def test_fork_into_the_table_itself_in_a_graph():
+    """Replays, with eager work between, follow the eager calls."""
+    g = gen(73)
+    B, M, page, P = 6, 5, 4, 400
+
+    def state():
+        h = gen(74)
+        table = torch.randperm(P, generator=h)[:B * M].view(B, M).int()
+        refs = torch.zeros(P, dtype=torch.int32)
+        refs[table.flatten().long()] = 1
+        return refs.to(dev()), table.to(dev()), torch.randint(0, 256, (P, 37), generator=h, dtype=torch.uint8).to(dev())
+
+    lens, parents = torch.zeros(B, dtype=torch.int32, device=dev()), torch.zeros(B, dtype=torch.int32, device=dev())
+
+    def step(refs, table, pages):
+        return ets.pages_fork(refs, table, lens, page, parents, [pages], out=table)[1]
+
+    step(*state())  # warm
+    a, b = state(), state()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kept = step(*a)
+    for _ in range(5):
+        lens.copy_(torch.randint(0, M * page + 1, (B,), generator=g, dtype=torch.int32))
+        parents.copy_(torch.randint(0, B, (B,), generator=g, dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        lacking = step(*b)
+        assert torch.equal(kept, lacking) and all(torch.equal(x, y) for x, y in zip(a, b))
+        torch.cuda.synchronize()
