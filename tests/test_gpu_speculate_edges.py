@@ -4,8 +4,9 @@ import torch
 
 import exact_top_selection_amd as ets
 from tests import speculate_reference as spec
-from tests.test_gpu_speculate import filled, ints, same_pages
+from tests.test_gpu_speculate import filled, ints, pages, run_blocks, same_pages, tree
 from tests.test_gpu_step import BF16, FP16, FP32, dev, gen
+from tests.test_gpu_step_edges import close_where_numbers
 
 pytestmark = pytest.mark.gpu
 
@@ -200,3 +201,49 @@ def test_fork_into_the_table_itself_in_a_graph():
         lacking = step(*b)
         assert torch.equal(kept, lacking) and all(torch.equal(x, y) for x, y in zip(a, b))
         torch.cuda.synchronize()
+
+
+# ---- attention with eight waves a workgroup: 256 rows on a list and more, in several turns of the device
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("form,B,T,Hq,Hkv,D,Dv", [("tree", 32, 64, 64, 16, 128, 128), ("tree", 64, 63, 40, 8, 64, 32), ("tree", 35, 50, 96, 16, 32, 96),
+                                                  ("causal", 32, 130, 32, 16, 128, 96), ("causal", 70, 300, 8, 8, 64, 64)])
+@pytest.mark.parametrize("spoilt", [False, True])
+def test_eight_waves(form, B, T, Hq, Hkv, D, Dv, dtype, spoilt):
+    """Trees, triangles and padding; rows that are no numbers among the drafts, in the last rows and behind the length."""
+    G, L, page, block = Hq // Hkv, T + 90, 16, 8
+    assert T * G >= 256 and max(D, Dv) <= 128 and B * Hkv * ((T * G + 255) // 256) >= 2 * ets.device_limits()[0]
+    g = gen(75)
+    table, P = pages(B, -(-L // page), 1, g)
+    kc, ks = filled(P * page, Hkv, D, block, g)
+    vc, vs = filled(P * page, Hkv, Dv, block, g)
+    q = torch.randn(B, T, Hq, D, generator=g).to(dtype)
+    lens = torch.randint(T, L + 1, (B,), generator=g, dtype=torch.int32)
+    first = lens - T
+    first[1] += T // 3  # its last tokens are padding
+    lens[2], first[2] = T // 2, 0
+    mask = tree(B, T, g) if form == "tree" else None
+    some = {0, 1, 2, B // 2, B - 1}
+    if spoilt:
+        for b in some:
+            at = lambda p: spec.place(table[b], page, P, p)  # noqa: E731,B023
+            start, end = int(first[b]), int(lens[b])
+            vc[at(min(start + T // 2, end - 1)), :, 3], vc[at(end - 1), Hkv - 1, Dv - 1] = 0x7F, 0xFF
+            kc[at(max(start, end - 2)), 0, 0] = 0xFF
+            for p in range(end, min(-(-L // page) * page, end + 40)):  # never written
+                kc[at(p)], vc[at(p)] = 0x7F, 0xFF
+    out, lse = run_blocks(q, kc, ks, vc, vs, table, lens, page, L, first, mask)
+    tokens = sorted({0, 1, T // 4, T // 2 - 1, T // 2, T - 2, T - 1})
+    numbers = 0
+    for b in some:
+        for h in {0, Hkv - 1}:
+            lists = spec.seen(table[b:b + 1], page, P, lens[b:b + 1], L, T, first[b:b + 1], None if mask is None else mask[b:b + 1])
+            heads = slice(h * G, h * G + G)
+            want = spec.attend(q[b:b + 1, tokens, heads], kc[:, h:h + 1], ks[:, h:h + 1], vc[:, h:h + 1], vs[:, h:h + 1],
+                               [[lists[0][t] for t in tokens]])
+            close_where_numbers(out[b:b + 1, tokens, heads], want[0], want[2], dtype)
+            close_where_numbers(lse[b:b + 1, tokens, heads], want[1], want[3], FP32)
+            numbers += int(torch.isnan(want[0]).any())
+    assert (numbers > 0) == spoilt
+    again = run_blocks(q, kc, ks, vc, vs, table, lens, page, L, first, mask)
+    assert torch.equal(out.view(torch.uint8), again[0].view(torch.uint8)) and torch.equal(lse.view(torch.uint8), again[1].view(torch.uint8))
