@@ -386,9 +386,7 @@ void launch(const AttendBlocksParams& p, hipStream_t s) {
 template <class T>
 void launch_type(const AttendBlocksParams& p, const RowsShape& r, hipStream_t s) {
   switch (r.width) {
-    case 1:
-      if (r.waves == 8) return launch<T, 1, 2, 1, 8>(p, s);
-      return r.tiles == 1 ? launch<T, 1, 1, 2, 4>(p, s) : launch<T, 1, 2, 1, 4>(p, s);
+    case 1: return r.tiles == 1 ? launch<T, 1, 1, 2, 4>(p, s) : launch<T, 1, 2, 1, 4>(p, s);
     case 2:
       if (r.waves == 8) return launch<T, 2, 2, 1, 8>(p, s);
       return r.tiles == 1 ? launch<T, 2, 1, 2, 4>(p, s) : launch<T, 2, 2, 1, 4>(p, s);

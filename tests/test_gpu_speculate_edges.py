@@ -203,16 +203,21 @@ def test_fork_into_the_table_itself_in_a_graph():
         torch.cuda.synchronize()
 
 
-# ---- attention with eight waves a workgroup: 256 rows on a list and more, in several turns of the device
+# ---- attention with eight waves a workgroup: filled groups of 256 rows of 65 to 128 channels, room for long lists, several
+# turns of the device; and with four waves next to that
 
 @pytest.mark.parametrize("dtype", [BF16, FP16])
-@pytest.mark.parametrize("form,B,T,Hq,Hkv,D,Dv", [("tree", 32, 64, 64, 16, 128, 128), ("tree", 64, 63, 40, 8, 64, 32), ("tree", 35, 50, 96, 16, 32, 96),
-                                                  ("causal", 32, 130, 32, 16, 128, 96), ("causal", 70, 300, 8, 8, 64, 64)])
+@pytest.mark.parametrize("waves,form,B,T,Hq,Hkv,D,Dv,room", [
+    (8, "tree", 32, 64, 64, 16, 128, 128, 8192), (8, "tree", 35, 31, 128, 16, 32, 96, 8192), (8, "tree", 64, 64, 32, 8, 96, 64, 9000),
+    (8, "causal", 32, 200, 32, 16, 128, 96, 8200), (8, "causal", 70, 256, 8, 8, 96, 96, 8192),
+    (4, "tree", 64, 63, 40, 8, 64, 32, 8192), (4, "tree", 35, 50, 96, 16, 32, 96, 8192), (4, "tree", 32, 64, 64, 16, 128, 128, 154),
+    (4, "causal", 32, 130, 32, 16, 128, 96, 8192), (4, "causal", 70, 300, 8, 8, 64, 64, 390)])
 @pytest.mark.parametrize("spoilt", [False, True])
-def test_eight_waves(form, B, T, Hq, Hkv, D, Dv, dtype, spoilt):
+def test_eight_waves(waves, form, B, T, Hq, Hkv, D, Dv, room, dtype, spoilt):
     """Trees, triangles and padding; rows that are no numbers among the drafts, in the last rows and behind the length."""
     G, L, page, block = Hq // Hkv, T + 90, 16, 8
-    assert T * G >= 256 and max(D, Dv) <= 128 and B * Hkv * ((T * G + 255) // 256) >= 2 * ets.device_limits()[0]
+    assert (waves == 8) == (64 < max(D, Dv) <= 128 and 2 * -(-T * G // 256) == -(-T * G // 128) and room >= 8192
+                            and B * Hkv * -(-T * G // 256) >= 2 * ets.device_limits()[0])
     g = gen(75)
     table, P = pages(B, -(-L // page), 1, g)
     kc, ks = filled(P * page, Hkv, D, block, g)
@@ -222,6 +227,7 @@ def test_eight_waves(form, B, T, Hq, Hkv, D, Dv, dtype, spoilt):
     first = lens - T
     first[1] += T // 3  # its last tokens are padding
     lens[2], first[2] = T // 2, 0
+    table = torch.nn.functional.pad(table, (0, -(-room // page) - table.shape[1]), value=-1)
     mask = tree(B, T, g) if form == "tree" else None
     some = {0, 1, 2, B // 2, B - 1}
     if spoilt:
@@ -232,12 +238,12 @@ def test_eight_waves(form, B, T, Hq, Hkv, D, Dv, dtype, spoilt):
             kc[at(max(start, end - 2)), 0, 0] = 0xFF
             for p in range(end, min(-(-L // page) * page, end + 40)):  # never written
                 kc[at(p)], vc[at(p)] = 0x7F, 0xFF
-    out, lse = run_blocks(q, kc, ks, vc, vs, table, lens, page, L, first, mask)
+    out, lse = run_blocks(q, kc, ks, vc, vs, table, lens, page, room, first, mask)
     tokens = sorted({0, 1, T // 4, T // 2 - 1, T // 2, T - 2, T - 1})
     numbers = 0
     for b in some:
         for h in {0, Hkv - 1}:
-            lists = spec.seen(table[b:b + 1], page, P, lens[b:b + 1], L, T, first[b:b + 1], None if mask is None else mask[b:b + 1])
+            lists = spec.seen(table[b:b + 1], page, P, lens[b:b + 1], room, T, first[b:b + 1], None if mask is None else mask[b:b + 1])
             heads = slice(h * G, h * G + G)
             want = spec.attend(q[b:b + 1, tokens, heads], kc[:, h:h + 1], ks[:, h:h + 1], vc[:, h:h + 1], vs[:, h:h + 1],
                                [[lists[0][t] for t in tokens]])
@@ -245,5 +251,5 @@ def test_eight_waves(form, B, T, Hq, Hkv, D, Dv, dtype, spoilt):
             close_where_numbers(lse[b:b + 1, tokens, heads], want[1], want[3], FP32)
             numbers += int(torch.isnan(want[0]).any())
     assert (numbers > 0) == spoilt
-    again = run_blocks(q, kc, ks, vc, vs, table, lens, page, L, first, mask)
+    again = run_blocks(q, kc, ks, vc, vs, table, lens, page, room, first, mask)
     assert torch.equal(out.view(torch.uint8), again[0].view(torch.uint8)) and torch.equal(lse.view(torch.uint8), again[1].view(torch.uint8))
