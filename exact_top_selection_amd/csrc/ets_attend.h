@@ -42,7 +42,7 @@ struct AttendParams {
 struct AttendBlocksParams : AttendParams {
   const int32_t* first;  // where a sequence's tokens stand, or null
   FastDiv by_block;
-  int dealt;  // to the XCDs: 0, shares with all their heads; 1, lists; 2, workgroups
+  int dealt;  // many rows; to the XCDs: 0, shares with all their heads; 1, lists; 2, workgroups
 };
 
 // Where a workgroup stands: its list, its query rows, its share of the keys.
@@ -72,15 +72,16 @@ __device__ __forceinline__ uint32_t attend_deal(const AttendParams& p, AttendSpo
   s->group = static_cast<int>(in) - heads * p.row_groups;
   return bt;
 }
-template <class P>
+// MANY: of the kernel for many rows.  All row groups of a list read the same rows, so they follow each other on one XCD
+// where there are lists for all, and go to the XCDs in turn where not.
+template <bool MANY = false, class P>
 __device__ __forceinline__ AttendSpot attend_spot(const P& p) {
   const ets_attend_args& a = p.a;
   AttendSpot s;
   s.paged = a.slots == nullptr;
   uint32_t bt;
-  if constexpr (std::is_same_v<P, AttendBlocksParams>) {
+  if constexpr (MANY) {
     if (p.dealt == 1 || p.dealt == 2) {
-      // all row groups of a list read the same rows, so they follow each other on one XCD where there are lists for all
       const uint32_t i = p.dealt == 1 ? blockIdx.x >> 3 : blockIdx.x, turn = div_by(i, p.by_groups);
       const uint32_t list = p.dealt == 1 ? turn * 8 + (blockIdx.x & 7) : turn, share = div_by(list, p.by_heads);
       bt = div_by(share, p.by_splits);

@@ -89,10 +89,16 @@ ets_status make_plan(const ets_attend_blocks_args* a, BlocksPlan* plan) {
   const int64_t cap = plan->many ? (tiles + 3) / 4 : (tiles + kAttendWaves / p.heads - 1) / (kAttendWaves / p.heads);
   splits = splits > cap ? cap : splits;
   p.splits = static_cast<int>(splits < 1 ? 1 : splits);
-  // Heads of a slot lie side by side in memory, so they are read on one XCD where there are shares for all 8 (seven with
-  // one more than the eighth do no harm where each has many).
+  // With many rows XCDs are dealt whole lists where they get equally many, or at least 8 (one more does no harm then),
+  // else workgroups.  Workgroups' times over lists', 220 random batches: 1.01 for 8 to 63 lists that 8 divides (one
+  // prompt of 8192, 8 lists: 959 us against 857), 1.03 from 64 lists on; 0.94 for 1 to 63 others, down to 0.44.
+  // With one row group nothing is read twice, and heads of a slot, which lie side by side in memory, are read on one XCD
+  // where there are shares for all 8: 0.99 of lists' time for even numbers of heads (12 trees of 13, 4 heads of 96
+  // channels: 69 us against 70), 1.02 for others.  With more row groups that was 1.02 where 8 divided the shares or there
+  // were 64, to 1.14 (8 sequences of uneven length, 512 tokens each: 698 us against 620).
   const int64_t shares = static_cast<int64_t>(a->B) * p.splits, all = shares * a->Hkv;
-  p.dealt = !plan->many || shares % 8 == 0 || shares >= 64 ? 0 : all % 8 == 0 || all >= 64 ? 1 : 2;
+  const bool together = p.row_groups == 1 && a->Hkv % 2 == 0 && (shares % 8 == 0 || shares >= 64);
+  p.dealt = together ? 0 : all % 8 == 0 || all >= 64 ? 1 : 2;
   if (lists * (p.splits + 8) > INT32_MAX / 16) return ETS_ERR_INVALID_ARG;
   // one launch, of fewer than 2^32 lanes
   if ((plan->many ? attend_rows_groups(p) * 64 * waves_rows : attend_groups(p) * kAttendThreads) > UINT32_MAX) return ETS_ERR_INVALID_ARG;

@@ -56,7 +56,7 @@ __global__ __launch_bounds__(64 * WAVES, rows_per_unit(N, WAVES)) void attend_ro
   extern __shared__ __align__(16) char lds[];
   const ets_attend_args& a = p.a;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 15, g = lane >> 4;
-  const AttendSpot spot = attend_spot(p);
+  const AttendSpot spot = attend_spot<true>(p);
   if (!spot.live) return;
   const int b = spot.b, hk = spot.hk;
   const int k0 = spot.first * kAttendTile, k1 = min(spot.last * kAttendTile, spot.n);
