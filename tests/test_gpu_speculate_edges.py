@@ -4,8 +4,8 @@ import torch
 
 import exact_top_selection_amd as ets
 from tests import speculate_reference as spec
-from tests.test_gpu_speculate import filled, ints, pages, run_blocks, same_pages, tree
-from tests.test_gpu_step import BF16, FP16, FP32, dev, gen
+from tests.test_gpu_speculate import filled, ints, pages, run_blocks, same_codes, same_pages, tree
+from tests.test_gpu_step import BF16, FP16, FP32, close, dev, gen
 from tests.test_gpu_step_edges import close_where_numbers
 
 pytestmark = pytest.mark.gpu
@@ -253,3 +253,121 @@ def test_eight_waves(waves, form, B, T, Hq, Hkv, D, Dv, room, dtype, spoilt):
     assert (numbers > 0) == spoilt
     again = run_blocks(q, kc, ks, vc, vs, table, lens, page, room, first, mask)
     assert torch.equal(out.view(torch.uint8), again[0].view(torch.uint8)) and torch.equal(lse.view(torch.uint8), again[1].view(torch.uint8))
+
+
+# ---- numbers that the documentation allows and that no program above brings
+
+ENDS = [-0x80000000, -0x7FFFFFFF, -1, 0x7FFFFFFF, 0x7FFFFF00]
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("T,Hq,Hkv,D,Dv,form", [(3, 4, 2, 64, 64, "causal"), (9, 2, 2, 128, 96, "tree"), (40, 6, 2, 96, 128, "causal"), (64, 2, 1, 128, 128, "tree"),
+                                                (17, 12, 1, 256, 192, "tree"), (150, 2, 1, 64, 32, "causal"), (20, 5, 1, 160, 224, "causal")])
+def test_attend_blocks_of_any_first_length_and_mask(T, Hq, Hkv, D, Dv, form, dtype):
+    """Tokens that stand anywhere next to the length, bits of any kind, pages that are not there, a cache that is not whole pages."""
+    g = gen(76)
+    B, block, page, L = 24, 4, 12, 170
+    table, P = pages(B, -(-L // page), 3, g)
+    table[torch.rand(table.shape, generator=g) < 0.1] = -1
+    table[3, :], table[4, 2] = P, P - 1
+    S = P * page - block  # the last page is not whole: not there
+    kc, ks = filled(P * page, Hkv, D, block, g)
+    vc, vs = filled(P * page, Hkv, Dv, block, g)
+    kc, vc, ks, vs = kc[:S], vc[:S], ks[:S // block], vs[:S // block]
+    q = torch.randn(B, T, Hq, D, generator=g).to(dtype)
+    lens = torch.randint(-3, L + 30, (B,), generator=g, dtype=torch.int32)
+    first = (torch.rand(B, generator=g) * (L + T + 20) - T - 10).to(torch.int32)
+    first[:5], lens[5:10] = ints(*ENDS), ints(*ENDS)
+    first[10:12], lens[10:12] = 0, L
+    mask = None
+    if form == "tree":
+        mask = torch.randint(-(1 << 63), (1 << 63) - 1, (B, T), generator=g)
+        mask[::3] &= torch.randint(-(1 << 63), (1 << 63) - 1, (len(range(0, B, 3)), T), generator=g) & 0x1111111111111111
+        mask[11], mask[12, ::2] = 0, 0
+    out, lse = run_blocks(q, kc, ks, vc, vs, table, lens, page, L, first, mask)
+    lists = spec.seen(table, page, S // page, lens, L, T, first, mask)
+    want = spec.attend(q, kc, ks, vc, vs, lists)
+    close(out, want[0], want[2], dtype)
+    close(lse, want[1], want[3], FP32)
+    nothing = torch.tensor([[not bool((row >= 0).any()) for row in rows] for rows in lists])
+    assert nothing.any() and not nothing.all()
+    assert not out.cpu()[nothing].any() and bool((lse.cpu()[nothing] == -float("inf")).all())
+
+
+@pytest.mark.parametrize("block,page,D", [(4, 12, 64), (1, 3, 32), (20, 20, 256)])
+def test_writes_at_the_ends_of_a_table(block, page, D):
+    """Rows that stand across either end of the table, or beyond it; a cache that is not whole pages."""
+    g = gen(77)
+    B, T, H, M = 30, 25, 2, 4
+    table, P = pages(B, M, 1, g)
+    table[7, 3] = P - 1
+    codes, scales = filled(P * page, H, D, block, g)
+    S = (P - 1) * page + page // 2 // block * block
+    codes, scales = codes[:S], scales[:S // block]
+    first = torch.randint(M * page - T, M * page + 3, (B,), generator=g, dtype=torch.int32).clamp(min=0)
+    first[:5], first[5] = ints(*ENDS), 0
+    counts = torch.randint(-2, T + 3, (B,), generator=g, dtype=torch.int32)
+    counts[10:15] = ints(*ENDS)
+    x = torch.randn(B, T, H, D, generator=g).to(BF16)
+    want = spec.block_write(x, codes, scales, table, first, counts, page)
+    got = codes.to(dev()), scales.to(dev())
+    ets.block_write(x.to(dev()), *got, table.to(dev()), first.to(dev()), counts.to(dev()), page)
+    assert torch.equal(got[0].cpu(), want[0]) and torch.equal(got[1].cpu(), want[1])
+    path = torch.stack([torch.randperm(T, generator=g) for _ in range(B)]).to(torch.int32)
+    path[3, 2], path[9, 1], path[8, :3] = -0x80000000, 0x7FFFFFFF, ints(0, 1, 2)
+    codes, scales = want
+    want = spec.block_keep(codes, scales, table, first, path, counts, page)
+    ets.block_keep(*got, table.to(dev()), first.to(dev()), path.to(dev()), counts.to(dev()), page)
+    assert same_codes(got[0], want[0]) and torch.equal(got[1].cpu(), want[1])
+
+
+def test_pages_of_any_numbers():
+    g = gen(78)
+    P, B, M, page = 300, 12, 9, 5
+    held = [torch.randint(0, 256, (P, 21), generator=g, dtype=torch.uint8)]
+    for turn in range(4):
+        refs = torch.randint(-1, 2, (P,), generator=g, dtype=torch.int32)
+        refs[:3] = ints(-0x80000000, -5, 0)
+        table = torch.full((B, M), -1, dtype=torch.int32)
+        used = (refs > 0).nonzero()[:, 0].int()
+        some = torch.rand(B, M, generator=g) < 0.5
+        table[some] = used[torch.randperm(used.numel(), generator=g)[:int(some.sum())]]
+        table[1, 2], table[2, 0], table[3, 1] = 0x7FFFFFFF, -0x80000000, P
+        lens = torch.randint(-3, M * page + 9, (B,), generator=g, dtype=torch.int32)
+        lens[:5] = ints(*ENDS)
+        parents = torch.randint(-2, B + 2, (15,), generator=g, dtype=torch.int32)
+        parents[:2], parents[3:8] = ints(0x7FFFFFFF, -0x80000000), ints(0, 1, 2, 3, 4)
+        got, on = refs.to(dev()), [t.to(dev()) for t in held]
+        want = spec.fork(refs, table, lens, page, parents, M)
+        rows, lacking = ets.pages_fork(got, table.to(dev()), lens.to(dev()), page, parents.to(dev()), on)
+        assert got.tolist() == want[0] and rows.tolist() == want[1] and lacking.tolist() == want[2]
+        same_pages(on, held, want[3], P)
+        got, rows = refs.to(dev()), table.to(dev())
+        want = spec.extend(refs, table, lens, page)
+        lacking = ets.pages_extend(got, rows, lens.to(dev()), page)
+        assert got.tolist() == want[0] and rows.tolist() == want[1] and lacking.tolist() == want[2]
+        got, rows = refs.to(dev()), table.to(dev())
+        want = spec.release(refs, table, lens, page)
+        ets.pages_free(got, rows, lens.to(dev()), page)
+        assert got.tolist() == want[0] and rows.tolist() == want[1]
+    # branches of no table at all
+    rows, lacking = ets.pages_fork(got, rows[:0], lens[:0].to(dev()), page, parents.to(dev()))
+    assert rows.shape == (15, M) and bool((rows == -1).all()) and not lacking.any()
+
+
+def test_verification_of_any_masks_and_lengths():
+    g = gen(79)
+    B, T, V = 50, 64, 40
+    probs = torch.softmax(torch.randn(B, T, V, generator=g), -1)
+    mask = torch.randint(-(1 << 63), (1 << 63) - 1, (B, T), generator=g)
+    mask[::2] = tree(len(range(0, B, 2)), T, g)
+    tokens = torch.randint(-2, V + 2, (B, T), generator=g, dtype=torch.int32)
+    tokens[0, 1:6], tokens[1, :] = ints(*ENDS), 7
+    lens = torch.randint(-2, T + 5, (B,), generator=g, dtype=torch.int32)
+    lens[5:10] = ints(*ENDS)
+    uniform = torch.rand(B, T, generator=g) * 0.2
+    for m in (mask, None):
+        want = spec.verify(probs, tokens, uniform, None, m, lens)
+        got = ets.verify_drafts(probs.to(dev()), tokens.to(dev()), uniform.to(dev()), tree_mask=None if m is None else m.to(dev()), lens=lens.to(dev()))
+        for a, b in zip(got, want):
+            assert torch.equal(a.cpu(), b)
