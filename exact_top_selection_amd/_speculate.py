@@ -19,8 +19,8 @@ from typing import Optional, Sequence, Tuple
 
 import torch
 
-from . import _check, _load, _on, _require, _rows, _same_device, _vec
-from ._decode import _DTYPES, _INT32, CACHE_BLOCK, MAX_LENGTH, MAX_TREE, _floats, _no_grad, _overlaps, _run, _vector
+from . import _check, _load, _on, _require, _rows, _same_device
+from ._decode import _INT32, CACHE_BLOCK, MAX_LENGTH, MAX_TREE, _floats, _no_grad, _overlaps, _run, _vector
 
 MAX_BLOCK_DIM, MAX_BUFFERS, MAX_PAGES = 256, 64, 1 << 26
 

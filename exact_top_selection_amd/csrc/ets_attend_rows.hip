@@ -35,13 +35,19 @@ constexpr int lds_bytes(int n, int waves) { return 2 * step_bytes(n) + 2 * 64 * 
 // Slots and scales come through LDS too, found by a lane each: every thread
 // finding those of its own piece cost 60 vector instructions a step.
 //
-// Measured: 309 us for pieces of 1000 tokens of two prompts of up to 8192, 32
-// heads on 8 of 128 channels, bf16 (690 TFLOP/s of the formula's, half as many
-// again with the probabilities' second part; 740 on four full prompts).  64 us
-// and 7 of join for 12 trees of 13 tokens behind up to 10007, 32 heads on 4 of 96,
-// fp16.  The bound is the issue of a SIMD: vector instructions take half of its
-// cycles and matrix instructions two fifths, and little of one runs under the
-// other.  Two waves a SIMD leave no registers for a third.
+// Measured, a call in a row of them: 342 us for pieces of 1000 tokens of two
+// prompts of 8192 and 7329, 280 of 8192 and 4430, 32 heads on 8 of 128 channels,
+// bf16 (690 TFLOP/s of the formula's, half as many again with the probabilities'
+// second part; 750 on four full prompts).  65 us and 7 of join for 12 trees of 13
+// tokens behind up to 10007 (92945 positions in all), 32 heads on 4 of 96, fp16.
+// The bound is the issue of a SIMD: vector instructions take half of its cycles
+// and matrix instructions two fifths, and little of one runs under the other.
+// Two waves a SIMD leave no registers for a third.  The vector instructions count
+// lane moves: no vector register spills, but 62 to 128 scalar ones do, into lanes
+// (110 in the bf16 instance of 128 channels).  There the block that finds the
+// slots of 4 steps holds 47 reads and 18 writes of lanes beside 248 other vector
+// instructions, the one that brings and decodes a step 49 and 1 beside 93, and
+// those of the products 2 between them.
 //
 // KB: 32-key parts of a step that a wave has in its registers at once.
 template <class T, int N, int NT, int KB, int WAVES>
@@ -53,6 +59,7 @@ __global__ __launch_bounds__(64 * WAVES, rows_per_unit(N, WAVES)) void attend_ro
   constexpr int kTurn = kThreads;           // keys whose slots and scales are found at a time, one a lane
   constexpr int kPieces = 4 * N;            // 16 channels each, of a key or a value
   constexpr int kItems = 2 * kPieces / WAVES;  // pieces of a step that a thread brings
+  static_assert(kItems % 2 == 0, "as many of keys as of values");
   extern __shared__ __align__(16) char lds[];
   const ets_attend_args& a = p.a;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 15, g = lane >> 4;
@@ -116,7 +123,7 @@ __global__ __launch_bounds__(64 * WAVES, rows_per_unit(N, WAVES)) void attend_ro
   int key[kItems], piece[kItems];
 #pragma unroll
   for (int j = 0; j < kItems; ++j) {
-    is_value[j] = kItems % 2 == 0 ? j >= kItems / 2 : wave + WAVES * j >= kPieces;
+    is_value[j] = j >= kItems / 2;
     const int i = static_cast<int>(threadIdx.x) + j * kThreads - (is_value[j] ? kKeys * kPieces : 0);
     key[j] = i / kPieces, piece[j] = i % kPieces;
     row[j] = reinterpret_cast<uint64_t>(is_value[j] ? a.v_codes + hk * a.v_h : a.k_codes + hk * a.k_h) + 16 * piece[j];
