@@ -56,9 +56,12 @@ constexpr int attend_per_unit(int np, int mt) { return mt == 1 && np <= 2 ? 3 : 
 // scale bytes for its 16 keys (row g: the keys' lower and upper half, the
 // values'), and gets the others' from their lanes.  fp16 queries meet the codes
 // themselves, and scores are multiplied by the key's scale.  All keys are
-// positions of the sequence; from `edge` on rows differ in what they see.  163
-// us and 5 us of join for 64 sequences of up to 8192, 32 heads on 8 of 128, bf16
-// (816 MB, 5.0 TB/s); 10 us and 4 us for one sequence of 2047.
+// positions of the sequence; from `edge` on rows differ in what they see.  166
+// us and 5 us of join for 64 sequences of 397659 positions in all, 32 heads on 8
+// of 128, bf16 (814 MB, 4.9 TB/s); 10 us and 4 us for one sequence of 2047.
+// Scalar registers spill into lanes (40 to 122 of them); the instances of less
+// than 64 channels and one row tile keep 68 bytes a lane in scratch, and those of
+// fp16, more than 192 channels and two row tiles spill 6 vector registers.
 template <class T, int NP, int NV, int MT, bool FULL, bool BLOCKS = false>
 __global__ __launch_bounds__(kAttendThreads, attend_per_unit(NP, MT)) void attend_kernel(std::conditional_t<BLOCKS, AttendBlocksParams, AttendParams> p) {
   typedef Mat<T> M;

@@ -117,7 +117,7 @@ __device__ __forceinline__ void raise_rows(const BlockParams& p, uint8_t* codes,
 //
 // Measured: 20 us for pieces of 8192 tokens of four prompts, 8 x 128, fp16,
 // blocks of 32 (75 MB, 3.7 TB/s; 29 us with 256 lanes and the page first), in one
-// turn of waves, each with three loads in turn; 4.8 us for 64 rows (the loads).
+// turn of waves, each with three loads in turn; 4.6 us for 64 rows (the loads).
 template <class T, int THREADS>
 __global__ __launch_bounds__(THREADS) void block_write_kernel(BlockParams p) {
   typedef T V8 __attribute__((ext_vector_type(8)));

@@ -89,7 +89,10 @@ ets_status ets_block_keep(int32_t B, int32_t T, int32_t H, int32_t D, uint8_t* c
  *     first[b], and first[b] + j for j <= t, or, with tree_mask, for j < T with
  *     bit j of tree_mask[b][t] set (T <= ETS_MAX_TREE then).
  * A row that sees nothing has out = 0 and lse = -inf.  Numerics are those of
- * ets_attend; products of keys are exact for bf16 and fp16 queries.  One launch
+ * ets_attend; products of keys are exact for bf16 and fp16 queries.  The
+ * probabilities' 16 bits show where an exact result lies next to a border of the
+ * output type: one bf16 result in a thousand is the other neighbour of what 32-bit
+ * probabilities give, as near to the exact one over all.  One launch
  * takes a call, a workgroup of 256 or 512 lanes 16 to 256 rows of a list: sizes
  * that need 2^32 lanes or more (16 million workgroups) are refused.
  */
