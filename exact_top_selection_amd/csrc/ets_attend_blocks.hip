@@ -57,17 +57,18 @@ ets_status make_plan(const ets_attend_blocks_args* a, BlocksPlan* plan) {
   int fits = 1, waves_rows = 1;
   if (plan->many) {
     // Two workgroups of four waves share a compute unit, and one works while the other waits at its barrier.  Eight waves
-    // decode each key for twice the rows, which pays for 65 to 128 channels where a group's second half is not mostly
-    // empty, lists are long, and there are workgroups for several turns of the device.  Their times over those of four
-    // waves, 220 random batches and some that are not:
-    //   within the rule      0.99 in the mean of 32, 0.94 to 1.11 (8 full sequences of 8192, 1024 tokens each: 1363 us
+    // decode each key for twice the rows, which pays for 65 to 128 channels and 256 rows and more where no group's second
+    // half is empty, lists are long, and there are workgroups for several turns of the device.  Their times over those of
+    // four waves, 300 random batches and some that are not:
+    //   within the rule      0.99 in the mean of 72, 0.92 to 1.11 (8 full sequences of 8192, 1024 tokens each: 1363 us
     //                        against 1438; 4: 687 against 736; 5 of uneven length: 740 against 741)
+    //   129 to 255 rows      1.01, 0.92 to 1.12
     //   lists under 8192     1.04, to 1.15 (16 of 1000, all tokens: 323 us against 300)
-    //   emptier halves       1.13, to 1.33 (64 x 300 rows over 4096: 768 us against 595)
+    //   empty second halves  1.13, to 1.33 (64 x 300 rows over 4096: 768 us against 595)
     //   fewer workgroups     1.01, 0.91 to 1.23
     //   64 channels          1.20, 1.08 to 1.30
     const int64_t wide = (p.rows + 255) / 256, narrow = (p.rows + 127) / 128;
-    const bool eight = plan->width == 2 && 2 * wide == narrow && a->L >= kLongList && p.units * wide >= 2 * cu;
+    const bool eight = plan->width == 2 && p.rows >= 256 && 2 * wide == narrow && a->L >= kLongList && p.units * wide >= 2 * cu;
     plan->shape = {plan->width, eight ? 8 : 4, p.rows > 64 || plan->width > 2 ? 2 : 1};
     plan->mt = plan->shape.tiles;
     waves_rows = plan->shape.waves;
